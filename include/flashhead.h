@@ -418,6 +418,178 @@ fh_status fh_cluster(const void* E, fh_dtype dtype, int64_t v, int64_t d, int64_
                      const double* u, float* out_C, int32_t* out_c2t, int32_t* out_init,
                      int32_t* out_assign, fh_cluster_times* out_times, void* stream);
 
+/*
+ * Around the dense head: the final norm that makes its input, a dense head
+ * whose operands are both int8 (W8A8), and the rules a server applies to
+ * logits before a token is chosen.  These calls need no fh_engine.  They run
+ * on the current device (fh_w8a8_*: the handle's device) and keep no state
+ * between calls: scratch memory is the caller's (`workspace`, of the size
+ * that the matching *_workspace call returns, 16-byte aligned, read and
+ * written only by the call it is given to), so calls on different streams or
+ * captured graphs overlap freely if their workspaces and outputs differ.
+ * Row strides (ld_*) are in elements.
+ */
+
+/*
+ * fh_rmsnorm — root-mean-square norm of B rows with the residual's addition,
+ * and an int8 output with a scale per row.  Per row, in float32:
+ *   s = x + residual;  y = s / sqrt(mean(s^2) + eps) * (weight_offset + weight)
+ *   out = y rounded to dtype;  out_residual = s rounded to dtype
+ *   out_scale = max |y| / 127;  out_q = rint(y / out_scale) (ties to even,
+ *   within [-127, 127]; 0 where out_scale is 0)
+ * The norm and the codes are taken from the unrounded s and y.  A row that
+ * holds an infinity or NaN, or whose sum of squares exceeds float32, has an
+ * out_scale or out that says so (NaN, or 0 from the infinite norm) and codes
+ * that mean nothing.
+ *   x             device [B x d] of dtype, row stride ld_x >= d.
+ *   residual      the same, row stride ld_residual; NULL: s = x.
+ *   weight        device [d] of dtype; NULL: the factor is 1.
+ *   weight_offset 0, or 1 for norms stored as (1 + w); unused without weight.
+ *   eps           >= 0.
+ *   out, out_residual  device [B x d] of dtype, out_q device [B x d] int8, with
+ *                 their row strides, out_scale device [B] float.  Any of out,
+ *                 out_residual and the pair (out_q, out_scale) may be NULL,
+ *                 not all.  out or out_residual may be x or residual itself
+ *                 (same address and stride); no other overlap.
+ * 1 <= B < 2^31, 1 <= d < 2^31.  Any alignment of the elements' own size;
+ * rows aligned to 16 bytes are read and written 16 bytes at a time.
+ */
+fh_status fh_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
+                     const void* weight, fh_dtype dtype, int64_t B, int64_t d, float eps,
+                     float weight_offset, void* out, int64_t ld_out, void* out_residual,
+                     int64_t ld_out_residual, int8_t* out_q, int64_t ld_q, float* out_scale,
+                     void* stream);
+
+/* An int8 weight matrix [n x k] with a float scale per row (output channel). */
+typedef struct fh_w8a8 fh_w8a8; /* opaque */
+
+/*
+ * fh_w8a8_create — quantise W, device [n x k] of dtype, dense: per row
+ * scale = max |W| / 127 (float32 division), code = rint(W / scale) (ties to
+ * even, within [-127, 127]; 0 where scale is 0).  A row that holds an infinity
+ * or NaN gives FH_EINVAL.
+ * fh_w8a8_create_codes — take codes [n x k] int8 (-128 included) and scales
+ * [n] float as they are, both device and dense.
+ * Both copy into the handle's own layout (n k bytes, n rounded up to 16 and k
+ * to 64, plus 4 n), wait for `stream`, and keep nothing of their arguments.
+ * 1 <= n <= 2^30, 1 <= k < 131072 (the int32 sums of the product are exact).
+ */
+fh_status fh_w8a8_create(const void* W, fh_dtype dtype, int64_t n, int64_t k, void* stream,
+                         fh_w8a8** out);
+fh_status fh_w8a8_create_codes(const int8_t* codes, const float* scales, int64_t n, int64_t k,
+                               void* stream, fh_w8a8** out);
+
+/* fh_w8a8_destroy — release the handle (NULL is a no-op), after waiting for
+ * the device to finish work that may still read it. */
+void fh_w8a8_destroy(fh_w8a8* w);
+
+/* fh_w8a8_get — copy the codes [n x k] and scales [n] out (device). */
+fh_status fh_w8a8_get(const fh_w8a8* w, int8_t* codes, float* scales, void* stream);
+
+/*
+ * fh_w8a8_workspace — bytes of workspace that a fh_w8a8_matmul (forward = 0)
+ * or fh_w8a8_forward (forward = 1) call with these q, ld_q and B needs, or a
+ * negative fh_status.  0 for a product whose rows are aligned to 16 bytes.
+ */
+int64_t fh_w8a8_workspace(const fh_w8a8* w, const int8_t* q, int64_t ld_q, int64_t B, int forward);
+
+/*
+ * fh_w8a8_matmul — out[b, j] = (sum_i q[b, i] code[j, i]) (q_scale[b] scale[j]),
+ * the sum exact in int32, the two products rounded to float32, then to bf16
+ * for out_dtype FH_BF16.
+ *   q        device [B x k] int8, row stride ld_q >= k.
+ *   q_scale  device [B] float.
+ *   out      device [B x n] of out_dtype, row stride ld_out >= n.
+ *   workspace, workspace_bytes  see fh_w8a8_workspace (NULL, 0 if that is 0).
+ * 1 <= B <= 65535.  q and out may have any alignment of their elements' size.
+ */
+fh_status fh_w8a8_matmul(const fh_w8a8* w, const int8_t* q, int64_t ld_q, const float* q_scale,
+                         int64_t B, void* out, int64_t ld_out, fh_dtype out_dtype, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/*
+ * fh_w8a8_forward — the dense head on that product: fh_dense_forward's
+ * choice over the n logits of each row (argmax or one draw from softmax(z / T)
+ * with the same Philox stream, LSE over all n).
+ *   mode, temperature, seed   as for fh_dense_forward.
+ *   out_token  [B] int32: the token, -1 where no logit of the row is above
+ *              -inf (NaN is never chosen).
+ *   out_token_logit, out_lse  [B] float or NULL; out_logits [B x n] float,
+ *              row stride ld_logits, or NULL.
+ */
+fh_status fh_w8a8_forward(const fh_w8a8* w, const int8_t* q, int64_t ld_q, const float* q_scale,
+                          int64_t B, int mode, float temperature, uint64_t seed,
+                          int32_t* out_token, float* out_token_logit, float* out_lse,
+                          float* out_logits, int64_t ld_logits, void* workspace,
+                          int64_t workspace_bytes, void* stream);
+
+/*
+ * fh_logit_rules — what a server lays on the logits of each row before it
+ * chooses a token.  All pointers are device memory; a NULL one leaves its rule
+ * out.  Token ids outside [0, v) in history and bias_ids are skipped.
+ */
+typedef struct {
+  const int32_t* history;     /* [B x history_len] token ids, row stride ld_history */
+  int64_t ld_history;
+  int64_t history_len;
+  const int32_t* n_prompt;    /* [B] ids at the row's start that are its prompt; NULL: 0 */
+  const int32_t* n_history;   /* [B] ids of the row that count, clamped to
+                                 [0, history_len]; NULL: history_len */
+  const float* repetition;    /* [B] > 0: ids in prompt or output, z > 0 ? z / r : z r */
+  const float* frequency;     /* [B]: z -= f times its count in the output */
+  const float* presence;      /* [B]: z -= p if it is in the output */
+  const int32_t* bias_ids;    /* [B x bias_len] ids, row stride ld_bias */
+  const float* bias;          /* [B x bias_len], the same stride: z += each listed
+                                 bias; an id listed several times takes their sum,
+                                 added up in the list's order */
+  int64_t ld_bias;
+  int64_t bias_len;
+  const int32_t* n_bias;      /* [B] entries that count, clamped; NULL: bias_len */
+  const uint32_t* mask;       /* [mask_rows x ceil(v / 32)] words, row stride ld_mask:
+                                 token t is allowed where bit t % 32 of word t / 32 is set */
+  int64_t ld_mask;
+  int64_t mask_rows;
+  const int32_t* mask_row;    /* [B] the mask row of each row, outside [0, mask_rows):
+                                 all allowed; NULL: row b takes mask row b */
+} fh_logit_rules;
+
+/*
+ * fh_logits_workspace — bytes of workspace of a fh_logits_apply call over
+ * [B x n] logits that asks for tokens or LSEs (0 is enough for one that does
+ * not), or FH_EINVAL.
+ */
+int64_t fh_logits_workspace(int64_t B, int64_t n);
+
+/*
+ * fh_logits_apply — the rules, then the choice of the token.  Per row b and
+ * token t with logit z, in float32 and in this order: the repetition, the
+ * frequency and the presence penalty, the bias, and -inf where the mask does
+ * not allow t (whatever z was, NaN too).  Then fh_dense_forward's choice over
+ * the row: argmax or a draw from softmax(z / T), the same Philox stream, LSE.
+ *   logits   device [B x n] float, row stride ld_logits: of all tokens (ids
+ *            NULL, n = v), e.g. fh_dense_forward's or fh_w8a8_matmul's, or of
+ *            the tokens in ids, e.g. fh_forward's out_logits and out_ids.
+ *   ids      device [B x n] int32, row stride ld_ids, or NULL.  An id outside
+ *            [0, v) is no token: its logit becomes -inf.  Every place of an id
+ *            listed several times gets the same rules.
+ *   rules    host, the struct of device pointers; NULL: no rules.
+ *   mode     FH_TOKEN_ARGMAX or FH_TOKEN_SAMPLE; temperature > 0 to sample.
+ *   out_logits  device [B x n] float, row stride ld_out, or NULL; may be
+ *            logits itself (same address and stride).
+ *   out_token   [B] int32 or NULL: the token; ties go to the smaller id; -1
+ *            where no logit is above -inf (NaN is never chosen).
+ *   out_token_logit, out_lse  [B] float or NULL: its logit after the rules
+ *            (-inf for token -1); log sum exp(z / T') over the row (-inf where
+ *            nothing is left, NaN where an allowed logit is NaN).
+ * 1 <= B <= 65535, 1 <= n, v <= 2^30.  At least one output.
+ */
+fh_status fh_logits_apply(const float* logits, int64_t ld_logits, const int32_t* ids,
+                          int64_t ld_ids, int64_t B, int64_t n, int64_t v,
+                          const fh_logit_rules* rules, int mode, float temperature, uint64_t seed,
+                          float* out_logits, int64_t ld_out, int32_t* out_token,
+                          float* out_token_logit, float* out_lse, void* workspace,
+                          int64_t workspace_bytes, void* stream);
+
 /* Thread-local description of the last error on this thread ("" if none). */
 const char* fh_last_error(void);
 

@@ -17,4 +17,9 @@ def __getattr__(name):
                 "fh_last_error", "fh_version"):
         from . import flashhead
         return getattr(flashhead, name)
+    if name in ("LogitRules", "W8A8Head", "rmsnorm", "logits_apply", "fh_rmsnorm", "fh_w8a8_create",
+                "fh_w8a8_create_codes", "fh_w8a8_destroy", "fh_w8a8_get", "fh_w8a8_workspace",
+                "fh_w8a8_matmul", "fh_w8a8_forward", "fh_logits_workspace", "fh_logits_apply"):
+        from . import serve
+        return getattr(serve, name)
     raise AttributeError(name)

@@ -25,7 +25,9 @@ EXPORTS = (
     "fh_dense_forward",
     "fh_get_int4", "fh_get_int8", "fh_spec_verify", "fh_profile_begin", "fh_profile_end",
     "fh_set_path", "fh_sync_status",
-    "fh_balanced_assign", "fh_cluster", "fh_last_error", "fh_version",
+    "fh_balanced_assign", "fh_cluster", "fh_rmsnorm", "fh_w8a8_create", "fh_w8a8_create_codes",
+    "fh_w8a8_destroy", "fh_w8a8_get", "fh_w8a8_workspace", "fh_w8a8_matmul", "fh_w8a8_forward",
+    "fh_logits_workspace", "fh_logits_apply", "fh_last_error", "fh_version",
 )
 
 
@@ -38,6 +40,18 @@ class FhClusterTimes(ctypes.Structure):
     _fields_ = [("init_ms", ctypes.c_float), ("sims_ms", ctypes.c_float),
                 ("total_ms", ctypes.c_float), ("pp_step_us", ctypes.c_float),
                 ("rounds", ctypes.c_int)]
+
+
+class FhLogitRules(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("ld_history", ctypes.c_int64),
+                ("history_len", ctypes.c_int64), ("n_prompt", ctypes.c_void_p),
+                ("n_history", ctypes.c_void_p), ("repetition", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("bias_ids", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("ld_bias", ctypes.c_int64), ("bias_len", ctypes.c_int64),
+                ("n_bias", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+                ("ld_mask", ctypes.c_int64), ("mask_rows", ctypes.c_int64),
+                ("mask_row", ctypes.c_void_p)]
 
 
 class FlashHeadError(RuntimeError):
@@ -75,6 +89,19 @@ _SIGS = {
     "fh_balanced_assign": ([_p, _i64, _i64, _p, ctypes.POINTER(_int), _p], _int),
     "fh_cluster": ([_p, _int, _i64, _i64, _i64, _int, ctypes.POINTER(ctypes.c_double), _p, _p, _p,
                     _p, ctypes.POINTER(FhClusterTimes), _p], _int),
+    "fh_rmsnorm": ([_p, _i64, _p, _i64, _p, _int, _i64, _i64, _f, _f, _p, _i64, _p, _i64, _p, _i64,
+                    _p, _p], _int),
+    "fh_w8a8_create": ([_p, _int, _i64, _i64, _p, ctypes.POINTER(_p)], _int),
+    "fh_w8a8_create_codes": ([_p, _p, _i64, _i64, _p, ctypes.POINTER(_p)], _int),
+    "fh_w8a8_destroy": ([_p], None),
+    "fh_w8a8_get": ([_p, _p, _p, _p], _int),
+    "fh_w8a8_workspace": ([_p, _p, _i64, _i64, _int], _i64),
+    "fh_w8a8_matmul": ([_p, _p, _i64, _p, _i64, _p, _i64, _int, _p, _i64, _p], _int),
+    "fh_w8a8_forward": ([_p, _p, _i64, _p, _i64, _int, _f, _u64, _p, _p, _p, _p, _i64, _p, _i64,
+                         _p], _int),
+    "fh_logits_workspace": ([_i64, _i64], _i64),
+    "fh_logits_apply": ([_p, _i64, _p, _i64, _i64, _i64, _i64, ctypes.POINTER(FhLogitRules), _int,
+                         _f, _u64, _p, _i64, _p, _p, _p, _p, _i64, _p], _int),
     "fh_last_error": ([], ctypes.c_char_p),
     "fh_version": ([], ctypes.c_char_p),
 }

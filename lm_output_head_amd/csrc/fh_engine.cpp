@@ -21,10 +21,11 @@
 #include <string>
 #include <vector>
 
+#include "fh_host.hpp"
 #include "fh_internal.hpp"
 #include "flashhead.h"
 
-namespace {
+namespace fh {
 
 thread_local std::string g_err;
 
@@ -38,7 +39,15 @@ fh_status hip_fail(hipError_t e, const char* what) {
   return e == hipErrorOutOfMemory ? FH_ENOMEM : FH_EHIP;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace fh
+
+namespace {
+
+using fh::DeviceGuard;
+using fh::aligned16;
+using fh::fail;
+using fh::g_err;
+using fh::hip_fail;
 
 constexpr int64_t kMaxC = 16384;
 
@@ -123,19 +132,6 @@ hipError_t timed(fh_engine* e, hipStream_t st, const char* name, F&& launch) {
   }
   return hipSuccess;
 }
-
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) != hipSuccess) { ok = false; return; }
-    if (prev != dev && hipSetDevice(dev) != hipSuccess) ok = false;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
-  }
-};
 
 void free_engine(fh_engine* e) {
   if (!e) return;

@@ -356,6 +356,15 @@ class FlashHead:
         fh_probs_fp8(out["logits"], out["lse"], temperature, res["probs"], res["scale_exp"], stream)
         return res
 
+    def logits_apply(self, out: dict, rules, mode: int = 0, temperature: float = 1.0, seed: int = 0,
+                     stream=None) -> dict:
+        """Rules (LogitRules) on a forward's retrieved candidates (its "logits"
+        and "ids") or a dense call's "logits", and the choice of the token
+        among what they leave: "logits", "token", "token_logit", "lse"."""
+        from .serve import logits_apply
+        return logits_apply(out["logits"], rules, ids=out.get("ids"), v=self.v, mode=mode,
+                            temperature=temperature, seed=seed, stream=stream)
+
     def score(self, h: torch.Tensor, stream=None) -> torch.Tensor:
         out = self._alloc((h.shape[0], self.c), torch.float32)
         fh_score(self.eng, h, out, stream)

@@ -1,0 +1,460 @@
+"""Torch binding of the operators around the dense head: the final norm with
+the residual's addition and an int8 output (``fh_rmsnorm``), the int8 product
+and the dense head on it (``fh_w8a8_*``), the rules on logits and the choice of
+the token (``fh_logits_apply``).
+
+Functions named like the C entry points marshal arguments: they check types,
+shapes and placement, pass raw pointers and the HIP stream, and raise on a
+non-OK status.  ``rmsnorm``, ``W8A8Head``, ``LogitRules`` and ``logits_apply``
+allocate outputs and workspaces on top of them.  Matrices may have any row
+stride; their rows are dense.  All tensors of a call are on one GPU, which need
+not be the current one; work goes to its current stream unless ``stream`` is
+given, and what the call allocates belongs to that stream.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import sys
+
+import torch
+
+from . import _abi
+from ._abi import FH_BF16, FH_F32, check
+
+_DTYPES = {torch.float32: FH_F32, torch.bfloat16: FH_BF16}
+
+
+def _shaped(t, dtype, shape, name):
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _rows(t, dtype, shape, name):
+    """Row stride of a matrix [B x w] whose rows are dense."""
+    _shaped(t, dtype, shape, name)
+    ld, inner = t.stride()
+    if inner != 1 and shape[1] != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if shape[0] == 1:
+        return max(ld, shape[1])  # one row: its stride says nothing
+    if ld < shape[1]:
+        raise ValueError(f"{name}: rows must not overlap (stride {ld})")
+    return ld
+
+
+def _vector(t, dtype, n, name):
+    _shaped(t, dtype, (n,), name)
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _device(*tensors):
+    """The one GPU that every tensor is on."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and (t.device != dev or not t.is_cuda):
+            raise ValueError("tensors of a libflashhead call must be on one GPU")
+    return dev
+
+
+_SAME = contextlib.nullcontext()
+
+
+def _on(dev, stream):
+    """Make `dev` current for a call, and `stream`, so that outputs allocated
+    in the call belong to the stream that writes them."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError("stream is on another device than the tensors")
+        return torch.cuda.stream(stream)
+    return _SAME if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# ------------------------------------------------------------------ the norm
+
+def fh_rmsnorm(x, residual, weight, eps, weight_offset, out=None, out_residual=None, out_q=None,
+               out_scale=None, stream=None) -> None:
+    """out = rmsnorm(x + residual) * (weight_offset + weight); out_residual =
+    x + residual; (out_q, out_scale) = the norm in int8 with a scale per row."""
+    if x.dim() != 2 or x.dtype not in _DTYPES:
+        raise ValueError(f"x must be [B x d] float32 or bfloat16, got {x.dtype} {tuple(x.shape)}")
+    if (out_q is None) != (out_scale is None):
+        raise ValueError("out_q and out_scale go together")
+    shape, dt = x.shape, x.dtype
+    B, d = shape
+    ld_x = _rows(x, dt, shape, "x")
+    ld_r = ld_o = ld_s = ld_q = 0
+    if residual is not None:
+        ld_r = _rows(residual, dt, shape, "residual")
+    if weight is not None:
+        _vector(weight, dt, d, "weight")
+    if out is not None:
+        ld_o = _rows(out, dt, shape, "out")
+    if out_residual is not None:
+        ld_s = _rows(out_residual, dt, shape, "out_residual")
+    if out_q is not None:
+        ld_q = _rows(out_q, torch.int8, shape, "out_q")
+        _vector(out_scale, torch.float32, B, "out_scale")
+    dev = _device(x, residual, weight, out, out_residual, out_q, out_scale)
+    with _on(dev, stream):
+        check(_abi.load().fh_rmsnorm(x.data_ptr(), ld_x, _ptr(residual), ld_r, _ptr(weight), _DTYPES[dt], B, d, eps,
+                                     weight_offset, _ptr(out), ld_o, _ptr(out_residual), ld_s, _ptr(out_q), ld_q,
+                                     _ptr(out_scale), _stream(dev)))
+
+
+def rmsnorm(x, weight=None, *, residual=None, eps=1e-6, weight_offset=0.0, want_out=True, want_q=False,
+            stream=None) -> dict:
+    """The final norm of hidden states x [B x d] (any row stride, so the last
+    positions of [B x T x d] need no copy).  Returns "out" (the head's h) with
+    want_out, "residual" (x + residual) with a residual, and with want_q the
+    int8 head's "q" [B x d] (rows padded to 16 bytes) and "q_scale" [B]."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [B x d], got shape {tuple(x.shape)}")
+    B, d = x.shape
+    got = {}
+    with _on(_device(x), stream):
+        if want_out:
+            got["out"] = torch.empty((B, d), dtype=x.dtype, device=x.device)
+        if residual is not None:
+            got["residual"] = torch.empty((B, d), dtype=x.dtype, device=x.device)
+        if want_q:
+            q = torch.empty((B, (d + 15) // 16 * 16), dtype=torch.int8, device=x.device)
+            got["q"] = q if d % 16 == 0 else q[:, :d]
+            got["q_scale"] = torch.empty((B,), dtype=torch.float32, device=x.device)
+        fh_rmsnorm(x, residual, weight, eps, weight_offset, got.get("out"), got.get("residual"), got.get("q"),
+                   got.get("q_scale"))
+    return got
+
+
+# ------------------------------------------------------- int8 product and head
+
+# What each handle holds, keyed by its value: (n, k, device).
+_WEIGHTS = {}
+
+
+def _key(w):
+    return w.value if isinstance(w, ctypes.c_void_p) else w
+
+
+def _weight(w):
+    info = _WEIGHTS.get(_key(w))
+    if info is None:
+        raise ValueError("unknown int8 weight (not created by fh_w8a8_create, or destroyed)")
+    return info
+
+
+def fh_w8a8_create(W: torch.Tensor, stream=None) -> ctypes.c_void_p:
+    """Quantise W [n x k] (float32 or bfloat16, contiguous) row by row."""
+    if W.dim() != 2 or W.dtype not in _DTYPES or not W.is_contiguous():
+        raise ValueError("W must be a contiguous [n x k] float32 or bfloat16 matrix")
+    dev = _device(W)
+    w = ctypes.c_void_p()
+    with _on(dev, stream):
+        check(_abi.load().fh_w8a8_create(W.data_ptr(), _DTYPES[W.dtype], W.shape[0], W.shape[1], _stream(dev),
+                                         ctypes.byref(w)))
+    _WEIGHTS[w.value] = (W.shape[0], W.shape[1], dev)
+    return w
+
+
+def fh_w8a8_create_codes(codes: torch.Tensor, scales: torch.Tensor, stream=None) -> ctypes.c_void_p:
+    """Take int8 codes [n x k] and float32 scales [n] as they are."""
+    if codes.dim() != 2 or codes.dtype is not torch.int8 or not codes.is_contiguous():
+        raise ValueError("codes must be a contiguous [n x k] int8 matrix")
+    _vector(scales, torch.float32, codes.shape[0], "scales")
+    dev = _device(codes, scales)
+    w = ctypes.c_void_p()
+    with _on(dev, stream):
+        check(_abi.load().fh_w8a8_create_codes(codes.data_ptr(), scales.data_ptr(), codes.shape[0], codes.shape[1],
+                                               _stream(dev), ctypes.byref(w)))
+    _WEIGHTS[w.value] = (codes.shape[0], codes.shape[1], dev)
+    return w
+
+
+def fh_w8a8_destroy(w) -> None:
+    _WEIGHTS.pop(_key(w), None)
+    _abi.load().fh_w8a8_destroy(w)
+
+
+def fh_w8a8_get(w, codes, scales, stream=None) -> None:
+    n, k, dev = _weight(w)
+    _shaped(codes, torch.int8, (n, k), "codes")
+    if not codes.is_contiguous():
+        raise ValueError("codes: must be contiguous")
+    _vector(scales, torch.float32, n, "scales")
+    if _device(codes, scales) != dev:
+        raise ValueError("codes and scales must be on the weight's GPU")
+    with _on(dev, stream):
+        check(_abi.load().fh_w8a8_get(w, codes.data_ptr(), scales.data_ptr(), _stream(dev)))
+
+
+def _product_args(w, q, q_scale):
+    n, k, dev = _weight(w)
+    if q.dim() != 2:
+        raise ValueError(f"q must be [B x k], got shape {tuple(q.shape)}")
+    B = q.shape[0]
+    ld_q = _rows(q, torch.int8, (B, k), "q")
+    _vector(q_scale, torch.float32, B, "q_scale")
+    return n, B, ld_q, dev
+
+
+def _size(status):
+    if status < 0:
+        check(status)
+    return status
+
+
+def _workspace_arg(workspace):
+    if workspace is None:
+        return None, 0
+    _vector(workspace, torch.uint8, workspace.numel(), "workspace")
+    return workspace.data_ptr(), workspace.numel()
+
+
+def fh_w8a8_workspace(w, q, forward: bool) -> int:
+    """Bytes of workspace of a product (or, with forward, head) call on q."""
+    _, k, _ = _weight(w)
+    ld_q = _rows(q, torch.int8, (q.shape[0], k), "q")
+    return _size(_abi.load().fh_w8a8_workspace(w, q.data_ptr(), ld_q, q.shape[0], int(forward)))
+
+
+def fh_w8a8_matmul(w, q, q_scale, out, workspace=None, stream=None) -> None:
+    n, B, ld_q, dev = _product_args(w, q, q_scale)
+    if out.dtype not in _DTYPES:
+        raise ValueError("out must be float32 or bfloat16")
+    ld_out = _rows(out, out.dtype, (B, n), "out")
+    ws, ws_bytes = _workspace_arg(workspace)
+    if _device(q, q_scale, out, workspace) != dev:
+        raise ValueError("tensors must be on the weight's GPU")
+    with _on(dev, stream):
+        check(_abi.load().fh_w8a8_matmul(w, q.data_ptr(), ld_q, q_scale.data_ptr(), B, out.data_ptr(), ld_out,
+                                         _DTYPES[out.dtype], ws, ws_bytes, _stream(dev)))
+
+
+def fh_w8a8_forward(w, q, q_scale, mode, temperature, seed, out_token, out_token_logit=None, out_lse=None,
+                    out_logits=None, workspace=None, stream=None) -> None:
+    n, B, ld_q, dev = _product_args(w, q, q_scale)
+    _vector(out_token, torch.int32, B, "out_token")
+    if out_token_logit is not None:
+        _vector(out_token_logit, torch.float32, B, "out_token_logit")
+    if out_lse is not None:
+        _vector(out_lse, torch.float32, B, "out_lse")
+    ld_out = 0 if out_logits is None else _rows(out_logits, torch.float32, (B, n), "out_logits")
+    ws, ws_bytes = _workspace_arg(workspace)
+    if _device(q, q_scale, out_token, out_token_logit, out_lse, out_logits, workspace) != dev:
+        raise ValueError("tensors must be on the weight's GPU")
+    with _on(dev, stream):
+        check(_abi.load().fh_w8a8_forward(w, q.data_ptr(), ld_q, q_scale.data_ptr(), B, mode, temperature, seed,
+                                          out_token.data_ptr(), _ptr(out_token_logit), _ptr(out_lse),
+                                          _ptr(out_logits), ld_out, ws, ws_bytes, _stream(dev)))
+
+
+class W8A8Head:
+    """A dense head (or any linear layer) with int8 weights and activations:
+    the rows of E quantised here, or int8 codes and scales as they are."""
+
+    def __init__(self, E: torch.Tensor = None, *, codes: torch.Tensor = None, scales: torch.Tensor = None,
+                 stream=None):
+        self.w = None
+        if (E is None) == (codes is None) or (codes is None) != (scales is None):
+            raise ValueError("give either E, or codes and scales")
+        if E is not None:
+            self.w = fh_w8a8_create(E, stream)
+        else:
+            self.w = fh_w8a8_create_codes(codes, scales, stream)
+        self.n, self.k, self.device = _weight(self.w)
+
+    def close(self):
+        if self.w is not None:
+            fh_w8a8_destroy(self.w)
+            self.w = None
+
+    def __del__(self):
+        # not while the interpreter shuts down (see FlashHead)
+        if sys.is_finalizing():
+            return
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _workspace(self, q, forward):
+        size = fh_w8a8_workspace(self.w, q, forward)
+        return torch.empty((size,), dtype=torch.uint8, device=self.device) if size else None
+
+    def codes(self, stream=None):
+        """The codes [n x k] and scales [n]."""
+        with _on(self.device, stream):
+            codes = torch.empty((self.n, self.k), dtype=torch.int8, device=self.device)
+            scales = torch.empty((self.n,), dtype=torch.float32, device=self.device)
+            fh_w8a8_get(self.w, codes, scales)
+        return codes, scales
+
+    def matmul(self, q: torch.Tensor, q_scale: torch.Tensor, dtype=torch.float32, stream=None) -> torch.Tensor:
+        """[B x n] = (q code^T) scaled per token and channel, in float32 or
+        bfloat16; q and q_scale as rmsnorm(want_q=True) gives them."""
+        with _on(self.device, stream):
+            out = torch.empty((q.shape[0], self.n), dtype=dtype, device=self.device)
+            fh_w8a8_matmul(self.w, q, q_scale, out, self._workspace(q, False))
+        return out
+
+    def forward(self, q: torch.Tensor, q_scale: torch.Tensor, mode: int = 0, temperature: float = 1.0,
+                seed: int = 0, want_logits: bool = False, stream=None) -> dict:
+        """FlashHead.dense on int8 operands: "token", "token_logit", "lse" and
+        with want_logits "logits" [B x n]."""
+        B = q.shape[0]
+        with _on(self.device, stream):
+            out = {"token": torch.empty((B,), dtype=torch.int32, device=self.device),
+                   "token_logit": torch.empty((B,), dtype=torch.float32, device=self.device),
+                   "lse": torch.empty((B,), dtype=torch.float32, device=self.device)}
+            if want_logits:
+                out["logits"] = torch.empty((B, self.n), dtype=torch.float32, device=self.device)
+            fh_w8a8_forward(self.w, q, q_scale, mode, temperature, seed, out["token"], out["token_logit"],
+                            out["lse"], out.get("logits"), self._workspace(q, True))
+        return out
+
+    def step(self, x: torch.Tensor, weight=None, *, residual=None, eps=1e-6, weight_offset=0.0, rules=None,
+             mode: int = 0, temperature: float = 1.0, seed: int = 0, want_logits: bool = False,
+             stream=None) -> dict:
+        """One decode step after the last layer: rmsnorm(x + residual) in int8,
+        the head, the rules (LogitRules, or None) and the choice of the token."""
+        with _on(self.device, stream):
+            h = rmsnorm(x, weight, residual=residual, eps=eps, weight_offset=weight_offset, want_out=False,
+                        want_q=True)
+            if rules is None:
+                return self.forward(h["q"], h["q_scale"], mode, temperature, seed, want_logits)
+            z = self.matmul(h["q"], h["q_scale"])
+            out = logits_apply(z, rules, mode=mode, temperature=temperature, seed=seed, out=z)
+            if not want_logits:
+                del out["logits"]
+            return out
+
+
+# ------------------------------------------------------------ rules on logits
+
+class LogitRules:
+    """The rules of a batch of B rows over a vocabulary of v tokens, kept from
+    step to step: the tensors are borrowed and read at every call, so a program
+    (or a captured graph) updates them in place.
+
+    history [B x L] int32 with n_prompt, n_history [B] int32; repetition,
+    frequency, presence [B] float32; bias_ids [B x N] int32 with bias float32
+    and n_bias [B] int32; mask [R x ceil(v / 32)] int32 words (bit t % 32 of
+    word t / 32 allows token t) with mask_row [B] int32 (outside [0, R): all
+    allowed; without it row b takes mask row b).  Each may be None.
+    """
+
+    def __init__(self, v: int, *, history=None, n_prompt=None, n_history=None, repetition=None, frequency=None,
+                 presence=None, bias_ids=None, bias=None, n_bias=None, mask=None, mask_row=None):
+        vectors = {"n_prompt": (n_prompt, torch.int32), "n_history": (n_history, torch.int32),
+                   "repetition": (repetition, torch.float32), "frequency": (frequency, torch.float32),
+                   "presence": (presence, torch.float32), "n_bias": (n_bias, torch.int32),
+                   "mask_row": (mask_row, torch.int32)}
+        lists = {"history": history, "bias_ids": bias_ids, "bias": bias}
+        sized = [t for t in lists.values() if t is not None] + [t for t, _ in vectors.values() if t is not None]
+        for name, t in lists.items():
+            if t is not None and t.dim() != 2:
+                raise ValueError(f"{name} must be [B x length], got shape {tuple(t.shape)}")
+        if history is None and any(t is not None for t in (n_prompt, n_history, repetition, frequency, presence)):
+            raise ValueError("n_prompt, n_history and penalties need a history")
+        if (bias_ids is None) != (bias is None) or (n_bias is not None and bias is None):
+            raise ValueError("bias_ids and bias go together, n_bias needs them")
+        if mask is None and mask_row is not None:
+            raise ValueError("mask_row needs a mask")
+        self.v = v
+        self.B = sized[0].shape[0] if sized else (mask.shape[0] if mask is not None else None)
+        s = _abi.FhLogitRules()
+        for name, (t, dt) in vectors.items():
+            if t is not None:
+                _vector(t, dt, self.B, name)
+                setattr(s, name, t.data_ptr())
+        if history is not None:
+            s.ld_history = _rows(history, torch.int32, (self.B, history.shape[1]), "history")
+            s.history, s.history_len = history.data_ptr(), history.shape[1]
+        if bias is not None:
+            shape = (self.B, bias.shape[1])
+            s.ld_bias = _rows(bias, torch.float32, shape, "bias")
+            if _rows(bias_ids, torch.int32, shape, "bias_ids") != s.ld_bias:
+                raise ValueError("bias_ids and bias must have the same row stride")
+            s.bias_ids, s.bias, s.bias_len = bias_ids.data_ptr(), bias.data_ptr(), bias.shape[1]
+        if mask is not None:
+            if mask.dim() != 2:
+                raise ValueError(f"mask must be [R x words], got shape {tuple(mask.shape)}")
+            s.ld_mask = _rows(mask, torch.int32, (mask.shape[0], (v + 31) // 32), "mask")
+            s.mask, s.mask_rows = mask.data_ptr(), mask.shape[0]
+            if mask_row is None and mask.shape[0] < (self.B or 0):
+                raise ValueError("the mask has fewer rows than the batch; give mask_row")
+        kept = [t for t in sized + [mask] if t is not None]
+        self.device = _device(*kept) if kept else None
+        self._kept = kept  # borrowed: alive as long as the struct points to them
+        self._struct = s
+
+
+def fh_logits_workspace(B: int, n: int) -> int:
+    """Bytes of workspace of a call over [B x n] logits that chooses tokens."""
+    return _size(_abi.load().fh_logits_workspace(B, n))
+
+
+def fh_logits_apply(logits, ids, v, rules, mode, temperature, seed, out_logits=None, out_token=None,
+                    out_token_logit=None, out_lse=None, workspace=None, stream=None) -> None:
+    """The rules (LogitRules or None) on logits [B x n], of all v tokens or of
+    the tokens ids [B x n], then the choice of the token."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [B x n], got shape {tuple(logits.shape)}")
+    shape = logits.shape
+    B, n = shape
+    ld_z = _rows(logits, torch.float32, shape, "logits")
+    ld_ids = 0 if ids is None else _rows(ids, torch.int32, shape, "ids")
+    ld_out = 0 if out_logits is None else _rows(out_logits, torch.float32, shape, "out_logits")
+    if out_token is not None:
+        _vector(out_token, torch.int32, B, "out_token")
+    if out_token_logit is not None:
+        _vector(out_token_logit, torch.float32, B, "out_token_logit")
+    if out_lse is not None:
+        _vector(out_lse, torch.float32, B, "out_lse")
+    struct = None
+    if rules is not None:
+        if rules.v != v or (rules.B is not None and rules.B != B):
+            raise ValueError(f"rules are of {rules.B} rows over {rules.v} tokens, logits of {B} rows over {v}")
+        if rules.device is not None and rules.device != logits.device:
+            raise ValueError("rules and logits must be on one GPU")
+        struct = rules._struct
+    ws, ws_bytes = _workspace_arg(workspace)
+    dev = _device(logits, ids, out_logits, out_token, out_token_logit, out_lse, workspace)
+    with _on(dev, stream):
+        check(_abi.load().fh_logits_apply(logits.data_ptr(), ld_z, _ptr(ids), ld_ids, B, n, v, struct, mode,
+                                          temperature, seed, _ptr(out_logits), ld_out, _ptr(out_token),
+                                          _ptr(out_token_logit), _ptr(out_lse), ws, ws_bytes, _stream(dev)))
+
+
+def logits_apply(logits, rules=None, *, ids=None, v=None, mode: int = 0, temperature: float = 1.0, seed: int = 0,
+                 want_token: bool = True, out=None, stream=None) -> dict:
+    """The rules on logits [B x n] of all tokens, or of the tokens ids [B x n]
+    (a forward's "logits" and "ids"): "logits" (in `out`, which may be logits
+    itself) and with want_token "token", "token_logit" and "lse"."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [B x n], got shape {tuple(logits.shape)}")
+    B, n = logits.shape
+    if v is None:
+        v = rules.v if rules is not None else n
+    dev = _device(logits)
+    with _on(dev, stream):
+        got = {"logits": torch.empty((B, n), dtype=torch.float32, device=dev) if out is None else out}
+        workspace = None
+        if want_token:
+            got["token"] = torch.empty((B,), dtype=torch.int32, device=dev)
+            got["token_logit"] = torch.empty((B,), dtype=torch.float32, device=dev)
+            got["lse"] = torch.empty((B,), dtype=torch.float32, device=dev)
+            workspace = torch.empty((fh_logits_workspace(B, n),), dtype=torch.uint8, device=dev)
+        fh_logits_apply(logits, ids, v, rules, mode, temperature, seed, got["logits"], got.get("token"),
+                        got.get("token_logit"), got.get("lse"), workspace)
+    return got

@@ -1,0 +1,138 @@
+"""GPU parity of fh_rmsnorm against the float64 definition.
+
+Tolerances, u = 2^-24 (float32's half step): s = x + r rounds once (u).  The sum
+of squares is of positive terms: with at least 64 lanes a term goes through at
+most d / 64 + 16 roundings, of which the root halves the effect.  The mean, eps,
+the root, the reciprocal, its product with s, offset + w and its product round
+at most once each, s itself once more: 10 u.  So y is within
+(d / 128 + 20) u of itself; a bfloat16 output adds 2^-8.  Where offset + w
+cancels, its rounding is relative to the result, so nothing is added.  The scale
+is max |y| / 127 (u more); a code is off by half a step plus 127 times y's and
+the scale's relative errors and the division's."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serve_oracle
+
+from _gpu import need_gpu, say
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+    from lm_output_head_amd import load_library
+    load_library()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def check(x, r, w, eps, off, got):
+    B, d = x.shape
+    y, s = serve_oracle.rmsnorm(f64(x), None if r is None else f64(r), None if w is None else f64(w), eps, off)
+    rel = (d / 128 + 20) * U
+    half = 2.0 ** -8 if x.dtype == torch.bfloat16 else 0.0
+    if "out" in got:
+        assert got["out"].dtype == x.dtype
+        assert np.all(np.abs(f64(got["out"]) - y) <= (rel + half * (1 + rel)) * np.abs(y) + 1e-38)
+    if r is not None and "residual" in got:
+        assert np.all(np.abs(f64(got["residual"]) - s) <= (U + half * (1 + U)) * np.abs(s))
+    if "q" in got:
+        q, sc = f64(got["q"]), f64(got["q_scale"])
+        want = np.abs(y).max(1) / 127
+        assert np.all(np.abs(sc - want) <= (rel + U) * want + 1e-38)
+        assert q.min() >= -127 and q.max() <= 127
+        step = np.where(sc > 0, sc, 1.0)[:, None]
+        assert np.all(np.abs(q - y / step) <= 0.5 + 128 * (2 * rel + 2 * U))
+        assert np.all(q[sc == 0] == 0)
+
+
+def make(B, d, dt, seed, res):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(B, d, generator=g) * 3).to(dt).cuda()
+    r = torch.randn(B, d, generator=g).to(dt).cuda() if res else None
+    w = torch.randn(d, generator=g).to(dt).cuda()
+    return x, r, w
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,d", [(1, 1), (1, 2048), (3, 7), (2, 64), (5, 1152), (17, 1000), (4, 2560), (2, 8192),
+                                 (300, 96), (3, 4104), (2, 16385), (1, 70001)])
+def test_sizes(dt, B, d):
+    from lm_output_head_amd import rmsnorm
+    x, r, w = make(B, d, dt, B * d, True)
+    say("norm", dt, B, d)
+    check(x, r, w, 1e-6, 0.0, rmsnorm(x, w, residual=r, want_q=True))
+    check(x, None, w, 1e-5, 1.0, rmsnorm(x, w, eps=1e-5, weight_offset=1.0))
+    check(x, None, None, 1e-6, 0.0, rmsnorm(x, want_out=False, want_q=True))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("off", [0, 1])
+def test_strides_alignment_and_what_lies_between(dt, off):
+    """Rows inside wider ones at an odd offset: only the rows are written."""
+    from lm_output_head_amd import fh_rmsnorm
+    for B, d, ld in [(4, 256, 264), (5, 250, 333), (3, 2048, 2056)]:
+        x, r, w = make(B, d, dt, ld + off, True)
+        wide = [torch.full((B + 1, ld), 7, dtype=t, device="cuda") for t in (dt, dt, dt, dt, torch.int8)]
+        at = slice(off, off + d)
+        xs, rs, os_, ss, qs = [t[:B, at] for t in wide]
+        xs.copy_(x)
+        rs.copy_(r)
+        ws = torch.zeros(d + 1, dtype=dt, device="cuda")[off:off + d]
+        ws.copy_(w)
+        scale = torch.full((B + 1,), 7.0, device="cuda")
+        say("norm strides", dt, B, d, ld, off)
+        fh_rmsnorm(xs, rs, ws, 1e-6, 0.0, os_, ss, qs, scale[:B])
+        check(x, r, w, 1e-6, 0.0, {"out": os_, "residual": ss, "q": qs, "q_scale": scale[:B]})
+        for t in wide[2:]:
+            mark = t.clone()
+            mark[:B, at] = 7
+            assert torch.all(mark == 7)
+        assert scale[B] == 7 and torch.equal(xs, x) and torch.equal(rs, r)
+
+
+@pytest.mark.parametrize("dt,d", [(torch.bfloat16, 2048), (torch.float32, 1000), (torch.bfloat16, 40000)])
+def test_in_place(dt, d):
+    from lm_output_head_amd import fh_rmsnorm, rmsnorm
+    x, r, w = make(6, d, dt, 5, True)
+    ref = rmsnorm(x, w, residual=r, want_q=True)
+    x2, r2 = x.clone(), r.clone()
+    q, sc = torch.empty(6, d, dtype=torch.int8, device="cuda"), torch.empty(6, device="cuda")
+    say("norm in place", dt, d)
+    fh_rmsnorm(x2, r2, w, 1e-6, 0.0, x2, r2, q, sc)
+    assert torch.equal(x2, ref["out"]) and torch.equal(r2, ref["residual"])
+    assert torch.equal(q, ref["q"]) and torch.equal(sc, ref["q_scale"])
+
+
+def test_zero_and_non_finite_rows():
+    from lm_output_head_amd import rmsnorm
+    x = torch.randn(5, 512, device="cuda").bfloat16()
+    x[1] = 0
+    x[2, 17] = float("inf")
+    x[3, 500] = float("nan")
+    say("norm zero and non-finite rows")
+    got = rmsnorm(x, want_q=True)
+    torch.cuda.synchronize()
+    assert torch.all(got["out"][1] == 0) and got["q_scale"][1] == 0 and torch.all(got["q"][1] == 0)
+    assert got["out"][2, 17].isnan() and got["out"][3].isnan().all()
+    assert got["q_scale"][2].isnan() and got["q_scale"][3].isnan()
+    keep = [0, 4]
+    check(x[keep], None, None, 1e-6, 0.0, {k: v[keep] for k, v in got.items()})
+
+
+def test_last_positions_of_a_batch():
+    """x = hidden[:, -1] of [B x T x d] is taken without a copy."""
+    from lm_output_head_amd import rmsnorm
+    hidden = torch.randn(3, 9, 640, device="cuda").bfloat16()
+    w = torch.randn(640, device="cuda").bfloat16()
+    say("norm of last positions")
+    a, b = rmsnorm(hidden[:, -1], w, want_q=True), rmsnorm(hidden[:, -1].contiguous(), w, want_q=True)
+    assert all(torch.equal(a[k], b[k]) for k in a)
+    check(hidden[:, -1], None, w, 1e-6, 0.0, a)
