@@ -13,85 +13,250 @@
 namespace fh {
 namespace {
 
+// Elements of T as they are stored, eight of bfloat16 or four of float32 (16
+// bytes), at any alignment of the element: rows of odd widths are read and
+// written 16 bytes at a time too, only a row's last chunk may be partial.
 template <typename T>
-__device__ __forceinline__ float to_f32(T v);
+struct Elems;
 template <>
-__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+struct Elems<float> {
+  static constexpr int N = 4;
+  typedef float V __attribute__((ext_vector_type(4), aligned(4)));
+  __device__ static float get(float v) { return v; }
+  __device__ static float put(float v) { return v; }
+};
 template <>
-__device__ __forceinline__ float to_f32<uint16_t>(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+struct Elems<uint16_t> {
+  static constexpr int N = 8;
+  typedef uint16_t V __attribute__((ext_vector_type(8), aligned(2)));
+  __device__ static float get(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+  __device__ static uint16_t put(float v) {
+    return __builtin_bit_cast(uint16_t, (__bf16)v);  // round to nearest even
+  }
+};
+
+// Elements at .. at + N - 1 of a row of d, zero past it.
+template <typename T>
+__device__ __forceinline__ void load_chunk(const T* p, int64_t at, int64_t d, float (&v)[Elems<T>::N]) {
+  constexpr int N = Elems<T>::N;
+  if (at + N <= d) {
+    const typename Elems<T>::V x = *reinterpret_cast<const typename Elems<T>::V*>(p + at);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = Elems<T>::get(x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = at + i < d ? Elems<T>::get(p[at + i]) : 0.f;
+  }
+}
 
 template <typename T>
-__device__ __forceinline__ T from_f32(float v);
-template <>
-__device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ uint16_t from_f32<uint16_t>(float v) {
-  return __builtin_bit_cast(uint16_t, (__bf16)v);  // round to nearest even
+__device__ __forceinline__ void store_chunk(T* p, int64_t at, int64_t d, const float (&v)[Elems<T>::N]) {
+  constexpr int N = Elems<T>::N;
+  if (at + N <= d) {
+    typename Elems<T>::V x;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = Elems<T>::put(v[i]);
+    *reinterpret_cast<typename Elems<T>::V*>(p + at) = x;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (at + i < d) p[at + i] = Elems<T>::put(v[i]);
+  }
 }
 
 // Largest |y| as its bit pattern: NaN's is above infinity's, so a maximum of
 // patterns keeps it.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-__device__ __forceinline__ int quant8(float y, float scale) {
-  return scale > 0.f ? (int)fminf(fmaxf(rintf(y / scale), -127.f), 127.f) : 0;
+// rint(t), |t| <= 127.01, as a byte: adding 1.5 2^23 leaves the integer, rounded
+// to nearest even, in the low bits of the sum.
+__device__ __forceinline__ uint32_t byte_of(float t) { return __float_as_uint(t + 12582912.f) & 0xFFu; }
+
+// Codes of one chunk; y r with r = 127 / max |y| (one multiplication for the
+// division, which only decides within a rounding of a half).
+template <int N>
+__device__ __forceinline__ void store_codes(int8_t* p, int64_t at, int64_t d, const float (&y)[N], float r) {
+  uint32_t w[N / 4];
+#pragma unroll
+  for (int j = 0; j < N / 4; ++j)
+    w[j] = byte_of(y[4 * j] * r) | byte_of(y[4 * j + 1] * r) << 8 | byte_of(y[4 * j + 2] * r) << 16 |
+           byte_of(y[4 * j + 3] * r) << 24;
+  if (at + N <= d) {
+    typedef uint32_t W __attribute__((ext_vector_type(N / 4), aligned(1)));
+    W x;
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) x[j] = w[j];
+    *reinterpret_cast<W*>(p + at) = x;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (at + i < d) p[at + i] = (int8_t)(w[i >> 2] >> (8 * (i & 3)));
+  }
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void k_rmsnorm(NormArgs a, int64_t B) {
-  __shared__ float red[4];
-  __shared__ uint32_t redu[4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t d = a.d;
-  for (int64_t b = blockIdx.x; b < B; b += gridDim.x) {
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
+  return v;
+}
+
+// Sum (or maximum) over the W waves that share a row; W = 1 needs no LDS.
+template <int W, typename V, typename Op>
+__device__ __forceinline__ V across(V v, V* sh, Op op) {
+  if constexpr (W == 1) return v;
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = sh[0];
+#pragma unroll
+  for (int w = 1; w < W; ++w) v = op(v, sh[w]);
+  return v;
+}
+
+__device__ __forceinline__ float scale_of(uint32_t top) { return __uint_as_float(top) / 127.f; }
+__device__ __forceinline__ float inverse_of(uint32_t top) { return top ? 127.f / __uint_as_float(top) : 0.f; }
+
+// W waves per row, C chunks per lane: the row stays in registers between its
+// one read and the writes.  A workgroup is max(4, W) waves.
+template <typename T, int W, int C>
+__global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void k_rmsnorm(NormArgs a, int64_t B) {
+  constexpr int N = Elems<T>::N, kRows = W <= 4 ? 4 / W : 1;
+  static_assert(kRows == 1 || W == 1, "waves that share a row make up the workgroup");
+  __shared__ float sum_sh[W];
+  __shared__ uint32_t top_sh[W];
+  const int64_t b = (int64_t)blockIdx.x * kRows + (kRows > 1 ? threadIdx.x >> 6 : 0), d = a.d;
+  if (b >= B) return;
+  const int lane = kRows > 1 ? threadIdx.x & 63 : threadIdx.x;
   const T* x = static_cast<const T*>(a.x) + b * a.ld_x;
   const T* r = a.residual ? static_cast<const T*>(a.residual) + b * a.ld_residual : nullptr;
   const T* w = static_cast<const T*>(a.weight);
-  auto sum_at = [&](int64_t i) { return r ? to_f32<T>(x[i]) + to_f32<T>(r[i]) : to_f32<T>(x[i]); };
-  float ss = 0.f;
-  for (int64_t i = tid; i < d; i += 256) {
-    const float s = sum_at(i);
-    ss = fmaf(s, s, ss);
-  }
-  ss = wave_sum(ss);
-  if (lane == 0) red[wave] = ss;
-  __syncthreads();
-  const float inv = 1.f / sqrtf(((red[0] + red[1]) + (red[2] + red[3])) / (float)d + a.eps);
-  auto norm_at = [&](int64_t i, float s) {
-    const float y = s * inv;
-    return w ? y * (a.offset + to_f32<T>(w[i])) : y;
-  };
-  float scale = 0.f;
-  if (a.out_q) {
-    uint32_t top = 0u;
-    for (int64_t i = tid; i < d; i += 256) top = max(top, abs_bits(norm_at(i, sum_at(i))));
+  float y[C][N];
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
-    if (lane == 0) redu[wave] = top;
-    __syncthreads();
-    scale = __uint_as_float(max(max(redu[0], redu[1]), max(redu[2], redu[3]))) / 127.f;
-    if (tid == 0) a.out_scale[b] = scale;
+  for (int c = 0; c < C; ++c) load_chunk<T>(x, (int64_t)N * (lane + 64 * W * c), d, y[c]);
+  if (r) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float v[N];
+      load_chunk<T>(r, (int64_t)N * (lane + 64 * W * c), d, v);
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[c][i] += v[i];
+    }
   }
-  // each element is read and written by one thread, x and residual before the
-  // outputs that may be their own storage
-  for (int64_t i = tid; i < d; i += 256) {
-    const float s = sum_at(i), y = norm_at(i, s);
-    if (a.out) static_cast<T*>(a.out)[b * a.ld_out + i] = from_f32<T>(y);
-    if (a.out_residual) static_cast<T*>(a.out_residual)[b * a.ld_out_residual + i] = from_f32<T>(s);
-    if (a.out_q) a.out_q[b * a.ld_q + i] = (int8_t)quant8(y, scale);
+  // the sum leaves here: out_residual may be x or residual, whose chunk this
+  // lane has read
+  if (a.out_residual) {
+    T* o = static_cast<T*>(a.out_residual) + b * a.ld_out_residual;
+#pragma unroll
+    for (int c = 0; c < C; ++c) store_chunk<T>(o, (int64_t)N * (lane + 64 * W * c), d, y[c]);
+    if (!a.out && !a.out_q) return;
   }
-  __syncthreads();  // red and redu are free for the next row
+  float ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < N; ++i) ss = fmaf(y[c][i], y[c][i], ss);
+  ss = across<W>(wave_sum(ss), sum_sh, [](float p, float q) { return p + q; });
+  const float inv = 1.f / sqrtf(ss / (float)d + a.eps);
+  uint32_t top = 0u;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int64_t at = (int64_t)N * (lane + 64 * W * c);
+    float v[N];
+    if (w) load_chunk<T>(w, at, d, v);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      y[c][i] *= inv;
+      if (w) y[c][i] *= a.offset + v[i];
+      if (at + i < d) top = max(top, abs_bits(y[c][i]));
+    }
+    if (a.out) store_chunk<T>(static_cast<T*>(a.out) + b * a.ld_out, at, d, y[c]);
   }
+  if (!a.out_q) return;
+  top = across<W>(wave_umax(top), top_sh, [](uint32_t p, uint32_t q) { return max(p, q); });
+  if (lane == 0) a.out_scale[b] = scale_of(top);
+  const float rs = inverse_of(top);
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    store_codes<N>(a.out_q + b * a.ld_q, (int64_t)N * (lane + 64 * W * c), d, y[c], rs);
+}
+
+// Rows too long for the registers: three passes over the row, the later two from
+// the caches.
+template <typename T>
+__global__ __launch_bounds__(1024) void k_rmsnorm_long(NormArgs a, int64_t B) {
+  constexpr int W = 16;
+  __shared__ float sum_sh[W];
+  __shared__ uint32_t top_sh[W];
+  const int tid = threadIdx.x;
+  const int64_t d = a.d;
+  const T* w = static_cast<const T*>(a.weight);
+  for (int64_t b = blockIdx.x; b < B; b += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + b * a.ld_x;
+    const T* r = a.residual ? static_cast<const T*>(a.residual) + b * a.ld_residual : nullptr;
+    auto sum_at = [&](int64_t i) { return Elems<T>::get(x[i]) + (r ? Elems<T>::get(r[i]) : 0.f); };
+    float ss = 0.f;
+    for (int64_t i = tid; i < d; i += 64 * W) {
+      const float s = sum_at(i);
+      ss = fmaf(s, s, ss);
+    }
+    ss = across<W>(wave_sum(ss), sum_sh, [](float p, float q) { return p + q; });
+    const float inv = 1.f / sqrtf(ss / (float)d + a.eps);
+    auto norm_at = [&](int64_t i, float s) { return w ? s * inv * (a.offset + Elems<T>::get(w[i])) : s * inv; };
+    float rs = 0.f;
+    if (a.out_q) {
+      uint32_t top = 0u;
+      for (int64_t i = tid; i < d; i += 64 * W) top = max(top, abs_bits(norm_at(i, sum_at(i))));
+      top = across<W>(wave_umax(top), top_sh, [](uint32_t p, uint32_t q) { return max(p, q); });
+      if (tid == 0) a.out_scale[b] = scale_of(top);
+      rs = inverse_of(top);
+    }
+    // an element is read and written by one thread, x and residual before the
+    // outputs that may be their own storage
+    for (int64_t i = tid; i < d; i += 64 * W) {
+      const float s = sum_at(i), y = norm_at(i, s);
+      if (a.out) static_cast<T*>(a.out)[b * a.ld_out + i] = Elems<T>::put(y);
+      if (a.out_residual) static_cast<T*>(a.out_residual)[b * a.ld_out_residual + i] = Elems<T>::put(s);
+      if (a.out_q) a.out_q[b * a.ld_q + i] = (int8_t)byte_of(y * rs);
+    }
+    __syncthreads();  // sum_sh and top_sh are free for the next row
+  }
+}
+
+template <typename T, int W>
+bool launch_w(const NormArgs& a, int64_t B, hipStream_t st) {
+  const int64_t chunks = (a.d + Elems<T>::N - 1) / Elems<T>::N, c = (chunks + 64 * W - 1) / (64 * W);
+  const int64_t rows = W == 1 ? 4 : 1;
+  const dim3 grid((unsigned)((B + rows - 1) / rows)), block(W <= 4 ? 256 : 64 * W);
+  switch (c) {
+#define FH_CASE(CC) \
+  case CC: hipLaunchKernelGGL((k_rmsnorm<T, W, CC>), grid, block, 0, st, a, B); return true;
+    FH_CASE(1) FH_CASE(2) FH_CASE(3) FH_CASE(4) FH_CASE(5) FH_CASE(6) FH_CASE(7) FH_CASE(8)
+#undef FH_CASE
+    default: return false;
+  }
+}
+
+template <typename T>
+void launch(const NormArgs& a, int64_t B, hipStream_t st) {
+  // a wave per row while rows are many and fit its lanes' 8 chunks; else the
+  // row's waves share it.  Grids stay below 2^32 threads.
+  const int64_t chunks = (a.d + Elems<T>::N - 1) / Elems<T>::N;
+  if (B <= (int64_t(1) << 21)) {
+    if (chunks <= 64 || (B > 2048 && chunks <= 64 * 8)) {
+      if (launch_w<T, 1>(a, B, st)) return;
+    }
+    if (chunks <= 256 * 8 && launch_w<T, 4>(a, B, st)) return;
+    if (launch_w<T, 16>(a, B, st)) return;
+  }
+  hipLaunchKernelGGL((k_rmsnorm_long<T>), dim3((unsigned)std::min<int64_t>(B, 1 << 20)), dim3(1024), 0, st, a, B);
 }
 
 }  // namespace
 
 hipError_t launch_rmsnorm(const NormArgs& a, bool bf16, int64_t B, hipStream_t stream) {
-  const dim3 grid((unsigned)std::min<int64_t>(B, 1 << 20)), block(256);
   if (bf16)
-    hipLaunchKernelGGL((k_rmsnorm<uint16_t>), grid, block, 0, stream, a, B);
+    launch<uint16_t>(a, B, stream);
   else
-    hipLaunchKernelGGL((k_rmsnorm<float>), grid, block, 0, stream, a, B);
+    launch<float>(a, B, stream);
   return hipGetLastError();
 }
 
