@@ -471,7 +471,7 @@ typedef struct fh_w8a8 fh_w8a8; /* opaque */
  * fh_w8a8_create_codes — take codes [n x k] int8 (-128 included) and scales
  * [n] float as they are, both device and dense.
  * Both copy into the handle's own layout (n k bytes, n rounded up to 16 and k
- * to 64, plus 4 n), wait for `stream`, and keep nothing of their arguments.
+ * to 128, plus 4 n), wait for `stream`, and keep nothing of their arguments.
  * 1 <= n <= 2^30, 1 <= k < 131072 (the int32 sums of the product are exact).
  */
 fh_status fh_w8a8_create(const void* W, fh_dtype dtype, int64_t n, int64_t k, void* stream,

@@ -44,6 +44,74 @@ __device__ __forceinline__ Part choice_merge(Part a, const Part& b) {
   return a;
 }
 
+// Philox4x32-10 of philox_block's counter for token draws (stage 1), both halves
+// of each 32 x 32 product from one instruction.
+__device__ __forceinline__ U4 token_words(uint64_t seed, uint32_t row, uint32_t blk) {
+  uint32_t x = blk, y = row, z = 1u, w = 0u, k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t a = (uint64_t)0xD2511F53u * x, c = (uint64_t)0xCD9E8D57u * z;
+    x = (uint32_t)(c >> 32) ^ y ^ k0;
+    y = (uint32_t)c;
+    z = (uint32_t)(a >> 32) ^ w ^ k1;
+    w = (uint32_t)a;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return U4{x, y, z, w};
+}
+
+// The exponential variate -ln u of a word (gumbel_from_word is -ln of it).
+__device__ __forceinline__ float exponential_from_word(uint32_t w) {
+  return -logf(((float)(w >> 9) + 0.5f) * 1.1920928955078125e-07f);
+}
+
+// A lane's N logits as a Part.  open(i): whether logit i counts; x(i): z / T';
+// word(i): its Philox word (sampling).  The largest x comes first, then the
+// exponentials e = exp(x - m) that the LSE sums.  The draw is the same race in
+// another form: max of x - ln(-ln u) is max of e / (-ln u), so it needs one
+// logarithm more per logit and no division (e l' > e' l); the key itself is
+// formed for the winner alone, to be compared between lanes.  Logits come by
+// ascending id or compare ids; a tie stays with the smaller id.
+template <int N>
+__device__ __forceinline__ Part choose(const float (&z)[N], const int32_t (&id)[N], const bool (&open)[N],
+                                       bool sample, float tprime, const uint32_t (&word)[N]) {
+  Part p = part_empty();
+  float x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = open[i] ? (sample ? scaled_logit(z[i], tprime) : z[i]) : -INFINITY;
+    p.m = fmaxf(p.m, x[i]);
+  }
+  if (sample) {
+    float be = 0.f, bl = 1.f, bx = -INFINITY;
+    uint32_t bw = 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float e = open[i] ? exp_from(x[i], p.m) : 0.f, l = exponential_from_word(word[i]);
+      p.s += e;
+      const float mine = e * bl, best = be * l;
+      if (mine > best || (mine == best && mine > 0.f && id[i] < p.id)) {
+        be = e;
+        bl = l;
+        bx = x[i];
+        bw = word[i];
+        p.z = z[i];
+        p.id = id[i];
+      }
+    }
+    if (p.m == -INFINITY) p.id = 0x7FFFFFFF;  // nothing is left: all e are 1 by definition
+    p.key = p.id == 0x7FFFFFFF ? -INFINITY : bx + gumbel_from_word(bw);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      p.s += open[i] ? exp_from(x[i], p.m) : 0.f;
+      if (open[i]) choice_key(p, z[i], z[i], id[i]);
+    }
+  }
+  return p;
+}
+
 __device__ __forceinline__ Part shfl_part(const Part& p, int mask) {
   return Part{__shfl_xor(p.key, mask), __shfl_xor(p.z, mask), __shfl_xor(p.m, mask),
               __shfl_xor(p.s, mask), __shfl_xor(p.id, mask)};

@@ -222,7 +222,7 @@ hipError_t launch_rmsnorm(const NormArgs& a, bool bf16, int64_t B, hipStream_t s
 // row l % 16 and elements 16 (l / 16) .. + 15, tiles of a row group by
 // ascending k; rows and elements past n and k are zero.
 struct W8A8Args {
-  const uint4* W;        // [ceil(n / 16)][ceil(k / 64)][64]
+  const void* W;         // [ceil(n / 16)][2 ceil(k / 128)][64]
   const float* ws;       // [n]
   int64_t n;
   int k;                 // elements of a row
@@ -279,7 +279,7 @@ struct RulesArgs {
   int64_t ld_out;
   Part* parts;           // [B x rules_parts], or null: no choice
 };
-int64_t rules_parts(int64_t B, int64_t n, bool dense);
+int64_t rules_parts(int64_t B, int64_t n);
 hipError_t launch_rules(const RulesArgs& a, int64_t B, hipStream_t st);
 // the choice over each row's parts (w8a8 head, rules)
 hipError_t launch_choice(const Part* parts, int64_t B, int64_t nparts, int32_t* out_token,

@@ -4,12 +4,12 @@
 //
 // A workgroup owns one tile of one row and keeps a table of its tokens in LDS:
 // a word with the token's count in the output and, in bit 31, whether it is in
-// the prompt, and the sum of its biases.  It walks the row's whole history and
-// bias list once, adds what falls into its tile, and then streams the tile's
-// logits.  Dense rows index the table by token; rows of listed candidates
-// through a hash of their ids.  Counts are integer sums, and one thread adds
-// all biases of a token in the list's order, so results do not depend on the
-// order of execution.
+// the prompt, and the sum of its biases.  The tile's logits travel to registers
+// while the workgroup walks the row's whole history and bias list and adds what
+// falls into its tile.  Dense rows index the table by token; rows of listed
+// candidates through a hash of their ids.  Counts are integer sums, and one
+// thread adds all biases of a token in the list's order, so results do not
+// depend on the order of execution.
 
 #include <hip/hip_runtime.h>
 
@@ -19,87 +19,138 @@
 namespace fh {
 namespace {
 
-typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
-
 constexpr int kThreads = 256;
-constexpr int kTileDense = 4096;   // tokens of a dense tile: 32 KB of tables
-constexpr int kTileIds = 1024;     // candidates of a tile
-constexpr int kSlots = 2048;       // hash slots: at most half of them in use
 constexpr uint32_t kPrompt = 0x80000000u;
 constexpr int32_t kFree = -1;
 
-template <bool DENSE>
+typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// Four consecutive elements at i, those below n; `other` in the places past it.
+template <typename V, typename T>
+__device__ __forceinline__ void load4(const T* p, int64_t i, int64_t n, T other, T (&v)[4]) {
+  if (i + 4 <= n) {
+    const V x = *reinterpret_cast<const V*>(p + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = x[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = i + e < n ? p[i + e] : other;
+  }
+}
+
+// DENSE: a table word per token of the tile.  Else a hash of twice the tile's
+// size, so that at most half of its slots are taken and every search ends.
+template <bool DENSE, int TILE>
 struct Tables {
-  static constexpr int kSize = DENSE ? kTileDense : kSlots;
+  static constexpr int kSize = DENSE ? TILE : 2 * TILE;
   uint32_t count[kSize];
   float bias[kSize];
   int32_t key[DENSE ? 1 : kSize];
   int list_at[kThreads];
   float list_add[kThreads];
   Part parts[kThreads / 64];
-};
 
-__device__ __forceinline__ uint32_t hash_id(int32_t id) { return ((uint32_t)id * 0x9E3779B1u) >> 21; }
-static_assert(kSlots == 1 << (32 - 21), "the hash gives a slot");
-
-// The table's place of token t, or -1.
-template <bool DENSE>
-__device__ __forceinline__ int place_of(const Tables<DENSE>& sh, int32_t t, int64_t base, int64_t width, int64_t v) {
-  if constexpr (DENSE) {
-    const int64_t u = (int64_t)t - base;
-    return u >= 0 && u < width ? (int)u : -1;
-  } else {
-    if (t < 0 || (int64_t)t >= v) return -1;
-    uint32_t s = hash_id(t);
-    while (true) {  // ends at the token or at a free slot: half of the slots are free
-      const int32_t k = sh.key[s];
-      if (k == t) return (int)s;
-      if (k == kFree) return -1;
-      s = (s + 1) & (kSlots - 1);
+  __device__ static uint32_t hash(int32_t id) { return ((uint32_t)id * 0x9E3779B1u) >> 16 & (kSize - 1); }
+  // the token's place, or -1
+  __device__ int find(int32_t t, int64_t base, int64_t width, int64_t v) const {
+    if constexpr (DENSE) {
+      const int64_t u = (int64_t)t - base;
+      return u >= 0 && u < width ? (int)u : -1;
+    } else {
+      if (t < 0 || (int64_t)t >= v) return -1;
+      for (uint32_t s = hash(t);; s = (s + 1) & (kSize - 1)) {
+        const int32_t k = key[s];
+        if (k == t) return (int)s;
+        if (k == kFree) return -1;
+      }
     }
   }
-}
+  // the place of a token of the tile, taken if it has none yet
+  __device__ int take(int32_t t) {
+    for (uint32_t s = hash(t);; s = (s + 1) & (kSize - 1)) {
+      const int32_t k = atomicCAS(&key[s], kFree, t);
+      if (k == kFree || k == t) return (int)s;
+    }
+  }
+};
 
-template <bool DENSE>
+// G groups of 4 logits per thread: a tile is 1024 G.
+template <bool DENSE, int G>
 __global__ __launch_bounds__(kThreads) void k_rules(RulesArgs a) {
-  __shared__ Tables<DENSE> sh;
-  constexpr int kTile = DENSE ? kTileDense : kTileIds;
+  constexpr int kTile = 4 * G * kThreads, N = 4 * G;
+  typedef Tables<DENSE, kTile> Table;
+  static_assert((Table::kSize & (Table::kSize - 1)) == 0 && Table::kSize <= 65536, "the hash masks 16 bits");
+  __shared__ Table sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t b = blockIdx.y, base = (int64_t)blockIdx.x * kTile;
   const int64_t width = min((int64_t)kTile, a.n - base);
-  const int32_t* ids = DENSE ? nullptr : a.ids + b * a.ld_ids + base;
 
-  for (int i = tid; i < Tables<DENSE>::kSize; i += kThreads) {
-    sh.count[i] = 0u;
-    sh.bias[i] = 0.f;
-    if (!DENSE) sh.key[i] = kFree;
+  // this thread's logits 4 (tid + 256 j) .. + 3 of the tile and their ids
+  float z[N];
+  int32_t id[N];
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    const int64_t at = 4 * (tid + (int64_t)kThreads * j);
+    float v[4];
+    int32_t t[4];
+    load4<f32x4>(a.z + b * a.ld_z + base, at, width, -INFINITY, v);
+    if constexpr (!DENSE) load4<i32x4>(a.ids + b * a.ld_ids + base, at, width, (int32_t)-1, t);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      z[4 * j + e] = v[e];
+      id[4 * j + e] = DENSE ? (int32_t)(base + at + e) : t[e];
+    }
   }
-  __syncthreads();
-  if constexpr (!DENSE) {
-    for (int64_t i = tid; i < width; i += kThreads) {
-      const int32_t t = ids[i];
-      if (t < 0 || (int64_t)t >= a.v) continue;
-      uint32_t s = hash_id(t);
-      while (true) {  // at most kTileIds of the kSlots slots are taken
-        const int32_t k = atomicCAS(&sh.key[s], kFree, t);
-        if (k == kFree || k == t) break;
-        s = (s + 1) & (kSlots - 1);
-      }
+  bool open[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) open[i] = DENSE ? id[i] < a.n : id[i] >= 0 && (int64_t)id[i] < a.v;
+
+  // the row's mask, a word for four consecutive tokens of a dense row
+  const uint32_t* mask = nullptr;
+  if (a.mask) {
+    const int64_t r = a.mask_row ? (int64_t)a.mask_row[b] : b;
+    if (r >= 0 && r < a.mask_rows) mask = a.mask + r * a.ld_mask;
+  }
+  uint32_t allow[DENSE ? G : N];
+#pragma unroll
+  for (int i = 0; i < (DENSE ? G : N); ++i) {
+    const int e = DENSE ? 4 * i : i;
+    allow[i] = mask && open[e] ? mask[id[e] >> 5] >> (id[e] & 31) : 0xFFFFFFFFu;
+  }
+
+  int place[DENSE ? 1 : N];
+  if (a.history || a.bias_ids) {
+    for (int i = tid; i < Table::kSize; i += kThreads) {
+      sh.count[i] = 0u;
+      sh.bias[i] = 0.f;
+      if (!DENSE) sh.key[i] = kFree;
     }
     __syncthreads();
+    if constexpr (!DENSE) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) place[i] = open[i] ? sh.take(id[i]) : 0;
+      __syncthreads();
+    }
   }
   if (a.history) {
     int64_t nh = a.n_history ? (int64_t)a.n_history[b] : a.history_len;
     nh = min(max(nh, (int64_t)0), a.history_len);
     const int64_t np = a.n_prompt ? min(max((int64_t)a.n_prompt[b], (int64_t)0), nh) : 0;
     const int32_t* h = a.history + b * a.ld_history;
-    for (int64_t i = tid; i < nh; i += kThreads) {
-      const int p = place_of<DENSE>(sh, h[i], base, width, a.v);
-      if (p < 0) continue;
-      if (i < np)
-        atomicOr(&sh.count[p], kPrompt);
-      else
-        atomicAdd(&sh.count[p], 1u);
+    for (int64_t i = 4 * tid; i < nh; i += 4 * kThreads) {
+      int32_t t[4];
+      load4<i32x4>(h, i, nh, (int32_t)-1, t);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int p = sh.find(t[e], base, width, a.v);
+        if (p >= 0) {
+          if (i + e < np)
+            atomicOr(&sh.count[p], kPrompt);
+          else
+            atomicAdd(&sh.count[p], 1u);
+        }
+      }
     }
   }
   if (a.bias_ids) {
@@ -108,102 +159,116 @@ __global__ __launch_bounds__(kThreads) void k_rules(RulesArgs a) {
     for (int64_t i0 = 0; i0 < nb; i0 += kThreads) {
       const int64_t i = i0 + tid;
       const int m = (int)min((int64_t)kThreads, nb - i0);
-      __syncthreads();
-      sh.list_at[tid] = i < nb ? place_of<DENSE>(sh, a.bias_ids[b * a.ld_bias + i], base, width, a.v) : -1;
+      const int mine = i < nb ? sh.find(a.bias_ids[b * a.ld_bias + i], base, width, a.v) : -1;
+      __syncthreads();  // the list before is done with
+      sh.list_at[tid] = mine;
       sh.list_add[tid] = i < nb ? a.bias[b * a.ld_bias + i] : 0.f;
       __syncthreads();
-      for (int e = 0; e < m; ++e)
-        if (sh.list_at[e] >= 0 && (sh.list_at[e] & (kThreads - 1)) == tid) sh.bias[sh.list_at[e]] += sh.list_add[e];
+      if (mine >= 0) {
+        // the first entry of a place adds up the place's entries, in order
+        float sum = sh.bias[mine];
+        int first = tid;
+#pragma unroll 8
+        for (int e = 0; e < m; ++e) {
+          if (sh.list_at[e] == mine) {
+            first = min(first, e);
+            sum += sh.list_add[e];
+          }
+        }
+        if (first == tid) sh.bias[mine] = sum;
+      }
     }
   }
   __syncthreads();
 
-  const float rep = a.repetition ? a.repetition[b] : 1.f;
-  const float freq = a.frequency ? a.frequency[b] : 0.f;
-  const float pres = a.presence ? a.presence[b] : 0.f;
-  const uint32_t* mask = nullptr;
-  if (a.mask) {
-    const int64_t r = a.mask_row ? (int64_t)a.mask_row[b] : b;
-    if (r >= 0 && r < a.mask_rows) mask = a.mask + r * a.ld_mask;
+  if (a.history || a.bias_ids) {
+    const float rep = a.repetition ? a.repetition[b] : 1.f;
+    const float freq = a.frequency ? a.frequency[b] : 0.f;
+    const float pres = a.presence ? a.presence[b] : 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = DENSE ? 4 * (tid + kThreads * (i / 4)) + i % 4 : place[DENSE ? 0 : i];
+      const uint32_t c = sh.count[p];
+      if (c) {
+        z[i] = z[i] > 0.f ? z[i] / rep : z[i] * rep;
+        const uint32_t made = c & ~kPrompt;
+        z[i] -= freq * (float)made;
+        if (made) z[i] -= pres;
+      }
+      z[i] += sh.bias[p];
+    }
   }
-  const float* z = a.z + b * a.ld_z + base;
-  float* out = a.out ? a.out + b * a.ld_out + base : nullptr;
-  Part part = part_empty();
-  for (int64_t i0 = 4 * tid; i0 < width; i0 += 4 * kThreads) {
-    const int m = (int)min((int64_t)4, width - i0);
-    float x[4];
-    int32_t id[4];
-    if (m == 4) {
-      const f32x4u v = *reinterpret_cast<const f32x4u*>(z + i0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = v[e];
-    } else {
+  for (int i = 0; i < N; ++i) {
+    open[i] = open[i] && (DENSE ? allow[i / 4] >> (i % 4) : allow[i]) & 1u;
+    if (!open[i]) z[i] = -INFINITY;
+  }
+  if (a.out) {
+    float* out = a.out + b * a.ld_out + base;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = e < m ? z[i0 + e] : -INFINITY;
-    }
-    U4 words{0u, 0u, 0u, 0u};
-    if (DENSE && a.token_sample) words = philox_block(a.seed, (uint32_t)b, (uint32_t)((base + i0) >> 2), 1u);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (e >= m) break;
-      id[e] = DENSE ? (int32_t)(base + i0 + e) : ids[i0 + e];
-      bool open = DENSE || (id[e] >= 0 && (int64_t)id[e] < a.v);
-      if (open) {
-        const int p = DENSE ? (int)i0 + e : place_of<DENSE>(sh, id[e], base, width, a.v);
-        const uint32_t c = sh.count[p];
-        if (c) {
-          x[e] = x[e] > 0.f ? x[e] / rep : x[e] * rep;
-          const uint32_t made = c & ~kPrompt;
-          x[e] -= freq * (float)made;
-          if (made) x[e] -= pres;
-        }
-        x[e] += sh.bias[p];
-        if (mask) open = (mask[id[e] >> 5] >> (id[e] & 31)) & 1u;
-      }
-      if (!open) {
-        x[e] = -INFINITY;
-        id[e] = 0x7FFFFFFF;
-      }
-      if (a.parts) {
-        const float y = scaled_logit(x[e], a.tprime);
-        float key = x[e];
-        if (a.token_sample && open)
-          key = y + (DENSE ? gumbel_from_word(u4_word(words, e)) : gumbel_at(a.seed, (uint32_t)b, (uint32_t)id[e], 1u));
-        choice_key(part, key, x[e], id[e]);
-        choice_lse(part, y, 1.f);
-      }
-    }
-    if (out) {
-      if (m == 4)
-        *reinterpret_cast<f32x4u*>(out + i0) = f32x4u{x[0], x[1], x[2], x[3]};
+    for (int j = 0; j < G; ++j) {
+      const int64_t at = 4 * (tid + (int64_t)kThreads * j);
+      if (at + 4 <= width)
+        *reinterpret_cast<f32x4*>(out + at) = f32x4{z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]};
       else
-        for (int e = 0; e < m; ++e) out[i0 + e] = x[e];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (at + e < width) out[at + e] = z[4 * j + e];
     }
   }
   if (a.parts) {
-    part = wave_choice(part);
+    uint32_t word[N] = {};
+    if (a.token_sample) {
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        if constexpr (DENSE) {
+          const U4 w = token_words(a.seed, (uint32_t)b, (uint32_t)id[4 * j] >> 2);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) word[4 * j + e] = u4_word(w, e);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const U4 w = token_words(a.seed, (uint32_t)b, (uint32_t)id[4 * j + e] >> 2);
+            word[4 * j + e] = u4_word(w, id[4 * j + e] & 3);
+          }
+        }
+      }
+    }
+    Part part = wave_choice(choose<N>(z, id, open, a.token_sample != 0, a.tprime, word));
     if (lane == 0) sh.parts[wave] = part;
     __syncthreads();
     if (tid == 0) {
+#pragma unroll
       for (int w = 1; w < kThreads / 64; ++w) part = choice_merge(part, sh.parts[w]);
       a.parts[b * gridDim.x + blockIdx.x] = part;
     }
   }
 }
 
+// Groups per thread: four where that still leaves two workgroups per CU.
+int groups_of(int64_t B, int64_t n) { return B * ((n + 4095) / 4096) >= 512 ? 4 : 1; }
+
+template <bool DENSE>
+void launch(const RulesArgs& a, int64_t B, hipStream_t st) {
+  const dim3 grid((unsigned)rules_parts(B, a.n), (unsigned)B), block(kThreads);
+  if (groups_of(B, a.n) == 4)
+    hipLaunchKernelGGL((k_rules<DENSE, 4>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((k_rules<DENSE, 1>), grid, block, 0, st, a);
+}
+
 }  // namespace
 
-int64_t rules_parts(int64_t, int64_t n, bool dense) {
-  const int tile = dense ? kTileDense : kTileIds;
+int64_t rules_parts(int64_t B, int64_t n) {
+  const int tile = 4 * kThreads * groups_of(B, n);
   return (n + tile - 1) / tile;
 }
 
 hipError_t launch_rules(const RulesArgs& a, int64_t B, hipStream_t st) {
-  const dim3 grid((unsigned)rules_parts(B, a.n, !a.ids), (unsigned)B), block(kThreads);
   if (a.ids)
-    hipLaunchKernelGGL((k_rules<false>), grid, block, 0, st, a);
+    launch<false>(a, B, st);
   else
-    hipLaunchKernelGGL((k_rules<true>), grid, block, 0, st, a);
+    launch<true>(a, B, st);
   return hipGetLastError();
 }
 

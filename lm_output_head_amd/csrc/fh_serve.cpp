@@ -146,7 +146,7 @@ fh_status check_product(const fh_w8a8* w, const int8_t* q, int64_t ld_q, const f
 // q's rows where the kernel can read them, in fields q and ld_q of a.
 hipError_t take_rows(const fh_w8a8* w, const int8_t* q, int64_t ld_q, int64_t B, void* workspace, hipStream_t st,
                      fh::W8A8Args* a) {
-  a->W = static_cast<const uint4*>(w->packed);
+  a->W = w->packed;
   a->ws = w->scales;
   a->n = w->n;
   a->k = (int)w->k;
@@ -320,8 +320,7 @@ int64_t fh_logits_workspace(int64_t B, int64_t n) {
   return guarded<int64_t>(FH_ENOMEM, [&]() -> int64_t {
     if (B < 1 || B > 65535) return fail(FH_EINVAL, "B outside [1, 65535]");
     if (n < 1 || n > kMaxWidth) return fail(FH_EINVAL, "n outside [1, 2^30]");
-    const int64_t parts = std::max(fh::rules_parts(B, n, true), fh::rules_parts(B, n, false));
-    return (int64_t)sizeof(fh::Part) * B * parts;
+    return (int64_t)sizeof(fh::Part) * B * fh::rules_parts(B, n);
   });
 }
 
@@ -409,7 +408,7 @@ fh_status fh_logits_apply(const float* logits, int64_t ld_logits, const int32_t*
     hipStream_t st = static_cast<hipStream_t>(stream);
     hipError_t r = fh::launch_rules(a, B, st);
     if (r == hipSuccess && choice)
-      r = fh::launch_choice(a.parts, B, fh::rules_parts(B, n, !ids), out_token, out_token_logit, out_lse, st);
+      r = fh::launch_choice(a.parts, B, fh::rules_parts(B, n), out_token, out_token_logit, out_lse, st);
     return r == hipSuccess ? FH_OK : hip_fail(r, "logit rules launch");
   });
 }

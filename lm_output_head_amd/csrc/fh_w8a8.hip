@@ -18,105 +18,323 @@ namespace fh {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint16_t u16x4u __attribute__((ext_vector_type(4), aligned(2)));
 
-__device__ __forceinline__ i32x4 mfma_i8(const uint4& a, const uint4& b, i32x4 c) {
-  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+// Steps of 64 elements in a row of W: a multiple of kStepPad, zero past k.
+constexpr int kStepPad = 2;
+__host__ __device__ constexpr int w_steps(int64_t k) {
+  return (int)((k + 64 * kStepPad - 1) / (64 * kStepPad) * kStepPad);
 }
 
-__device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+__device__ __forceinline__ i32x4 mfma_i8(i32x4 a, i32x4 b, i32x4 c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
 
-// Four results of one token at channels j .. j + 3, those below n.
-__device__ __forceinline__ void store4(const W8A8Args& a, bool bf16, int64_t q, int64_t j, const float (&z)[4]) {
-  if (bf16) {
-    uint16_t* o = static_cast<uint16_t*>(a.out) + q * a.ld_out + j;
-    if (j + 3 < a.n)
-      *reinterpret_cast<u16x4u*>(o) = u16x4u{bf16_bits(z[0]), bf16_bits(z[1]), bf16_bits(z[2]), bf16_bits(z[3])};
+// N results of one token from channel j up, those below n, in 16 (or 8) bytes.
+// STREAM: past the caches, which the operands need (64 x 151936 float results
+// beside 389 MB of weights: 95 -> 85 us; 4096 x 10240 bf16: 138 -> 128 us).
+template <typename T, int N, bool STREAM>
+__device__ __forceinline__ void store_run(T* o, int64_t j, int64_t n, const T* v) {
+  typedef T V __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+  if (j + N <= n) {
+    V x;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = v[i];
+    if (STREAM)
+      __builtin_nontemporal_store(x, reinterpret_cast<V*>(o + j));
     else
-      for (int i = 0; i < 4 && j + i < a.n; ++i) o[i] = bf16_bits(z[i]);
+      *reinterpret_cast<V*>(o + j) = x;
   } else {
-    float* o = static_cast<float*>(a.out) + q * a.ld_out + j;
-    if (j + 3 < a.n)
-      *reinterpret_cast<f32x4u*>(o) = f32x4u{z[0], z[1], z[2], z[3]};
-    else
-      for (int i = 0; i < 4 && j + i < a.n; ++i) o[i] = z[i];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (j + i < n) o[j + i] = v[i];
   }
+}
+
+template <bool BF16>
+struct Out {
+  typedef float T;
+  __device__ static float of(float z) { return z; }
+};
+template <>
+struct Out<true> {
+  typedef uint16_t T;
+  __device__ static uint16_t of(float z) { return __builtin_bit_cast(uint16_t, (__bf16)z); }
+};
+
+// The scales of a lane's rows 16 (t0 + m) + 4 g + i, zero past n.
+template <int FN>
+__device__ __forceinline__ void load_scales(const W8A8Args& a, int64_t t0, int g, float (&ws)[FN][4]) {
+#pragma unroll
+  for (int m = 0; m < FN; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t j = 16 * (t0 + m) + 4 * g + i;
+      ws[m][i] = j < a.n ? a.ws[j] : 0.f;
+    }
+}
+
+// A lane's 4 FN logits z[m][i] of row q, tokens 16 (t0 + m) + 4 g + i, as a Part.
+template <int FN>
+__device__ __forceinline__ Part choose_tile(const W8A8Args& a, const float (&z)[FN][4], int64_t q, int64_t t0, int g) {
+  float v[4 * FN];
+  int32_t id[4 * FN];
+  bool open[4 * FN];
+  uint32_t word[4 * FN];
+#pragma unroll
+  for (int m = 0; m < FN; ++m) {
+    const int64_t j = 16 * (t0 + m) + 4 * g;
+    U4 words{0u, 0u, 0u, 0u};
+    if (a.token_sample) words = token_words(a.seed, (uint32_t)q, (uint32_t)(j >> 2));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[4 * m + i] = z[m][i];
+      id[4 * m + i] = (int32_t)(j + i);
+      open[4 * m + i] = j + i < a.n;
+      word[4 * m + i] = u4_word(words, i);
+    }
+  }
+  return choose<4 * FN>(v, id, open, a.token_sample != 0, a.tprime, word);
 }
 
 constexpr int kWaves = 4;
 
-// NT token tiles and MT row tiles of 16 per wave.
-template <int NT, int MT, bool BF16, bool HEAD>
-__global__ __launch_bounds__(64 * kWaves) void k_w8a8(W8A8Args a) {
-  __shared__ Part sh[HEAD ? kWaves : 1][HEAD ? 16 * NT : 1];
+// Up to 16 tokens: each wave streams 16 FN rows of W, the tokens come from the
+// caches.
+template <int FN, bool BF16, bool HEAD>
+__global__ __launch_bounds__(64 * kWaves) void k_w8a8_few(W8A8Args a) {
+  __shared__ Part sh[HEAD ? kWaves : 1][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, col = lane & 15;
   const int64_t tiles = (a.n + 15) / 16;
-  const int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * MT;
-  const int q0 = blockIdx.y * 16 * NT;
-  const int steps = (a.k + 63) / 64, chunks = (a.k + 15) / 16;
+  const int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * FN;
+  const int steps = w_steps(a.k), chunks = (a.k + 15) / 16;
 
-  const uint4* wp[MT];
+  const i32x4* wp[FN];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) wp[m] = a.W + min(t0 + m, tiles - 1) * steps * 64 + lane;
-  const int8_t* qp[NT];
+  for (int m = 0; m < FN; ++m) wp[m] = static_cast<const i32x4*>(a.W) + min(t0 + m, tiles - 1) * steps * 64 + lane;
+  const int8_t* qp = a.q + (int64_t)min(col, a.B - 1) * a.ld_q;
+  i32x4 acc[FN][1];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) qp[t] = a.q + (int64_t)min(q0 + 16 * t + col, a.B - 1) * a.ld_q;
-
-  i32x4 acc[MT][NT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[m][t] = i32x4{0, 0, 0, 0};
+  for (int m = 0; m < FN; ++m) acc[m][0] = i32x4{0, 0, 0, 0};
   for (int s = 0; s < steps; ++s) {
     // a 16-byte chunk past the row stands in as its first: W is zero there
     const int ch = 4 * s + g < chunks ? 4 * s + g : 0;
-    uint4 wf[MT], qf[NT];
+    i32x4 wf[FN];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) wf[m] = wp[m][s * 64];
+    for (int m = 0; m < FN; ++m) wf[m] = wp[m][s * 64];
+    const i32x4 qf = *reinterpret_cast<const i32x4*>(qp + 16 * ch);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) qf[t] = *reinterpret_cast<const uint4*>(qp[t] + 16 * ch);
+    for (int m = 0; m < FN; ++m) acc[m][0] = mfma_i8(wf[m], qf, acc[m][0]);
+  }
+  typedef typename Out<BF16>::T T;
+  float ws[FN][4];
+  load_scales<FN>(a, t0, g, ws);
+  const float qs = col < a.B ? a.qs[col] : 0.f;
+  float z[FN][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < FN; ++m) {
+    const int64_t j = 16 * (t0 + m) + 4 * g;
+    T o[4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) acc[m][t] = mfma_i8(wf[m], qf[t], acc[m][t]);
+    for (int i = 0; i < 4; ++i) {
+      z[m][i] = (float)acc[m][0][i] * (qs * ws[m][i]);
+      o[i] = Out<BF16>::of(z[m][i]);
+    }
+    if (a.out && col < a.B) store_run<T, 4, false>(static_cast<T*>(a.out) + col * a.ld_out, j, a.n, o);
+  }
+  if (HEAD) {
+    const Part p = wave_choice<16>(choose_tile<FN>(a, z, col, t0, g));
+    if (g == 0) sh[wave][col] = p;
+    __syncthreads();
+    const int i = threadIdx.x;
+    if (i < a.B && i < 16) {
+      Part p = sh[0][i];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) p = choice_merge(p, sh[w][i]);
+      a.parts[(int64_t)i * gridDim.x + blockIdx.x] = p;
+    }
+  }
+}
+
+// Orders this workgroup's LDS accesses around a barrier; loads from memory stay
+// in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// More tokens: a workgroup of WN x WM waves covers 16 FN WN rows by 16 FT WM
+// tokens.  The tokens' block of kStage steps of k is staged in LDS in fragment
+// order (a fragment is read as one contiguous 1 KB), double buffered and loaded
+// one block ahead; each wave's rows of W go straight to registers (fragment
+// order, one contiguous 1 KB per load), two blocks ahead.  ONCE: the rows are
+// read by this workgroup alone and pass the caches by (128 x 128256 x 2048:
+// 65 -> 62 us; where token tiles share them it costs 10 to 20%).
+template <int FT, int FN, int WN, int WM, bool ONCE, bool BF16, bool HEAD>
+__global__ __launch_bounds__(64 * WN * WM) void k_w8a8_tile(W8A8Args a, int n_tiles, int q_tiles) {
+  constexpr int kStage = kStepPad, kW = WN * WM, kFrags = FT * WM * kStage;  // fragments of a token block
+  constexpr int kOwn = (kFrags + kW - 1) / kW;            // of them, this wave's to stage
+  constexpr int kBlock = kFrags * 64;
+  typedef typename Out<BF16>::T T;
+  // results of 16 tokens of each token group on their way out, two buffers
+  constexpr int kRow = 16 * FN * WN + 16 / (int)sizeof(T), kTurn = 16 * WM * kRow;
+  constexpr int kShared = 2 * kBlock * 16, kStaged = 2 * kTurn * (int)sizeof(T);
+  __shared__ __attribute__((aligned(16))) char smem[kShared > kStaged ? kShared : kStaged];
+  __shared__ Part sP[HEAD ? kW : 1][HEAD ? 16 * FT : 1];
+  i32x4* sQ = reinterpret_cast<i32x4*>(smem);
+
+  // workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles, token
+  // tiles fastest, so that its L2 keeps the rows of W that they share
+  const int total = n_tiles * q_tiles, per = (total + 7) / 8;
+  const int tile = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || tile >= total) return;
+  const int nt = tile / q_tiles, qt = tile % q_tiles;
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wn = wave % WN, wm = wave / WN;
+  const int g = lane >> 4, col = lane & 15;
+  const int64_t rows = (a.n + 15) / 16;
+  const int64_t t0 = ((int64_t)nt * WN + wn) * FN;
+  const int q0 = qt * 16 * FT * WM;
+  const int steps = w_steps(a.k), chunks = (a.k + 15) / 16, blocks = steps / kStage;
+
+  const i32x4* wp[FN];
+#pragma unroll
+  for (int m = 0; m < FN; ++m) wp[m] = static_cast<const i32x4*>(a.W) + min(t0 + m, rows - 1) * steps * 64 + lane;
+  // this wave's fragments of a block: f = step * FT WM + token tile
+  const int8_t* qp[kOwn];
+  int qs[kOwn];
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int f = min(wave + i * kW, kFrags - 1);
+    // a token past the last stands in as the last, its results are dropped
+    qp[i] = a.q + (int64_t)min(q0 + 16 * (f % (FT * WM)) + col, a.B - 1) * a.ld_q;
+    qs[i] = f / (FT * WM);
+  }
+  i32x4 qr[kOwn];
+  auto load_q = [&](int blk) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      // a 16-byte chunk past the row stands in as its first: W is zero there
+      const int c = 4 * (kStage * blk + qs[i]) + g;
+      qr[i] = *reinterpret_cast<const i32x4*>(qp[i] + 16 * (c < chunks ? c : 0));
+    }
+  };
+  auto store_q = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      if (kFrags % kW == 0 || wave + i * kW < kFrags) sQ[buf * kBlock + (wave + i * kW) * 64 + lane] = qr[i];
+  };
+  i32x4 wf[2][kStage][FN];
+  auto load_w = [&](int blk, i32x4 (&dst)[kStage][FN]) {
+#pragma unroll
+    for (int s = 0; s < kStage; ++s)
+#pragma unroll
+      for (int m = 0; m < FN; ++m) {
+        const i32x4* p = wp[m] + (int64_t)min(kStage * blk + s, steps - 1) * 64;
+        dst[s][m] = ONCE ? __builtin_nontemporal_load(p) : *p;
+      }
+  };
+  i32x4 acc[FN][FT];
+#pragma unroll
+  for (int m = 0; m < FN; ++m)
+#pragma unroll
+    for (int t = 0; t < FT; ++t) acc[m][t] = i32x4{0, 0, 0, 0};
+  auto multiply = [&](int buf, const i32x4 (&w)[kStage][FN]) {
+#pragma unroll
+    for (int s = 0; s < kStage; ++s) {
+      i32x4 qf[FT];
+#pragma unroll
+      for (int t = 0; t < FT; ++t) qf[t] = sQ[buf * kBlock + ((s * WM + wm) * FT + t) * 64 + lane];
+#pragma unroll
+      for (int t = 0; t < FT; ++t)
+#pragma unroll
+        for (int m = 0; m < FN; ++m) acc[m][t] = mfma_i8(w[s][m], qf[t], acc[m][t]);
+    }
+  };
+
+  // The compiler would move the loads down to the stores that take them.
+  auto stay = []() { __builtin_amdgcn_sched_barrier(0); };
+  // Block blk is multiplied from buffer blk % 2 while block blk + 1 travels to
+  // registers; it is stored into the other buffer, which every wave has left
+  // since the barrier before.  Loads past the last block repeat its last step.
+  load_q(0);
+  load_w(0, wf[0]);
+  load_w(1, wf[1]);
+  store_q(0);
+  lds_barrier();
+  for (int blk = 0; blk < blocks; blk += 2) {
+    load_q(blk + 1);
+    stay();
+    multiply(0, wf[0]);
+    stay();
+    load_w(blk + 2, wf[0]);
+    stay();
+    store_q(1);
+    lds_barrier();
+    if (blk + 1 < blocks) {
+      load_q(blk + 2);
+      stay();
+      multiply(1, wf[1]);
+      stay();
+      load_w(blk + 3, wf[1]);
+      stay();
+      store_q(0);
+      lds_barrier();
+    }
   }
 
+  // Every wave is past its last read of the blocks.  16 tokens at a time the
+  // results go through LDS, so that a wave writes runs of whole rows (64 bytes
+  // per token straight from the accumulators cost 22 us of 96 at 64 x 151936 and
+  // 49 us of 187 at 4096 x 10240).
+  float ws[FN][4];
+  load_scales<FN>(a, t0, g, ws);
+  T* turn = reinterpret_cast<T*>(smem);
+  const int qw = q0 + 16 * FT * wm;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int64_t q = q0 + 16 * t + col;
-    const float qs = q < a.B ? a.qs[q] : 0.f;
-    Part p = part_empty();
+  for (int t = 0; t < FT; ++t) {
+    const int64_t q = qw + 16 * t + col;
+    const float qsc = q < a.B ? a.qs[q] : 0.f;
+    T* row = turn + (t & 1) * kTurn + (16 * wm + col) * kRow + 16 * FN * wn + 4 * g;
+    float z[FN][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int64_t j = 16 * (t0 + m) + 4 * g;
-      float z[4];
+    for (int m = 0; m < FN; ++m) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        z[i] = j + i < a.n ? (float)acc[m][t][i] * (qs * a.ws[j + i]) : 0.f;
-        if (HEAD && j + i < a.n) {
-          const float x = scaled_logit(z[i], a.tprime);
-          const int32_t id = (int32_t)(j + i);
-          choice_key(p, a.token_sample ? x + gumbel_at(a.seed, (uint32_t)q, (uint32_t)id, 1u) : z[i], z[i], id);
-          choice_lse(p, x, 1.f);
-        }
-      }
-      if (a.out && q < a.B && j < a.n) store4(a, BF16, q, j, z);
+      for (int i = 0; i < 4; ++i) z[m][i] = (float)acc[m][t][i] * (qsc * ws[m][i]);
+      typedef T V __attribute__((ext_vector_type(4)));
+      V o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = Out<BF16>::of(z[m][i]);
+      if (a.out) *reinterpret_cast<V*>(row + 16 * m) = o;
     }
     if (HEAD) {
-      p = wave_choice<16>(p);
-      if (g == 0) sh[wave][16 * t + col] = p;
+      const Part p = wave_choice<16>(choose_tile<FN>(a, z, q, t0, g));
+      if (g == 0) sP[wave][16 * t + col] = p;
+    }
+    if (a.out) {
+      lds_barrier();  // the other buffer is read until the barrier after this one
+      constexpr int kPer = 16 / (int)sizeof(T), kRuns = 16 * FN * WN / kPer;  // 16-byte runs of a token
+#pragma unroll
+      for (int c = 64 * wn + lane; c < 16 * kRuns; c += 64 * WN) {
+        const int tok = c / kRuns, at = c % kRuns * kPer;
+        const int64_t b = qw + 16 * t + tok;
+        if (b < a.B)
+          store_run<T, kPer, true>(static_cast<T*>(a.out) + b * a.ld_out, (int64_t)nt * (16 * FN * WN) + at, a.n,
+                             turn + (t & 1) * kTurn + (16 * wm + tok) * kRow + at);
+      }
     }
   }
   if (HEAD) {
     __syncthreads();
-    const int i = threadIdx.x;
-    if (i < 16 * NT && q0 + i < a.B) {
-      Part p = sh[0][i];
+    for (int i = tid; i < 16 * FT * WM; i += 64 * kW) {
+      const int m = i / (16 * FT), c = i % (16 * FT);
+      if (q0 + i >= a.B) break;
+      Part p = sP[m * WN][c];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) p = choice_merge(p, sh[w][i]);
-      a.parts[(int64_t)(q0 + i) * gridDim.x + blockIdx.x] = p;
+      for (int w = 1; w < WN; ++w) p = choice_merge(p, sP[m * WN + w][c]);
+      a.parts[(int64_t)(q0 + i) * n_tiles + nt] = p;
     }
   }
 }
@@ -150,7 +368,7 @@ __global__ __launch_bounds__(256) void k_w8a8_scales(const void* W, int64_t n, i
 template <typename T>
 __global__ __launch_bounds__(256) void k_w8a8_pack(const int8_t* codes, const void* W, const float* scales, int64_t n,
                                                    int64_t k, int64_t chunks, uint4* out) {
-  const int64_t steps = (k + 63) / 64;
+  const int64_t steps = w_steps(k);
   for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < chunks; c += (int64_t)gridDim.x * 256) {
     const int lane = (int)(c & 63);
     const int64_t s = (c >> 6) % steps, j = (c >> 6) / steps * 16 + (lane & 15), i0 = s * 64 + (lane >> 4) * 16;
@@ -173,7 +391,7 @@ __global__ __launch_bounds__(256) void k_w8a8_pack(const int8_t* codes, const vo
 }
 
 __global__ __launch_bounds__(256) void k_w8a8_unpack(const int8_t* packed, int64_t n, int64_t k, int8_t* codes) {
-  const int64_t steps = (k + 63) / 64;
+  const int64_t steps = w_steps(k);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n * k; i += (int64_t)gridDim.x * 256) {
     const int64_t j = i / k, e = i % k;
     const int64_t lane = (j & 15) + 16 * ((e & 63) >> 4);
@@ -189,44 +407,107 @@ __global__ __launch_bounds__(256) void k_w8a8_align(const int8_t* q, int64_t ld_
   }
 }
 
-__global__ __launch_bounds__(64) void k_choice(const Part* parts, int64_t nparts, int32_t* out_token, float* out_logit,
-                                               float* out_lse) {
+// The choice over a row's parts, 8 per thread at a time: their loads together,
+// the largest m first, then every part's sum relative to it.
+constexpr int kChoice = 256, kChoiceN = 8;
+__global__ __launch_bounds__(kChoice) void k_choice(const Part* parts, int64_t nparts, int32_t* out_token,
+                                                    float* out_logit, float* out_lse) {
+  __shared__ Part sh[kChoice / 64];
   const int64_t q = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const Part* row = parts + q * nparts;
   Part p = part_empty();
-  for (int64_t i = threadIdx.x; i < nparts; i += 64) p = choice_merge(p, parts[q * nparts + i]);
+  for (int64_t i0 = threadIdx.x; i0 < nparts; i0 += kChoice * kChoiceN) {
+    Part v[kChoiceN];
+#pragma unroll
+    for (int i = 0; i < kChoiceN; ++i) v[i] = row[min(i0 + i * kChoice, nparts - 1)];
+    float m = p.m, s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kChoiceN; ++i) {
+      if (i0 + i * kChoice >= nparts) v[i] = part_empty();
+      choice_key(p, v[i].key, v[i].z, v[i].id);
+      m = fmaxf(m, v[i].m);
+    }
+#pragma unroll
+    for (int i = 0; i < kChoiceN; ++i) s += v[i].s * exp_from(v[i].m, m);
+    p.s = p.s * exp_from(p.m, m) + s;
+    p.m = m;
+  }
   p = wave_choice(p);
-  if (threadIdx.x == 0) write_choice(p, q, out_token, out_logit, out_lse);
+  if (lane == 0) sh[wave] = p;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < kChoice / 64; ++w) p = choice_merge(p, sh[w]);
+    write_choice(p, q, out_token, out_logit, out_lse);
+  }
 }
 
 unsigned grid_of(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20); }
 
-int token_tiles(int64_t B) { return B <= 16 ? 1 : B <= 32 ? 2 : 4; }
-constexpr int kMT = 2;
+constexpr int kFewFN = 2;
 
-template <int NT>
-hipError_t launch_nt(const W8A8Args& a, bool out_bf16, bool head, hipStream_t st) {
-  const dim3 grid((unsigned)w8a8_parts(a.n, a.B), (unsigned)((a.B + 16 * NT - 1) / (16 * NT))), block(64 * kWaves);
-  if (head)
-    hipLaunchKernelGGL((k_w8a8<NT, kMT, false, true>), grid, block, 0, st, a);
-  else if (out_bf16)
-    hipLaunchKernelGGL((k_w8a8<NT, kMT, true, false>), grid, block, 0, st, a);
+// The tile of a call: rows and tokens of a workgroup.  The largest one that
+// leaves a workgroup for every CU and less than half its tokens empty; the head's
+// choice does not fit the registers beside the sums of k256.
+enum Tile { kFew, k32, k64, k128, k256 };
+constexpr int kTileRows[] = {16 * kFewFN * kWaves, 128, 128, 256, 256};
+constexpr int kTileTokens[] = {16, 32, 64, 128, 256};
+int64_t tiles_of(Tile t, int64_t n, int64_t B) {
+  return (n + kTileRows[t] - 1) / kTileRows[t] * ((B + kTileTokens[t] - 1) / kTileTokens[t]);
+}
+Tile tile_of(int64_t n, int64_t B, bool head) {
+  if (B <= 16) return kFew;
+  for (Tile t : {k256, k128, k64})
+    if (!(head && t == k256) && 2 * B > kTileTokens[t] && tiles_of(t, n, B) >= 256) return t;
+  return k32;
+}
+
+template <int FT, int FN, int WN, int WM, bool BF16, bool HEAD>
+void launch_tile(const W8A8Args& a, hipStream_t st) {
+  constexpr int kRows = 16 * FN * WN, kTokens = 16 * FT * WM;
+  const int nt = (int)((a.n + kRows - 1) / kRows), qt = (a.B + kTokens - 1) / kTokens;
+  const dim3 grid((unsigned)(((int64_t)nt * qt + 7) / 8 * 8)), block(64 * WN * WM);
+  if (qt == 1)
+    hipLaunchKernelGGL((k_w8a8_tile<FT, FN, WN, WM, true, BF16, HEAD>), grid, block, 0, st, a, nt, qt);
   else
-    hipLaunchKernelGGL((k_w8a8<NT, kMT, false, false>), grid, block, 0, st, a);
-  return hipGetLastError();
+    hipLaunchKernelGGL((k_w8a8_tile<FT, FN, WN, WM, false, BF16, HEAD>), grid, block, 0, st, a, nt, qt);
+}
+
+template <bool BF16, bool HEAD>
+void launch_kind(const W8A8Args& a, hipStream_t st) {
+  switch (tile_of(a.n, a.B, HEAD)) {
+    case kFew:
+      hipLaunchKernelGGL((k_w8a8_few<kFewFN, BF16, HEAD>), dim3((unsigned)tiles_of(kFew, a.n, 1)), dim3(64 * kWaves),
+                         0, st, a);
+      return;
+    case k32: return launch_tile<2, 2, 4, 1, BF16, HEAD>(a, st);
+    case k64: return launch_tile<4, 2, 4, 1, BF16, HEAD>(a, st);
+    case k128: return launch_tile<8, 2, 8, 1, BF16, HEAD>(a, st);
+    case k256:
+      if constexpr (!HEAD) launch_tile<8, 4, 4, 2, BF16, HEAD>(a, st);
+  }
 }
 
 }  // namespace
 
-int64_t w8a8_packed_bytes(int64_t n, int64_t k) { return (n + 15) / 16 * ((k + 63) / 64) * 1024; }
+int64_t w8a8_packed_bytes(int64_t n, int64_t k) { return (n + 15) / 16 * w_steps(k) * 1024; }
 
-int64_t w8a8_parts(int64_t n, int64_t) { return (n + 16 * kMT * kWaves - 1) / (16 * kMT * kWaves); }
+int64_t w8a8_parts(int64_t n, int64_t B) {
+  const int rows = kTileRows[tile_of(n, B, true)];
+  return (n + rows - 1) / rows;
+}
 
 hipError_t launch_w8a8(const W8A8Args& a, bool out_bf16, bool head, hipStream_t st) {
-  switch (token_tiles(a.B)) {
-    case 1: return launch_nt<1>(a, out_bf16, head, st);
-    case 2: return launch_nt<2>(a, out_bf16, head, st);
-    default: return launch_nt<4>(a, out_bf16, head, st);
-  }
+  // tiles are numbered in 32 bits
+  if (tiles_of(tile_of(a.n, a.B, head), a.n, a.B) >= (int64_t(1) << 30)) return hipErrorInvalidValue;
+  if (head)
+    launch_kind<false, true>(a, st);
+  else if (out_bf16)
+    launch_kind<true, false>(a, st);
+  else
+    launch_kind<false, false>(a, st);
+  return hipGetLastError();
 }
 
 hipError_t launch_w8a8_scales(const void* W, bool bf16, int64_t n, int64_t k, float* scales, int* bad, hipStream_t st) {
@@ -264,7 +545,7 @@ hipError_t launch_w8a8_align(const int8_t* q, int64_t ld_q, int64_t B, int64_t k
 
 hipError_t launch_choice(const Part* parts, int64_t B, int64_t nparts, int32_t* out_token, float* out_logit,
                          float* out_lse, hipStream_t st) {
-  hipLaunchKernelGGL(k_choice, dim3((unsigned)B), dim3(64), 0, st, parts, nparts, out_token, out_logit, out_lse);
+  hipLaunchKernelGGL(k_choice, dim3((unsigned)B), dim3(kChoice), 0, st, parts, nparts, out_token, out_logit, out_lse);
   return hipGetLastError();
 }
 
