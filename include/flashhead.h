@@ -526,7 +526,8 @@ fh_status fh_w8a8_forward(const fh_w8a8* w, const int8_t* q, int64_t ld_q, const
 /*
  * fh_logit_rules — what a server lays on the logits of each row before it
  * chooses a token.  All pointers are device memory; a NULL one leaves its rule
- * out.  Token ids outside [0, v) in history and bias_ids are skipped.
+ * out; penalties without a history do nothing.  Token ids outside [0, v) in
+ * history and bias_ids are skipped.
  */
 typedef struct {
   const int32_t* history;     /* [B x history_len] token ids, row stride ld_history */

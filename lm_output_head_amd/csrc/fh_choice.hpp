@@ -112,17 +112,61 @@ __device__ __forceinline__ Part choose(const float (&z)[N], const int32_t (&id)[
   return p;
 }
 
-__device__ __forceinline__ Part shfl_part(const Part& p, int mask) {
-  return Part{__shfl_xor(p.key, mask), __shfl_xor(p.z, mask), __shfl_xor(p.m, mask),
-              __shfl_xor(p.s, mask), __shfl_xor(p.id, mask)};
+// The two values that lanes l and l ^ SPAN hold (SPAN 16 or 32), in one
+// instruction and in one order for both lanes.
+template <int SPAN>
+__device__ __forceinline__ void pair(uint32_t x, uint32_t* lo, uint32_t* hi) {
+  static_assert(SPAN == 16 || SPAN == 32, "rows or halves of a wave");
+  if constexpr (SPAN == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    *lo = r[0];
+    *hi = r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    *lo = r[0];
+    *hi = r[1];
+  }
 }
 
-// Merge the lanes of a wave whose numbers differ in the bits from LO up.
-template <int LO = 1>
-__device__ __forceinline__ Part wave_choice(Part p) {
+template <int SPAN>
+__device__ __forceinline__ Part merge_pair(const Part& p) {
+  uint32_t lo[5], hi[5];
+  const uint32_t v[5] = {__float_as_uint(p.key), __float_as_uint(p.z), __float_as_uint(p.m),
+                         __float_as_uint(p.s), (uint32_t)p.id};
 #pragma unroll
-  for (int mask = LO; mask < 64; mask <<= 1) p = choice_merge(p, shfl_part(p, mask));
-  return p;
+  for (int i = 0; i < 5; ++i) pair<SPAN>(v[i], &lo[i], &hi[i]);
+  return choice_merge(
+      Part{__uint_as_float(lo[0]), __uint_as_float(lo[1]), __uint_as_float(lo[2]), __uint_as_float(lo[3]), (int32_t)lo[4]},
+      Part{__uint_as_float(hi[0]), __uint_as_float(hi[1]), __uint_as_float(hi[2]), __uint_as_float(hi[3]), (int32_t)hi[4]});
+}
+
+// The four lanes l % 16 of a wave merged; every one gets the result.
+__device__ __forceinline__ Part column_choice(const Part& p) { return merge_pair<32>(merge_pair<16>(p)); }
+
+// All lanes of a wave merged, uniform: the largest m, then one exponential per
+// lane; the largest key, then the lane that holds it.
+__device__ __forceinline__ Part wave_choice(const Part& p) {
+  Part r = part_empty();
+  r.m = wave_max(p.m);
+  r.s = wave_sum(p.s * exp_from(p.m, r.m));
+  const float key = wave_max(p.key);
+  if (key == -INFINITY) return r;
+  uint64_t who = __ballot(p.key == key);
+  if (who & (who - 1)) {  // a tie: the smallest id of those lanes
+    int32_t id = p.key == key ? p.id : 0x7FFFFFFF;
+    id = min(id, dpp_i<0xB1>(id));
+    id = min(id, dpp_i<0x4E>(id));
+    id = min(id, dpp_i<0x141>(id));
+    id = min(id, dpp_i<0x140>(id));
+    id = min(min(__builtin_amdgcn_readlane(id, 0), __builtin_amdgcn_readlane(id, 16)),
+             min(__builtin_amdgcn_readlane(id, 32), __builtin_amdgcn_readlane(id, 48)));
+    who = __ballot(p.key == key && p.id == id);
+  }
+  const int lane = __ffsll((unsigned long long)who) - 1;
+  r.key = key;
+  r.z = readlane_f(p.z, lane);
+  r.id = __builtin_amdgcn_readlane(p.id, lane);
+  return r;
 }
 
 __device__ __forceinline__ void write_choice(const Part& r, int64_t q, int32_t* out_token,

@@ -279,7 +279,7 @@ struct RulesArgs {
   int64_t ld_out;
   Part* parts;           // [B x rules_parts], or null: no choice
 };
-int64_t rules_parts(int64_t B, int64_t n);
+int64_t rules_parts(int64_t B, int64_t n, bool dense);  // partials per row
 hipError_t launch_rules(const RulesArgs& a, int64_t B, hipStream_t st);
 // the choice over each row's parts (w8a8 head, rules)
 hipError_t launch_choice(const Part* parts, int64_t B, int64_t nparts, int32_t* out_token,

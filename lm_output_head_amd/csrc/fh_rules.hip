@@ -2,11 +2,11 @@
 // repeated tokens, biases, grammar masks; then the choice (argmax or a
 // Gumbel-max draw, log-sum-exp) over the row.
 //
-// A workgroup owns one tile of one row and keeps a table of its tokens in LDS:
-// a word with the token's count in the output and, in bit 31, whether it is in
-// the prompt, and the sum of its biases.  The tile's logits travel to registers
-// while the workgroup walks the row's whole history and bias list and adds what
-// falls into its tile.  Dense rows index the table by token; rows of listed
+// A workgroup owns one tile of one row and keeps a table of its tokens in LDS: a
+// word with the token's count in the output and, in bit 31, whether it is in the
+// prompt.  The tile's logits travel to registers while the workgroup walks the
+// row's whole history and adds what falls into its tile; biases are added in a
+// second turn of the table.  Dense rows index the table by token; rows of listed
 // candidates through a hash of their ids.  Counts are integer sums, and one
 // thread adds all biases of a token in the list's order, so results do not
 // depend on the order of execution.
@@ -19,46 +19,66 @@
 namespace fh {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr uint32_t kPrompt = 0x80000000u;
 constexpr int32_t kFree = -1;
+constexpr int kAhead = 4;  // groups of four history ids that a thread loads at once
 
 typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef int32_t i32x4a __attribute__((ext_vector_type(4)));
 
-// Four consecutive elements at i, those below n; `other` in the places past it.
-template <typename V, typename T>
-__device__ __forceinline__ void load4(const T* p, int64_t i, int64_t n, T other, T (&v)[4]) {
-  if (i + 4 <= n) {
+// W (1 or 4) consecutive elements at i, those below n; `other` past it.
+template <int W, typename V, typename T>
+__device__ __forceinline__ void load_run(const T* p, int64_t i, int64_t n, T other, T (&v)[W]) {
+  if (W == 4 && i + 4 <= n) {
     const V x = *reinterpret_cast<const V*>(p + i);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = x[e];
+    for (int e = 0; e < W; ++e) v[e] = x[e];
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = i + e < n ? p[i + e] : other;
+    for (int e = 0; e < W; ++e) v[e] = i + e < n ? p[i + e] : other;
   }
 }
 
-// DENSE: a table word per token of the tile.  Else a hash of twice the tile's
-// size, so that at most half of its slots are taken and every search ends.
-template <bool DENSE, int TILE>
+// DENSE: a word per token of the tile, its count and later its logit.  Else a
+// hash of twice the tile's size, so that at most half of its slots are taken and
+// every search ends, behind a bitmap of the ids' low bits that turns most of the
+// history away at its first read.
+template <bool DENSE, int TILE, int TH>
 struct Tables {
   static constexpr int kSize = DENSE ? TILE : 2 * TILE;
-  uint32_t count[kSize];
-  float bias[kSize];
-  int32_t key[DENSE ? 1 : kSize];
-  int list_at[kThreads];
-  float list_add[kThreads];
-  Part parts[kThreads / 64];
+  static constexpr int kBits = 32768;
+  alignas(16) uint32_t count[kSize];
+  alignas(16) float bias[DENSE ? 4 : kSize];
+  alignas(16) int32_t key[DENSE ? 4 : kSize];
+  alignas(16) uint32_t maybe[DENSE ? 4 : kBits / 32];
+  // a list's entries that fall into the tile, by wave, in order
+  int listed[TH / 64];
+  int list_at[TH];
+  float list_add[TH];
+  Part parts[TH / 64];
 
+  __device__ void clear(int tid) {
+    const i32x4a zero{0, 0, 0, 0};
+    for (int i = 4 * tid; i < kSize; i += 4 * TH) {
+      *reinterpret_cast<i32x4a*>(&count[i]) = zero;
+      if constexpr (!DENSE) {
+        *reinterpret_cast<i32x4a*>(&bias[i]) = zero;
+        *reinterpret_cast<i32x4a*>(&key[i]) = i32x4a{kFree, kFree, kFree, kFree};
+      }
+    }
+    if constexpr (!DENSE)
+      for (int i = 4 * tid; i < kBits / 32; i += 4 * TH) *reinterpret_cast<i32x4a*>(&maybe[i]) = zero;
+  }
   __device__ static uint32_t hash(int32_t id) { return ((uint32_t)id * 0x9E3779B1u) >> 16 & (kSize - 1); }
   // the token's place, or -1
   __device__ int find(int32_t t, int64_t base, int64_t width, int64_t v) const {
     if constexpr (DENSE) {
-      const int64_t u = (int64_t)t - base;
-      return u >= 0 && u < width ? (int)u : -1;
+      const uint32_t u = (uint32_t)t - (uint32_t)base;  // past width too where t is below base
+      return u < (uint32_t)width ? (int)u : -1;
     } else {
       if (t < 0 || (int64_t)t >= v) return -1;
+      if (!(maybe[(t & (kBits - 1)) >> 5] >> (t & 31) & 1u)) return -1;
       for (uint32_t s = hash(t);; s = (s + 1) & (kSize - 1)) {
         const int32_t k = key[s];
         if (k == t) return (int)s;
@@ -68,6 +88,7 @@ struct Tables {
   }
   // the place of a token of the tile, taken if it has none yet
   __device__ int take(int32_t t) {
+    atomicOr(&maybe[(t & (kBits - 1)) >> 5], 1u << (t & 31));
     for (uint32_t s = hash(t);; s = (s + 1) & (kSize - 1)) {
       const int32_t k = atomicCAS(&key[s], kFree, t);
       if (k == kFree || k == t) return (int)s;
@@ -75,31 +96,32 @@ struct Tables {
   }
 };
 
-// G groups of 4 logits per thread: a tile is 1024 G.
-template <bool DENSE, int G>
-__global__ __launch_bounds__(kThreads) void k_rules(RulesArgs a) {
-  constexpr int kTile = 4 * G * kThreads, N = 4 * G;
-  typedef Tables<DENSE, kTile> Table;
+// G runs of W consecutive logits per thread: a tile is TH W G.
+template <bool DENSE, int TH, int W, int G>
+__global__ __launch_bounds__(TH) void k_rules(RulesArgs a) {
+  constexpr int kTile = TH * W * G, N = W * G;
+  typedef Tables<DENSE, kTile, TH> Table;
   static_assert((Table::kSize & (Table::kSize - 1)) == 0 && Table::kSize <= 65536, "the hash masks 16 bits");
+  static_assert(!DENSE || W == 4, "a Philox block and a mask word serve four tokens of a dense row");
   __shared__ Table sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t b = blockIdx.y, base = (int64_t)blockIdx.x * kTile;
   const int64_t width = min((int64_t)kTile, a.n - base);
 
-  // this thread's logits 4 (tid + 256 j) .. + 3 of the tile and their ids
+  // this thread's logits W (tid + TH j) .. + W - 1 of the tile and their ids
   float z[N];
   int32_t id[N];
 #pragma unroll
   for (int j = 0; j < G; ++j) {
-    const int64_t at = 4 * (tid + (int64_t)kThreads * j);
-    float v[4];
-    int32_t t[4];
-    load4<f32x4>(a.z + b * a.ld_z + base, at, width, -INFINITY, v);
-    if constexpr (!DENSE) load4<i32x4>(a.ids + b * a.ld_ids + base, at, width, (int32_t)-1, t);
+    const int64_t at = W * (tid + (int64_t)TH * j);
+    float v[W];
+    int32_t t[W];
+    load_run<W, f32x4>(a.z + b * a.ld_z + base, at, width, -INFINITY, v);
+    if constexpr (!DENSE) load_run<W, i32x4>(a.ids + b * a.ld_ids + base, at, width, (int32_t)-1, t);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      z[4 * j + e] = v[e];
-      id[4 * j + e] = DENSE ? (int32_t)(base + at + e) : t[e];
+    for (int e = 0; e < W; ++e) {
+      z[W * j + e] = v[e];
+      id[W * j + e] = DENSE ? (int32_t)(base + at + e) : t[e];
     }
   }
   bool open[N];
@@ -115,160 +137,191 @@ __global__ __launch_bounds__(kThreads) void k_rules(RulesArgs a) {
   uint32_t allow[DENSE ? G : N];
 #pragma unroll
   for (int i = 0; i < (DENSE ? G : N); ++i) {
-    const int e = DENSE ? 4 * i : i;
+    const int e = DENSE ? W * i : i;
     allow[i] = mask && open[e] ? mask[id[e] >> 5] >> (id[e] & 31) : 0xFFFFFFFFu;
   }
 
-  int place[DENSE ? 1 : N];
-  if (a.history || a.bias_ids) {
-    for (int i = tid; i < Table::kSize; i += kThreads) {
-      sh.count[i] = 0u;
-      sh.bias[i] = 0.f;
-      if (!DENSE) sh.key[i] = kFree;
+  // the first of the history and of the biases, on their way as well
+  const int32_t* h = a.history + b * a.ld_history;
+  int64_t nh = 0, np = 0, nb = 0;
+  if (a.history) {
+    nh = a.n_history ? (int64_t)a.n_history[b] : a.history_len;
+    nh = min(max(nh, (int64_t)0), a.history_len);
+    np = a.n_prompt ? min(max((int64_t)a.n_prompt[b], (int64_t)0), nh) : 0;
+  }
+  int32_t seen[kAhead][4];
+  auto load_history = [&](int64_t i) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load_run<4, i32x4>(h, i + 4 * TH * u, nh, (int32_t)-1, seen[u]);
+  };
+  load_history(4 * tid);
+  int32_t bias_id = -1;
+  float bias_add = 0.f;
+  auto load_bias = [&](int64_t i) {
+    bias_id = -1;
+    if (i < nb) {
+      bias_id = a.bias_ids[b * a.ld_bias + i];
+      bias_add = a.bias[b * a.ld_bias + i];
     }
+  };
+  if (a.bias_ids) {
+    nb = a.n_bias ? (int64_t)a.n_bias[b] : a.bias_len;
+    nb = min(max(nb, (int64_t)0), a.bias_len);
+    load_bias(tid);
+  }
+
+  int place[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) place[i] = DENSE ? W * (tid + TH * (i / W)) + i % W : 0;
+  if (a.history || (!DENSE && a.bias_ids)) {
+    sh.clear(tid);
     __syncthreads();
     if constexpr (!DENSE) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) place[i] = open[i] ? sh.take(id[i]) : 0;
+      for (int i = 0; i < N; ++i)
+        if (open[i]) place[i] = sh.take(id[i]);
       __syncthreads();
     }
   }
   if (a.history) {
-    int64_t nh = a.n_history ? (int64_t)a.n_history[b] : a.history_len;
-    nh = min(max(nh, (int64_t)0), a.history_len);
-    const int64_t np = a.n_prompt ? min(max((int64_t)a.n_prompt[b], (int64_t)0), nh) : 0;
-    const int32_t* h = a.history + b * a.ld_history;
-    for (int64_t i = 4 * tid; i < nh; i += 4 * kThreads) {
-      int32_t t[4];
-      load4<i32x4>(h, i, nh, (int32_t)-1, t);
+    for (int64_t i = 4 * tid; i < nh; i += 4 * TH * kAhead) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int p = sh.find(t[e], base, width, a.v);
-        if (p >= 0) {
-          if (i + e < np)
-            atomicOr(&sh.count[p], kPrompt);
-          else
-            atomicAdd(&sh.count[p], 1u);
-        }
-      }
-    }
-  }
-  if (a.bias_ids) {
-    int64_t nb = a.n_bias ? (int64_t)a.n_bias[b] : a.bias_len;
-    nb = min(max(nb, (int64_t)0), a.bias_len);
-    for (int64_t i0 = 0; i0 < nb; i0 += kThreads) {
-      const int64_t i = i0 + tid;
-      const int m = (int)min((int64_t)kThreads, nb - i0);
-      const int mine = i < nb ? sh.find(a.bias_ids[b * a.ld_bias + i], base, width, a.v) : -1;
-      __syncthreads();  // the list before is done with
-      sh.list_at[tid] = mine;
-      sh.list_add[tid] = i < nb ? a.bias[b * a.ld_bias + i] : 0.f;
-      __syncthreads();
-      if (mine >= 0) {
-        // the first entry of a place adds up the place's entries, in order
-        float sum = sh.bias[mine];
-        int first = tid;
-#pragma unroll 8
-        for (int e = 0; e < m; ++e) {
-          if (sh.list_at[e] == mine) {
-            first = min(first, e);
-            sum += sh.list_add[e];
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int p = sh.find(seen[u][e], base, width, a.v);
+          if (p >= 0) {
+            if (i + 4 * TH * u + e < np)
+              atomicOr(&sh.count[p], kPrompt);
+            else
+              atomicAdd(&sh.count[p], 1u);
           }
         }
-        if (first == tid) sh.bias[mine] = sum;
-      }
+      if (i + 4 * TH * kAhead < nh) load_history(i + 4 * TH * kAhead);
     }
-  }
-  __syncthreads();
-
-  if (a.history || a.bias_ids) {
+    __syncthreads();
     const float rep = a.repetition ? a.repetition[b] : 1.f;
     const float freq = a.frequency ? a.frequency[b] : 0.f;
     const float pres = a.presence ? a.presence[b] : 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int p = DENSE ? 4 * (tid + kThreads * (i / 4)) + i % 4 : place[DENSE ? 0 : i];
-      const uint32_t c = sh.count[p];
-      if (c) {
+      const uint32_t c = sh.count[place[i]];
+      if (c && open[i]) {
         z[i] = z[i] > 0.f ? z[i] / rep : z[i] * rep;
         const uint32_t made = c & ~kPrompt;
         z[i] -= freq * (float)made;
         if (made) z[i] -= pres;
       }
-      z[i] += sh.bias[p];
     }
+  }
+  if (a.bias_ids) {
+    // dense rows: the logits themselves in the table, each to its own thread's
+    // words, which only that thread has read above
+    float* sums = DENSE ? reinterpret_cast<float*>(sh.count) : sh.bias;
+    if constexpr (DENSE) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) sums[place[i]] = z[i];
+    }
+    for (int64_t i0 = 0; i0 < nb; i0 += TH) {
+      if (i0 > 0) load_bias(i0 + tid);
+      __syncthreads();  // the logits are there, the list before is done with
+      const int mine = sh.find(bias_id, base, width, a.v);
+      const uint64_t in = __ballot(mine >= 0);
+      const int at = 64 * wave + __popcll(in & ((1ull << lane) - 1));
+      if (mine >= 0) {
+        sh.list_at[at] = mine;
+        sh.list_add[at] = bias_add;
+      }
+      if (lane == 0) sh.listed[wave] = __popcll(in);
+      __syncthreads();
+      if (mine >= 0) {
+        // the first entry of a place adds up the place's entries, in order
+        float sum = 0.f;
+        int first = at;
+        for (int w = 0; w < TH / 64; ++w) {
+          const int m = sh.listed[w];
+          for (int e = 64 * w; e < 64 * w + m; ++e)
+            if (sh.list_at[e] == mine) {
+              first = min(first, e);
+              sum += sh.list_add[e];
+            }
+        }
+        if (first == at) sums[mine] += sum;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (DENSE || open[i]) z[i] = DENSE ? sums[place[i]] : z[i] + sums[place[i]];
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    open[i] = open[i] && (DENSE ? allow[i / 4] >> (i % 4) : allow[i]) & 1u;
+    open[i] = open[i] && (DENSE ? allow[i / W] >> (i % W) : allow[DENSE ? 0 : i]) & 1u;
     if (!open[i]) z[i] = -INFINITY;
   }
   if (a.out) {
     float* out = a.out + b * a.ld_out + base;
 #pragma unroll
     for (int j = 0; j < G; ++j) {
-      const int64_t at = 4 * (tid + (int64_t)kThreads * j);
-      if (at + 4 <= width)
-        *reinterpret_cast<f32x4*>(out + at) = f32x4{z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]};
+      const int64_t at = W * (tid + (int64_t)TH * j);
+      if (W == 4 && at + 4 <= width)
+        *reinterpret_cast<f32x4*>(out + at) = f32x4{z[W * j], z[W * j + 1 % W], z[W * j + 2 % W], z[W * j + 3 % W]};
       else
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (at + e < width) out[at + e] = z[4 * j + e];
+        for (int e = 0; e < W; ++e)
+          if (at + e < width) out[at + e] = z[W * j + e];
     }
   }
   if (a.parts) {
     uint32_t word[N] = {};
     if (a.token_sample) {
 #pragma unroll
-      for (int j = 0; j < G; ++j) {
+      for (int i = 0; i < N; i += DENSE ? 4 : 1) {
+        const U4 w = token_words(a.seed, (uint32_t)b, (uint32_t)id[i] >> 2);
         if constexpr (DENSE) {
-          const U4 w = token_words(a.seed, (uint32_t)b, (uint32_t)id[4 * j] >> 2);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) word[4 * j + e] = u4_word(w, e);
+          for (int e = 0; e < 4; ++e) word[i + e] = u4_word(w, e);
         } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const U4 w = token_words(a.seed, (uint32_t)b, (uint32_t)id[4 * j + e] >> 2);
-            word[4 * j + e] = u4_word(w, id[4 * j + e] & 3);
-          }
+          word[i] = u4_word(w, id[i] & 3);
         }
       }
     }
     Part part = wave_choice(choose<N>(z, id, open, a.token_sample != 0, a.tprime, word));
     if (lane == 0) sh.parts[wave] = part;
     __syncthreads();
-    if (tid == 0) {
-#pragma unroll
-      for (int w = 1; w < kThreads / 64; ++w) part = choice_merge(part, sh.parts[w]);
-      a.parts[b * gridDim.x + blockIdx.x] = part;
+    if (wave == 0) {
+      part = wave_choice(lane < TH / 64 ? sh.parts[lane] : part_empty());
+      if (lane == 0) a.parts[b * gridDim.x + blockIdx.x] = part;
     }
   }
 }
 
-// Groups per thread: four where that still leaves two workgroups per CU.
-int groups_of(int64_t B, int64_t n) { return B * ((n + 4095) / 4096) >= 512 ? 4 : 1; }
-
-template <bool DENSE>
-void launch(const RulesArgs& a, int64_t B, hipStream_t st) {
-  const dim3 grid((unsigned)rules_parts(B, a.n), (unsigned)B), block(kThreads);
-  if (groups_of(B, a.n) == 4)
-    hipLaunchKernelGGL((k_rules<DENSE, 4>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((k_rules<DENSE, 1>), grid, block, 0, st, a);
+// Tiles of a call: large ones walk the history less often, small ones spread few
+// rows over the CUs; the large one where it leaves two workgroups per CU.
+int tile_of(int64_t B, int64_t n, bool dense) {
+  const int large = dense ? 4096 : 1024, small = dense ? 1024 : 256;
+  return B * ((n + large - 1) / large) >= 512 ? large : small;
 }
 
 }  // namespace
 
-int64_t rules_parts(int64_t B, int64_t n) {
-  const int tile = 4 * kThreads * groups_of(B, n);
+int64_t rules_parts(int64_t B, int64_t n, bool dense) {
+  const int tile = tile_of(B, n, dense);
   return (n + tile - 1) / tile;
 }
 
 hipError_t launch_rules(const RulesArgs& a, int64_t B, hipStream_t st) {
-  if (a.ids)
-    launch<false>(a, B, st);
-  else
-    launch<true>(a, B, st);
+  const dim3 grid((unsigned)rules_parts(B, a.n, !a.ids), (unsigned)B);
+  switch (tile_of(B, a.n, !a.ids)) {
+    case 4096: hipLaunchKernelGGL((k_rules<true, 256, 4, 4>), grid, dim3(256), 0, st, a); break;
+    case 1024:
+      if (a.ids)
+        hipLaunchKernelGGL((k_rules<false, 256, 4, 1>), grid, dim3(256), 0, st, a);
+      else
+        hipLaunchKernelGGL((k_rules<true, 256, 4, 1>), grid, dim3(256), 0, st, a);
+      break;
+    default: hipLaunchKernelGGL((k_rules<false, 256, 1, 1>), grid, dim3(256), 0, st, a);
+  }
   return hipGetLastError();
 }
 

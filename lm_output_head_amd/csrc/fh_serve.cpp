@@ -320,7 +320,7 @@ int64_t fh_logits_workspace(int64_t B, int64_t n) {
   return guarded<int64_t>(FH_ENOMEM, [&]() -> int64_t {
     if (B < 1 || B > 65535) return fail(FH_EINVAL, "B outside [1, 65535]");
     if (n < 1 || n > kMaxWidth) return fail(FH_EINVAL, "n outside [1, 2^30]");
-    return (int64_t)sizeof(fh::Part) * B * fh::rules_parts(B, n);
+    return (int64_t)sizeof(fh::Part) * B * std::max(fh::rules_parts(B, n, true), fh::rules_parts(B, n, false));
   });
 }
 
@@ -355,8 +355,6 @@ fh_status fh_logits_apply(const float* logits, int64_t ld_logits, const int32_t*
       s = check_ld("ld_history", l.ld_history, l.history_len, B);
     } else if (l.n_history || l.n_prompt) {
       return fail(FH_EINVAL, "n_history and n_prompt need a history");
-    } else if (l.repetition || l.frequency || l.presence) {
-      return fail(FH_EINVAL, "penalties need a history");
     }
     if (s != FH_OK) return s;
     if (!l.bias_ids != !l.bias) return fail(FH_EINVAL, "bias_ids and bias go together");
@@ -408,7 +406,7 @@ fh_status fh_logits_apply(const float* logits, int64_t ld_logits, const int32_t*
     hipStream_t st = static_cast<hipStream_t>(stream);
     hipError_t r = fh::launch_rules(a, B, st);
     if (r == hipSuccess && choice)
-      r = fh::launch_choice(a.parts, B, fh::rules_parts(B, n), out_token, out_token_logit, out_lse, st);
+      r = fh::launch_choice(a.parts, B, fh::rules_parts(B, n, !ids), out_token, out_token_logit, out_lse, st);
     return r == hipSuccess ? FH_OK : hip_fail(r, "logit rules launch");
   });
 }

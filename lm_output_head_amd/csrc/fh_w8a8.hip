@@ -143,7 +143,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_w8a8_few(W8A8Args a) {
     if (a.out && col < a.B) store_run<T, 4, false>(static_cast<T*>(a.out) + col * a.ld_out, j, a.n, o);
   }
   if (HEAD) {
-    const Part p = wave_choice<16>(choose_tile<FN>(a, z, col, t0, g));
+    const Part p = column_choice(choose_tile<FN>(a, z, col, t0, g));
     if (g == 0) sh[wave][col] = p;
     __syncthreads();
     const int i = threadIdx.x;
@@ -310,7 +310,7 @@ __global__ __launch_bounds__(64 * WN * WM) void k_w8a8_tile(W8A8Args a, int n_ti
       if (a.out) *reinterpret_cast<V*>(row + 16 * m) = o;
     }
     if (HEAD) {
-      const Part p = wave_choice<16>(choose_tile<FN>(a, z, q, t0, g));
+      const Part p = column_choice(choose_tile<FN>(a, z, q, t0, g));
       if (g == 0) sP[wave][16 * t + col] = p;
     }
     if (a.out) {

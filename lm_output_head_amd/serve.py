@@ -80,36 +80,43 @@ def _stream(dev):
     return torch.cuda.current_stream(dev).cuda_stream
 
 
+# The same without building a Stream object (1.9 us of a call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is not None:
+    def _stream(dev):  # noqa: F811
+        return _raw_stream(dev.index)
+
+
 # ------------------------------------------------------------------ the norm
+
+def _norm_inputs(x, residual, weight):
+    if x.dim() != 2 or x.dtype not in _DTYPES:
+        raise ValueError(f"x must be [B x d] float32 or bfloat16, got {x.dtype} {tuple(x.shape)}")
+    ld_r = 0 if residual is None else _rows(residual, x.dtype, x.shape, "residual")
+    if weight is not None:
+        _vector(weight, x.dtype, x.shape[1], "weight")
+    return _rows(x, x.dtype, x.shape, "x"), ld_r
+
 
 def fh_rmsnorm(x, residual, weight, eps, weight_offset, out=None, out_residual=None, out_q=None,
                out_scale=None, stream=None) -> None:
     """out = rmsnorm(x + residual) * (weight_offset + weight); out_residual =
     x + residual; (out_q, out_scale) = the norm in int8 with a scale per row."""
-    if x.dim() != 2 or x.dtype not in _DTYPES:
-        raise ValueError(f"x must be [B x d] float32 or bfloat16, got {x.dtype} {tuple(x.shape)}")
+    ld_x, ld_r = _norm_inputs(x, residual, weight)
     if (out_q is None) != (out_scale is None):
         raise ValueError("out_q and out_scale go together")
-    shape, dt = x.shape, x.dtype
-    B, d = shape
-    ld_x = _rows(x, dt, shape, "x")
-    ld_r = ld_o = ld_s = ld_q = 0
-    if residual is not None:
-        ld_r = _rows(residual, dt, shape, "residual")
-    if weight is not None:
-        _vector(weight, dt, d, "weight")
-    if out is not None:
-        ld_o = _rows(out, dt, shape, "out")
-    if out_residual is not None:
-        ld_s = _rows(out_residual, dt, shape, "out_residual")
+    dt, shape = x.dtype, x.shape
+    ld_o = 0 if out is None else _rows(out, dt, shape, "out")
+    ld_s = 0 if out_residual is None else _rows(out_residual, dt, shape, "out_residual")
+    ld_q = 0
     if out_q is not None:
         ld_q = _rows(out_q, torch.int8, shape, "out_q")
-        _vector(out_scale, torch.float32, B, "out_scale")
+        _vector(out_scale, torch.float32, shape[0], "out_scale")
     dev = _device(x, residual, weight, out, out_residual, out_q, out_scale)
     with _on(dev, stream):
-        check(_abi.load().fh_rmsnorm(x.data_ptr(), ld_x, _ptr(residual), ld_r, _ptr(weight), _DTYPES[dt], B, d, eps,
-                                     weight_offset, _ptr(out), ld_o, _ptr(out_residual), ld_s, _ptr(out_q), ld_q,
-                                     _ptr(out_scale), _stream(dev)))
+        check(_abi.load().fh_rmsnorm(x.data_ptr(), ld_x, _ptr(residual), ld_r, _ptr(weight), _DTYPES[dt], shape[0],
+                                     shape[1], eps, weight_offset, _ptr(out), ld_o, _ptr(out_residual), ld_s,
+                                     _ptr(out_q), ld_q, _ptr(out_scale), _stream(dev)))
 
 
 def rmsnorm(x, weight=None, *, residual=None, eps=1e-6, weight_offset=0.0, want_out=True, want_q=False,
@@ -118,21 +125,24 @@ def rmsnorm(x, weight=None, *, residual=None, eps=1e-6, weight_offset=0.0, want_
     positions of [B x T x d] need no copy).  Returns "out" (the head's h) with
     want_out, "residual" (x + residual) with a residual, and with want_q the
     int8 head's "q" [B x d] (rows padded to 16 bytes) and "q_scale" [B]."""
-    if x.dim() != 2:
-        raise ValueError(f"x must be [B x d], got shape {tuple(x.shape)}")
-    B, d = x.shape
+    ld_x, ld_r = _norm_inputs(x, residual, weight)
+    dev = _device(x, residual, weight)
+    dt, (B, d) = x.dtype, x.shape
     got = {}
-    with _on(_device(x), stream):
+    out = out_residual = q = scale = None
+    with _on(dev, stream):
         if want_out:
-            got["out"] = torch.empty((B, d), dtype=x.dtype, device=x.device)
+            got["out"] = out = x.new_empty((B, d))
         if residual is not None:
-            got["residual"] = torch.empty((B, d), dtype=x.dtype, device=x.device)
+            got["residual"] = out_residual = x.new_empty((B, d))
+        ld_q = (d + 15) // 16 * 16
         if want_q:
-            q = torch.empty((B, (d + 15) // 16 * 16), dtype=torch.int8, device=x.device)
-            got["q"] = q if d % 16 == 0 else q[:, :d]
-            got["q_scale"] = torch.empty((B,), dtype=torch.float32, device=x.device)
-        fh_rmsnorm(x, residual, weight, eps, weight_offset, got.get("out"), got.get("residual"), got.get("q"),
-                   got.get("q_scale"))
+            q = x.new_empty((B, ld_q), dtype=torch.int8)
+            got["q"] = q if d == ld_q else q[:, :d]
+            got["q_scale"] = scale = x.new_empty((B,), dtype=torch.float32)
+        check(_abi.load().fh_rmsnorm(x.data_ptr(), ld_x, _ptr(residual), ld_r, _ptr(weight), _DTYPES[dt], B, d, eps,
+                                     weight_offset, _ptr(out), d, _ptr(out_residual), d, _ptr(q), ld_q, _ptr(scale),
+                                     _stream(dev)))
     return got
 
 
@@ -280,16 +290,19 @@ class W8A8Head:
 
     def __del__(self):
         # not while the interpreter shuts down (see FlashHead)
-        if sys.is_finalizing():
+        if sys is None or sys.is_finalizing():
             return
         try:
             self.close()
         except Exception:
             pass
 
-    def _workspace(self, q, forward):
-        size = fh_w8a8_workspace(self.w, q, forward)
-        return torch.empty((size,), dtype=torch.uint8, device=self.device) if size else None
+    def _inputs(self, q, q_scale, forward):
+        """Row stride, workspace size of a call on q; all on the weight's GPU."""
+        _, B, ld_q, dev = _product_args(self.w, q, q_scale)
+        if _device(q, q_scale) != dev:
+            raise ValueError("tensors must be on the weight's GPU")
+        return ld_q, _size(_abi.load().fh_w8a8_workspace(self.w, q.data_ptr(), ld_q, B, forward))
 
     def codes(self, stream=None):
         """The codes [n x k] and scales [n]."""
@@ -302,24 +315,35 @@ class W8A8Head:
     def matmul(self, q: torch.Tensor, q_scale: torch.Tensor, dtype=torch.float32, stream=None) -> torch.Tensor:
         """[B x n] = (q code^T) scaled per token and channel, in float32 or
         bfloat16; q and q_scale as rmsnorm(want_q=True) gives them."""
+        ld_q, size = self._inputs(q, q_scale, 0)
+        if dtype not in _DTYPES:
+            raise ValueError("dtype must be float32 or bfloat16")
+        B = q.shape[0]
         with _on(self.device, stream):
-            out = torch.empty((q.shape[0], self.n), dtype=dtype, device=self.device)
-            fh_w8a8_matmul(self.w, q, q_scale, out, self._workspace(q, False))
+            out = q.new_empty((B, self.n), dtype=dtype)
+            ws = q.new_empty((size,), dtype=torch.uint8) if size else None
+            check(_abi.load().fh_w8a8_matmul(self.w, q.data_ptr(), ld_q, q_scale.data_ptr(), B, out.data_ptr(),
+                                             self.n, _DTYPES[dtype], _ptr(ws), size, _stream(self.device)))
         return out
 
     def forward(self, q: torch.Tensor, q_scale: torch.Tensor, mode: int = 0, temperature: float = 1.0,
                 seed: int = 0, want_logits: bool = False, stream=None) -> dict:
         """FlashHead.dense on int8 operands: "token", "token_logit", "lse" and
         with want_logits "logits" [B x n]."""
+        ld_q, size = self._inputs(q, q_scale, 1)
         B = q.shape[0]
         with _on(self.device, stream):
-            out = {"token": torch.empty((B,), dtype=torch.int32, device=self.device),
-                   "token_logit": torch.empty((B,), dtype=torch.float32, device=self.device),
-                   "lse": torch.empty((B,), dtype=torch.float32, device=self.device)}
+            token = q.new_empty((B,), dtype=torch.int32)
+            logit = q.new_empty((B,), dtype=torch.float32)
+            lse = q.new_empty((B,), dtype=torch.float32)
+            out = {"token": token, "token_logit": logit, "lse": lse}
+            logits = None
             if want_logits:
-                out["logits"] = torch.empty((B, self.n), dtype=torch.float32, device=self.device)
-            fh_w8a8_forward(self.w, q, q_scale, mode, temperature, seed, out["token"], out["token_logit"],
-                            out["lse"], out.get("logits"), self._workspace(q, True))
+                out["logits"] = logits = q.new_empty((B, self.n), dtype=torch.float32)
+            ws = q.new_empty((size,), dtype=torch.uint8) if size else None
+            check(_abi.load().fh_w8a8_forward(self.w, q.data_ptr(), ld_q, q_scale.data_ptr(), B, mode, temperature,
+                                              seed, token.data_ptr(), logit.data_ptr(), lse.data_ptr(), _ptr(logits),
+                                              self.n, _ptr(ws), size, _stream(self.device)))
         return out
 
     def step(self, x: torch.Tensor, weight=None, *, residual=None, eps=1e-6, weight_offset=0.0, rules=None,
@@ -347,7 +371,7 @@ class LogitRules:
     (or a captured graph) updates them in place.
 
     history [B x L] int32 with n_prompt, n_history [B] int32; repetition,
-    frequency, presence [B] float32; bias_ids [B x N] int32 with bias float32
+    frequency, presence [B] float32 (without a history they do nothing); bias_ids [B x N] int32 with bias float32
     and n_bias [B] int32; mask [R x ceil(v / 32)] int32 words (bit t % 32 of
     word t / 32 allows token t) with mask_row [B] int32 (outside [0, R): all
     allowed; without it row b takes mask row b).  Each may be None.
@@ -364,8 +388,8 @@ class LogitRules:
         for name, t in lists.items():
             if t is not None and t.dim() != 2:
                 raise ValueError(f"{name} must be [B x length], got shape {tuple(t.shape)}")
-        if history is None and any(t is not None for t in (n_prompt, n_history, repetition, frequency, presence)):
-            raise ValueError("n_prompt, n_history and penalties need a history")
+        if history is None and (n_prompt is not None or n_history is not None):
+            raise ValueError("n_prompt and n_history need a history")
         if (bias_ids is None) != (bias is None) or (n_bias is not None and bias is None):
             raise ValueError("bias_ids and bias go together, n_bias needs them")
         if mask is None and mask_row is not None:
@@ -404,30 +428,35 @@ def fh_logits_workspace(B: int, n: int) -> int:
     return _size(_abi.load().fh_logits_workspace(B, n))
 
 
+def _apply_inputs(logits, ids, v, rules):
+    """Row strides of logits and ids, the rules' struct; all on one GPU."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [B x n], got shape {tuple(logits.shape)}")
+    shape = logits.shape
+    ld_z = _rows(logits, torch.float32, shape, "logits")
+    ld_ids = 0 if ids is None else _rows(ids, torch.int32, shape, "ids")
+    if rules is None:
+        return ld_z, ld_ids, None
+    if rules.v != v or (rules.B is not None and rules.B != shape[0]):
+        raise ValueError(f"rules are of {rules.B} rows over {rules.v} tokens, logits of {shape[0]} rows over {v}")
+    if rules.device is not None and rules.device != logits.device:
+        raise ValueError("rules and logits must be on one GPU")
+    return ld_z, ld_ids, rules._struct
+
+
 def fh_logits_apply(logits, ids, v, rules, mode, temperature, seed, out_logits=None, out_token=None,
                     out_token_logit=None, out_lse=None, workspace=None, stream=None) -> None:
     """The rules (LogitRules or None) on logits [B x n], of all v tokens or of
     the tokens ids [B x n], then the choice of the token."""
-    if logits.dim() != 2:
-        raise ValueError(f"logits must be [B x n], got shape {tuple(logits.shape)}")
-    shape = logits.shape
-    B, n = shape
-    ld_z = _rows(logits, torch.float32, shape, "logits")
-    ld_ids = 0 if ids is None else _rows(ids, torch.int32, shape, "ids")
-    ld_out = 0 if out_logits is None else _rows(out_logits, torch.float32, shape, "out_logits")
+    ld_z, ld_ids, struct = _apply_inputs(logits, ids, v, rules)
+    B, n = logits.shape
+    ld_out = 0 if out_logits is None else _rows(out_logits, torch.float32, logits.shape, "out_logits")
     if out_token is not None:
         _vector(out_token, torch.int32, B, "out_token")
     if out_token_logit is not None:
         _vector(out_token_logit, torch.float32, B, "out_token_logit")
     if out_lse is not None:
         _vector(out_lse, torch.float32, B, "out_lse")
-    struct = None
-    if rules is not None:
-        if rules.v != v or (rules.B is not None and rules.B != B):
-            raise ValueError(f"rules are of {rules.B} rows over {rules.v} tokens, logits of {B} rows over {v}")
-        if rules.device is not None and rules.device != logits.device:
-            raise ValueError("rules and logits must be on one GPU")
-        struct = rules._struct
     ws, ws_bytes = _workspace_arg(workspace)
     dev = _device(logits, ids, out_logits, out_token, out_token_logit, out_lse, workspace)
     with _on(dev, stream):
@@ -441,20 +470,26 @@ def logits_apply(logits, rules=None, *, ids=None, v=None, mode: int = 0, tempera
     """The rules on logits [B x n] of all tokens, or of the tokens ids [B x n]
     (a forward's "logits" and "ids"): "logits" (in `out`, which may be logits
     itself) and with want_token "token", "token_logit" and "lse"."""
-    if logits.dim() != 2:
-        raise ValueError(f"logits must be [B x n], got shape {tuple(logits.shape)}")
-    B, n = logits.shape
     if v is None:
-        v = rules.v if rules is not None else n
-    dev = _device(logits)
+        v = rules.v if rules is not None else logits.shape[-1]
+    ld_z, ld_ids, struct = _apply_inputs(logits, ids, v, rules)
+    dev = _device(logits, ids, out)
+    B, n = logits.shape
+    ld_out = n if out is None else _rows(out, torch.float32, logits.shape, "out")
+    lib = _abi.load()
+    token = logit = lse = ws = None
+    size = 0
     with _on(dev, stream):
-        got = {"logits": torch.empty((B, n), dtype=torch.float32, device=dev) if out is None else out}
-        workspace = None
+        if out is None:
+            out = logits.new_empty((B, n))
+        got = {"logits": out}
         if want_token:
-            got["token"] = torch.empty((B,), dtype=torch.int32, device=dev)
-            got["token_logit"] = torch.empty((B,), dtype=torch.float32, device=dev)
-            got["lse"] = torch.empty((B,), dtype=torch.float32, device=dev)
-            workspace = torch.empty((fh_logits_workspace(B, n),), dtype=torch.uint8, device=dev)
-        fh_logits_apply(logits, ids, v, rules, mode, temperature, seed, got["logits"], got.get("token"),
-                        got.get("token_logit"), got.get("lse"), workspace)
+            got["token"] = token = logits.new_empty((B,), dtype=torch.int32)
+            got["token_logit"] = logit = logits.new_empty((B,))
+            got["lse"] = lse = logits.new_empty((B,))
+            size = _size(lib.fh_logits_workspace(B, n))
+            ws = logits.new_empty((size,), dtype=torch.uint8)
+        check(lib.fh_logits_apply(logits.data_ptr(), ld_z, _ptr(ids), ld_ids, B, n, v, struct, mode, temperature, seed,
+                                  out.data_ptr(), ld_out, _ptr(token), _ptr(logit), _ptr(lse), _ptr(ws), size,
+                                  _stream(dev)))
     return got

@@ -190,6 +190,17 @@ def test_logits_alone_and_token_alone():
     assert torch.equal(only["logits"], full["logits"]) and torch.equal(tok, full["token"])
 
 
+def test_penalties_without_a_history_do_nothing():
+    from lm_output_head_amd import LogitRules, logits_apply
+    z = torch.randn(3, 4000, device="cuda")
+    two = torch.full((3,), 2.0, device="cuda")
+    a = logits_apply(z, LogitRules(4000, repetition=two, frequency=two, presence=two))
+    none = torch.zeros(3, 0, dtype=torch.int32, device="cuda")
+    b = logits_apply(z, LogitRules(4000, history=none, repetition=two, frequency=two, presence=two))
+    for o in (a, b):
+        assert torch.equal(o["logits"], z) and torch.equal(o["token"].long(), z.argmax(1))
+
+
 def test_same_choice_as_the_dense_head():
     """Without rules the choice over fh_dense_forward's logits is its own."""
     from lm_output_head_amd import FlashHead, logits_apply

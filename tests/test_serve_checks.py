@@ -120,7 +120,6 @@ CALL = dict(z=A, ld=100, ids=None, ld_ids=0, B=3, n=100, v=100, rules=None, mode
     ({"rules": {"ld_history": 9}}, "ld_history"),
     ({"rules": {"history_len": -1}}, "history_len"),
     ({"rules": {"history": None, "n_history": A.value}}, "need a history"),
-    ({"rules": {"history": None, "presence": A.value}}, "need a history"),
     ({"rules": {"bias": A.value}}, "go together"),
     ({"rules": {"bias": A.value, "bias_ids": A.value, "bias_len": 4, "ld_bias": 3}}, "ld_bias"),
     ({"rules": {"bias": A.value, "bias_ids": A.value, "bias_len": -4}}, "bias_len"),
@@ -214,7 +213,6 @@ def test_binding_product_refusals(weight):
     ({"history": torch.zeros(2, 5)}, "history: expected"),
     ({"history": torch.zeros(5, dtype=torch.int32)}, "history must be"),
     ({"n_history": torch.zeros(2, dtype=torch.int32)}, "need a history"),
-    ({"repetition": torch.zeros(2)}, "need a history"),
     ({"history": torch.zeros(2, 5, dtype=torch.int32), "repetition": torch.zeros(3)}, "repetition: expected"),
     ({"history": torch.zeros(2, 5, dtype=torch.int32), "n_prompt": torch.zeros(2)}, "n_prompt: expected"),
     ({"bias": torch.zeros(2, 3)}, "go together"),
