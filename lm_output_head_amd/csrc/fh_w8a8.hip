@@ -10,6 +10,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fh_choice.hpp"
 #include "fh_internal.hpp"
@@ -96,62 +97,99 @@ __device__ __forceinline__ Part choose_tile(const W8A8Args& a, const float (&z)[
   return choose<4 * FN>(v, id, open, a.token_sample != 0, a.tprime, word);
 }
 
-constexpr int kWaves = 4;
-
-// Up to 16 tokens: each wave streams 16 FN rows of W, the tokens come from the
-// caches.
-template <int FN, bool BF16, bool HEAD>
-__global__ __launch_bounds__(64 * kWaves) void k_w8a8_few(W8A8Args a) {
-  __shared__ Part sh[HEAD ? kWaves : 1][16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Few tokens, or too few rows for a tile per CU: 16 FN rows of W are streamed by
+// KW waves, each a run of the steps of k, that take their 16 FT tokens from the
+// caches and add up their sums in LDS (exact, so in any order).  A workgroup is
+// G such groups.  One wave per 32 rows left loads of one step in flight: 1 x
+// 128256 x 2048 45.7 -> 42.0 us, 1 x 4096 x 4096 20.8 -> 5.8, 1 x 1000 x 8192
+// 41.7 -> 5.2.
+template <int FT, int FN, int KW, int G, bool BF16, bool HEAD>
+__global__ __launch_bounds__(64 * KW * G) void k_w8a8_few(W8A8Args a) {
+  constexpr int kAhead = FN == 1 ? 4 : 2;  // steps whose loads go out together
+  typedef typename Out<BF16>::T T;
+  __shared__ i32x4 sums[G][KW * FN * FT * 64];
+  __shared__ Part sP[HEAD ? G : 1][HEAD ? 16 * FT : 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, kw = wave % KW, group = wave / KW;
   const int g = lane >> 4, col = lane & 15;
   const int64_t tiles = (a.n + 15) / 16;
-  const int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * FN;
+  const int64_t t0 = ((int64_t)blockIdx.x * G + group) * FN;
+  const int q0 = blockIdx.y * 16 * FT;
   const int steps = w_steps(a.k), chunks = (a.k + 15) / 16;
 
   const i32x4* wp[FN];
 #pragma unroll
   for (int m = 0; m < FN; ++m) wp[m] = static_cast<const i32x4*>(a.W) + min(t0 + m, tiles - 1) * steps * 64 + lane;
-  const int8_t* qp = a.q + (int64_t)min(col, a.B - 1) * a.ld_q;
-  i32x4 acc[FN][1];
+  const int8_t* qp[FT];
 #pragma unroll
-  for (int m = 0; m < FN; ++m) acc[m][0] = i32x4{0, 0, 0, 0};
-  for (int s = 0; s < steps; ++s) {
-    // a 16-byte chunk past the row stands in as its first: W is zero there
-    const int ch = 4 * s + g < chunks ? 4 * s + g : 0;
-    i32x4 wf[FN];
+  for (int t = 0; t < FT; ++t) qp[t] = a.q + (int64_t)min(q0 + 16 * t + col, a.B - 1) * a.ld_q;
+  i32x4 acc[FN][FT];
 #pragma unroll
-    for (int m = 0; m < FN; ++m) wf[m] = wp[m][s * 64];
-    const i32x4 qf = *reinterpret_cast<const i32x4*>(qp + 16 * ch);
+  for (int m = 0; m < FN; ++m)
 #pragma unroll
-    for (int m = 0; m < FN; ++m) acc[m][0] = mfma_i8(wf[m], qf, acc[m][0]);
-  }
-  typedef typename Out<BF16>::T T;
+    for (int t = 0; t < FT; ++t) acc[m][t] = i32x4{0, 0, 0, 0};
+  // N steps from s: their loads together, then their products.  A 16-byte chunk
+  // past the row stands in as its first: W is zero there.
+  auto advance = [&](auto count, int s) {
+    constexpr int N = decltype(count)::value;
+    i32x4 wf[N][FN], qf[N][FT];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int ch = 4 * (s + u) + g < chunks ? 4 * (s + u) + g : 0;
+#pragma unroll
+      for (int m = 0; m < FN; ++m) wf[u][m] = wp[m][(s + u) * 64];
+#pragma unroll
+      for (int t = 0; t < FT; ++t) qf[u][t] = *reinterpret_cast<const i32x4*>(qp[t] + 16 * ch);
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+      for (int m = 0; m < FN; ++m)
+#pragma unroll
+        for (int t = 0; t < FT; ++t) acc[m][t] = mfma_i8(wf[u][m], qf[u][t], acc[m][t]);
+  };
+  const int end = (int)((int64_t)steps * (kw + 1) / KW);
+  int s = (int)((int64_t)steps * kw / KW);
+  for (; s + kAhead <= end; s += kAhead) advance(std::integral_constant<int, kAhead>(), s);
+  for (; s < end; ++s) advance(std::integral_constant<int, 1>(), s);
+#pragma unroll
+  for (int m = 0; m < FN; ++m)
+#pragma unroll
+    for (int t = 0; t < FT; ++t) sums[group][((kw * FT + t) * FN + m) * 64 + lane] = acc[m][t];
+  __syncthreads();
   float ws[FN][4];
   load_scales<FN>(a, t0, g, ws);
-  const float qs = col < a.B ? a.qs[col] : 0.f;
-  float z[FN][4];
 #pragma unroll
-  for (int m = 0; m < FN; ++m) {
-    const int64_t j = 16 * (t0 + m) + 4 * g;
-    T o[4];
+  for (int t = 0; t < FT; ++t) {
+    if (t % KW != kw) continue;  // the group's waves finish its token tiles in turn
+    const int64_t q = q0 + 16 * t + col;
+    const float qs = q < a.B ? a.qs[q] : 0.f;
+    float z[FN][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      z[m][i] = (float)acc[m][0][i] * (qs * ws[m][i]);
-      o[i] = Out<BF16>::of(z[m][i]);
+    for (int m = 0; m < FN; ++m) {
+      i32x4 v = sums[group][(t * FN + m) * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < KW; ++w) v += sums[group][((w * FT + t) * FN + m) * 64 + lane];
+      T o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        z[m][i] = (float)v[i] * (qs * ws[m][i]);
+        o[i] = Out<BF16>::of(z[m][i]);
+      }
+      if (a.out && q < a.B) store_run<T, 4, false>(static_cast<T*>(a.out) + q * a.ld_out, 16 * (t0 + m) + 4 * g, a.n, o);
     }
-    if (a.out && col < a.B) store_run<T, 4, false>(static_cast<T*>(a.out) + col * a.ld_out, j, a.n, o);
+    if (HEAD) {
+      const Part p = column_choice(choose_tile<FN>(a, z, q, t0, g));
+      if (g == 0) sP[group][16 * t + col] = p;
+    }
   }
   if (HEAD) {
-    const Part p = column_choice(choose_tile<FN>(a, z, col, t0, g));
-    if (g == 0) sh[wave][col] = p;
     __syncthreads();
     const int i = threadIdx.x;
-    if (i < a.B && i < 16) {
-      Part p = sh[0][i];
+    if (i < 16 * FT && q0 + i < a.B) {
+      Part p = sP[0][i];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) p = choice_merge(p, sh[w][i]);
-      a.parts[(int64_t)i * gridDim.x + blockIdx.x] = p;
+      for (int w = 1; w < G; ++w) p = choice_merge(p, sP[w][i]);
+      a.parts[(int64_t)(q0 + i) * gridDim.x + blockIdx.x] = p;
     }
   }
 }
@@ -448,22 +486,44 @@ __global__ __launch_bounds__(kChoice) void k_choice(const Part* parts, int64_t n
 
 unsigned grid_of(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20); }
 
-constexpr int kFewFN = 2;
-
-// The tile of a call: rows and tokens of a workgroup.  The largest one that
-// leaves a workgroup for every CU and less than half its tokens empty; the head's
-// choice does not fit the registers beside the sums of k256.
-enum Tile { kFew, k32, k64, k128, k256 };
-constexpr int kTileRows[] = {16 * kFewFN * kWaves, 128, 128, 256, 256};
-constexpr int kTileTokens[] = {16, 32, 64, 128, 256};
-int64_t tiles_of(Tile t, int64_t n, int64_t B) {
-  return (n + kTileRows[t] - 1) / kTileRows[t] * ((B + kTileTokens[t] - 1) / kTileTokens[t]);
+// How a call is cut up: a tile of k_w8a8_tile (named by its tokens), or a shape
+// of k_w8a8_few.
+enum Kind { kFew16Rows8, kFew16Rows4, kFew32Rows2, kTokens32Rows8, kTokens32Rows4, k32, k64, k128, k256 };
+struct Plan {
+  Kind kind;
+  int rows, tokens;  // of a workgroup
+  int64_t row_tiles(int64_t n) const { return (n + rows - 1) / rows; }
+  int64_t tiles(int64_t n, int64_t B) const { return row_tiles(n) * ((B + tokens - 1) / tokens); }
+};
+// Up to 16 tokens: the fewer rows, the more waves share one's k (1 x 1000 x 8192
+// with 8 waves 5.2 us, with 4 7.5; 1 x 65536 x 512 9.5 and 7.9).  A wave of 16
+// rows reads its tokens once per KB of W, one of 32 half as often: 42.0 and 46.8
+// us for 1 x 128256 x 2048, 59.3 and 49.9 for 16; the head, whose choice one wave
+// of a group makes, 1 x 262144 x 1152 66.6 and 58.5.
+// More: the largest tile that leaves a workgroup for every CU and less than half
+// its tokens empty; the head's choice does not fit the registers beside the sums
+// of k256.  Where even the smallest leaves CUs idle, waves share k (32 x 4096 x
+// 4096 18.4 and 8.1 us, 128 x 4096 x 4096 18.6 and 12.7; with 224 tiles the
+// smallest is the better one, 23.5 and 33.8 for 32 x 28672 x 4096).
+Plan plan_of(int64_t n, int64_t B, bool head) {
+  if (B <= 16) {
+    const int64_t tiles = (n + 15) / 16;
+    if (tiles < 512) return Plan{kFew16Rows8, 16, 16};
+    if (tiles < 2048 || (B <= 4 && !head)) return Plan{kFew16Rows4, 16, 16};
+    return Plan{kFew32Rows2, 64, 16};
+  }
+  for (const Plan& p : {Plan{k256, 256, 256}, Plan{k128, 256, 128}, Plan{k64, 128, 64}})
+    if (!(head && p.kind == k256) && 2 * B > p.tokens && p.tiles(n, B) >= 256) return p;
+  const Plan least{k32, 128, 32};
+  if (least.tiles(n, B) >= 192) return least;
+  return B <= 32 ? Plan{kTokens32Rows8, 16, 32} : Plan{kTokens32Rows4, 32, 32};
 }
-Tile tile_of(int64_t n, int64_t B, bool head) {
-  if (B <= 16) return kFew;
-  for (Tile t : {k256, k128, k64})
-    if (!(head && t == k256) && 2 * B > kTileTokens[t] && tiles_of(t, n, B) >= 256) return t;
-  return k32;
+
+template <int FT, int FN, int KW, int G, bool BF16, bool HEAD>
+void launch_few(const W8A8Args& a, hipStream_t st) {
+  constexpr int kRows = 16 * FN * G, kTokens = 16 * FT;
+  const dim3 grid((unsigned)((a.n + kRows - 1) / kRows), (unsigned)((a.B + kTokens - 1) / kTokens));
+  hipLaunchKernelGGL((k_w8a8_few<FT, FN, KW, G, BF16, HEAD>), grid, dim3(64 * KW * G), 0, st, a);
 }
 
 template <int FT, int FN, int WN, int WM, bool BF16, bool HEAD>
@@ -479,11 +539,12 @@ void launch_tile(const W8A8Args& a, hipStream_t st) {
 
 template <bool BF16, bool HEAD>
 void launch_kind(const W8A8Args& a, hipStream_t st) {
-  switch (tile_of(a.n, a.B, HEAD)) {
-    case kFew:
-      hipLaunchKernelGGL((k_w8a8_few<kFewFN, BF16, HEAD>), dim3((unsigned)tiles_of(kFew, a.n, 1)), dim3(64 * kWaves),
-                         0, st, a);
-      return;
+  switch (plan_of(a.n, a.B, HEAD).kind) {
+    case kFew16Rows8: return launch_few<1, 1, 8, 1, BF16, HEAD>(a, st);
+    case kFew16Rows4: return launch_few<1, 1, 4, 1, BF16, HEAD>(a, st);
+    case kFew32Rows2: return launch_few<1, 2, 2, 2, BF16, HEAD>(a, st);
+    case kTokens32Rows8: return launch_few<2, 1, 8, 1, BF16, HEAD>(a, st);
+    case kTokens32Rows4: return launch_few<2, 2, 4, 1, BF16, HEAD>(a, st);
     case k32: return launch_tile<2, 2, 4, 1, BF16, HEAD>(a, st);
     case k64: return launch_tile<4, 2, 4, 1, BF16, HEAD>(a, st);
     case k128: return launch_tile<8, 2, 8, 1, BF16, HEAD>(a, st);
@@ -496,14 +557,11 @@ void launch_kind(const W8A8Args& a, hipStream_t st) {
 
 int64_t w8a8_packed_bytes(int64_t n, int64_t k) { return (n + 15) / 16 * w_steps(k) * 1024; }
 
-int64_t w8a8_parts(int64_t n, int64_t B) {
-  const int rows = kTileRows[tile_of(n, B, true)];
-  return (n + rows - 1) / rows;
-}
+int64_t w8a8_parts(int64_t n, int64_t B) { return plan_of(n, B, true).row_tiles(n); }
 
 hipError_t launch_w8a8(const W8A8Args& a, bool out_bf16, bool head, hipStream_t st) {
   // tiles are numbered in 32 bits
-  if (tiles_of(tile_of(a.n, a.B, head), a.n, a.B) >= (int64_t(1) << 30)) return hipErrorInvalidValue;
+  if (plan_of(a.n, a.B, head).tiles(a.n, a.B) >= (int64_t(1) << 30)) return hipErrorInvalidValue;
   if (head)
     launch_kind<false, true>(a, st);
   else if (out_bf16)

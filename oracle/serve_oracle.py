@@ -25,8 +25,8 @@ def rmsnorm(x, residual, weight, eps, offset):
 
 
 def product(q, q_scale, codes, scales):
-    """[B x n]: exact int64 sums, scaled in float64."""
-    acc = np.asarray(q, np.int64) @ np.asarray(codes, np.int64).T
+    """[B x n]: exact sums (whole numbers below 2^53 in float64), scaled in float64."""
+    acc = np.asarray(q, np.float64) @ np.asarray(codes, np.float64).T
     return acc * np.asarray(q_scale, np.float64)[:, None] * np.asarray(scales, np.float64)[None, :]
 
 

@@ -39,7 +39,11 @@ def dev(a):
 
 SIZES = [(1, 1, 1), (1, 16, 64), (3, 17, 65), (5, 130, 16), (16, 128, 128), (17, 1000, 192), (33, 515, 2048),
          (64, 272, 1152), (70, 301, 100), (128, 96, 2560), (129, 640, 320), (300, 1030, 80), (257, 2000, 576),
-         (1, 5003, 8192), (2, 40, 131071), (520, 513, 704)]
+         (1, 5003, 8192), (2, 40, 131071), (520, 513, 704),
+         # each way of cutting a call up, and odd and even numbers of blocks of k
+         (3, 9001, 70), (16, 8200, 448), (7, 32785, 48), (16, 33000, 320), (20, 25001, 320), (32, 24600, 448),
+         (40, 32801, 320), (64, 33000, 448), (100, 65601, 320), (128, 65600, 192), (300, 32801, 320),
+         (257, 33001, 448), (200, 4000, 320), (129, 70001, 130)]
 
 
 @pytest.mark.parametrize("B,n,k", SIZES)
@@ -124,7 +128,9 @@ def test_non_finite_weights_are_refused():
 
 
 @pytest.mark.parametrize("B,n,k", [(1, 1, 16), (1, 5000, 2048), (3, 1000, 100), (16, 4099, 128), (33, 700, 1152),
-                                   (64, 3000, 256), (130, 1111, 192), (300, 640, 64)])
+                                   (64, 3000, 256), (130, 1111, 192), (300, 640, 64),
+                                   (3, 9001, 70), (7, 32785, 48), (20, 25001, 80), (40, 32801, 64), (100, 65601, 64),
+                                   (300, 33001, 64), (200, 4000, 320)])
 @pytest.mark.parametrize("mode,T", [(0, 1.0), (2, 0.7)])
 def test_head(B, n, k, mode, T):
     from lm_output_head_amd import W8A8Head
