@@ -69,6 +69,10 @@ def parse():
     ap.add_argument("--spec", type=int, default=0, metavar="K",
                     help="time the speculative verification of K draft positions (fh_spec_verify) "
                          "beside K single-position drafts and the dense head at B=K; one JSON line")
+    ap.add_argument("--serve", action="store_true",
+                    help="time one decode step after the last layer at --shape, --B and --mode: norm, "
+                         "int8 dense head, rules on logits (W8A8Head.step), each part and the same step "
+                         "on the head in its own dtype; one JSON line")
     ap.add_argument("--burst", action="store_true",
                     help="time the plain one-shot read probe (fhb_read_probe) at the sizes of a "
                          "batch-1 call's phases, the whole call and the dense head; one JSON line")
@@ -198,15 +202,19 @@ def stream_bandwidth(sizes, nbuf=16, steps=100):
 
 
 CLUSTER_SOURCES = ("fh_cluster.hip",)  # the offline clustering, its own translation unit
+# the operators around the dense head: no code of theirs runs in a head call
+SERVE_SOURCES = ("fh_norm.hip", "fh_w8a8.hip", "fh_rules.hip", "fh_serve.cpp", "fh_serve.hpp",
+                 "fh_choice.hpp", "fh_host.hpp")
 
 
 def kernel_source_hash(cluster: bool = False) -> str:
     """Hash of the kernel sources a measurement depends on: the head's (every
-    file under csrc/ but the clustering's), or the clustering's."""
+    file under csrc/ but the clustering's and the operators' around the dense
+    head), or the clustering's."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "lm_output_head_amd", "csrc")
     for name in sorted(os.listdir(csrc)):
-        if (name in CLUSTER_SOURCES) != cluster:
+        if (name in CLUSTER_SOURCES) != cluster or name in SERVE_SOURCES:
             continue
         with open(os.path.join(csrc, name), "rb") as f:
             h.update(name.encode() + f.read())
@@ -739,6 +747,95 @@ def spec_main(args):
     head.close()
 
 
+def serve_main(args):
+    """One decode step after the last layer: rmsnorm(x + residual) with an
+    int8 output, the int8 dense head, the rules on its logits (penalties over
+    1000 tokens of history, 16 biases, a grammar mask on every other row) and
+    the choice of the token; beside it the step's parts, and the same step
+    with the norm's own output into the dense head of the shape's dtype.  Two
+    copies of each head are used in turn, so that no call finds the rows of
+    the one before in the 256 MB cache."""
+    import torch
+
+    from lm_output_head_amd import FlashHead, LogitRules, W8A8Head, logits_apply, rmsnorm
+    from synth import SHAPES, make_problem
+
+    if not torch.cuda.is_available():
+        print(json.dumps({"error": "no GPU visible"}))
+        sys.exit(1)
+    shape = SHAPES[args.shape]
+    B, v, d, mode, T = args.B, shape.v, shape.d, args.mode & 2, args.temperature
+    bf16 = shape.dtype == "bf16"
+    pb = make_problem(shape, nq=1)
+    if bf16:
+        E = torch.from_numpy(pb.E_bits.view("int16")).view(torch.bfloat16).cuda()
+        C = torch.from_numpy(pb.C_bits.view("int16")).view(torch.bfloat16).cuda()
+    else:
+        E, C = torch.from_numpy(pb.E).cuda(), torch.from_numpy(pb.C).cuda()
+    E2 = E.clone()
+    w8 = [W8A8Head(E), W8A8Head(E2)]
+    dense = [FlashHead(E, C, pb.C2T, max_batch=B), FlashHead(E2, C, pb.C2T, max_batch=B)]
+    g = torch.Generator(device="cuda").manual_seed(11)
+
+    def rand(*size):
+        return torch.randn(*size, generator=g, device="cuda")
+
+    x, res, weight = rand(B, d).to(E.dtype), rand(B, d).to(E.dtype), rand(d).to(E.dtype)
+    words = (v + 31) // 32
+    rules = LogitRules(
+        v, history=torch.randint(0, v, (B, 1000), generator=g, device="cuda", dtype=torch.int32),
+        n_prompt=torch.full((B,), 500, device="cuda", dtype=torch.int32),
+        repetition=torch.full((B,), 1.1, device="cuda"), presence=torch.full((B,), 0.2, device="cuda"),
+        bias_ids=torch.randint(0, v, (B, 16), generator=g, device="cuda", dtype=torch.int32), bias=rand(B, 16),
+        mask=torch.randint(-2 ** 31, 2 ** 31 - 1, (1, words), generator=g, device="cuda", dtype=torch.int32),
+        mask_row=(torch.arange(B, device="cuda", dtype=torch.int32) % 2) - 1)
+    st = torch.cuda.current_stream()
+
+    def timed(fn, n):
+        for i in range(10):
+            fn(i)
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        a.record(st)
+        for i in range(n):
+            fn(i)
+        b.record(st)
+        torch.cuda.synchronize()
+        return round(a.elapsed_time(b) * 1e3 / n, 2)
+
+    steps = max(20, min(args.steps, 400))
+    h = rmsnorm(x, weight, residual=res, want_q=True)
+    z = w8[0].matmul(h["q"], h["q_scale"])
+
+    def step_dense(i):
+        y = rmsnorm(x, weight, residual=res)
+        o = dense[i % 2].dense(y["out"], want_logits=True)
+        return logits_apply(o["logits"], rules, mode=mode, temperature=T, seed=i, out=o["logits"])
+
+    step_us = timed(lambda i: w8[i % 2].step(x, weight, residual=res, rules=rules, mode=mode, temperature=T,
+                                             seed=i), steps)
+    parts = {
+        "norm": timed(lambda i: rmsnorm(x, weight, residual=res, want_out=False, want_q=True), steps),
+        "int8_product": timed(lambda i: w8[i % 2].matmul(h["q"], h["q_scale"]), steps),
+        "int8_head": timed(lambda i: w8[i % 2].forward(h["q"], h["q_scale"], mode, T, i), steps),
+        "rules": timed(lambda i: logits_apply(z, rules, mode=mode, temperature=T, seed=i), steps),
+    }
+    dense_us = timed(step_dense, steps)
+    nbytes = v * d + 4 * v + 4 * B * v + B * d * (3 * E.element_size() + 1)
+    res_line = {
+        "metric": "decode step after the last layer: norm, int8 dense head, rules on logits, token",
+        "value": step_us, "unit": "us per step", "n_gpus": 1, "steps": steps, "higher_is_better": False,
+        "dtype": "int8 x int8, f32 logits", "data": "synthetic seeded clustered embeddings (no trained weights)",
+        "config": {"workload": f"{shape.name} B={B} mode={mode} T={T}", "B": B, "v": v, "d": d},
+        "parts_us": parts, f"step_{'bf16' if bf16 else 'f32'}_dense_us": dense_us,
+        "roofline": {"bound": "hbm", "achieved": round(nbytes / step_us / 1e3, 1), "peak": HBM_PEAK_GBS,
+                     "unit": "GB/s", "frac": round(nbytes / step_us / 1e3 / HBM_PEAK_GBS, 4)},
+    }
+    print(json.dumps(res_line), flush=True)
+    for o in w8 + dense:
+        o.close()
+
+
 def main():
     args = parse()
     if args.gpus != 1:
@@ -756,6 +853,9 @@ def main():
         return
     if args.spec:
         spec_main(args)
+        return
+    if args.serve:
+        serve_main(args)
         return
     if args.sweep:
         sweep_main(args)

@@ -8,7 +8,7 @@
 #include <algorithm>
 
 #include "fh_device.hpp"
-#include "fh_internal.hpp"
+#include "fh_serve.hpp"
 
 namespace fh {
 namespace {

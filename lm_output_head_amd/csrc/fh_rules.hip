@@ -14,7 +14,7 @@
 #include <hip/hip_runtime.h>
 
 #include "fh_choice.hpp"
-#include "fh_internal.hpp"
+#include "fh_serve.hpp"
 
 namespace fh {
 namespace {

@@ -13,7 +13,7 @@
 #include <string>
 
 #include "fh_host.hpp"
-#include "fh_internal.hpp"
+#include "fh_serve.hpp"
 #include "flashhead.h"
 
 struct fh_w8a8 {

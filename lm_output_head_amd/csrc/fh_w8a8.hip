@@ -13,7 +13,7 @@
 #include <type_traits>
 
 #include "fh_choice.hpp"
-#include "fh_internal.hpp"
+#include "fh_serve.hpp"
 
 namespace fh {
 namespace {
