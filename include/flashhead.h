@@ -440,7 +440,7 @@ fh_status fh_cluster(const void* E, fh_dtype dtype, int64_t v, int64_t d, int64_
  * The norm and the codes are taken from the unrounded s and y.  A row that
  * holds an infinity or NaN, or whose sum of squares exceeds float32, has an
  * out_scale or out that says so (NaN, or 0 from the infinite norm) and codes
- * that mean nothing.
+ * that mean nothing; so does a row of zeros with eps = 0.
  *   x             device [B x d] of dtype, row stride ld_x >= d.
  *   residual      the same, row stride ld_residual; NULL: s = x.
  *   weight        device [d] of dtype; NULL: the factor is 1.
@@ -473,6 +473,7 @@ typedef struct fh_w8a8 fh_w8a8; /* opaque */
  * Both copy into the handle's own layout (n k bytes, n rounded up to 16 and k
  * to 128, plus 4 n), wait for `stream`, and keep nothing of their arguments.
  * 1 <= n <= 2^30, 1 <= k < 131072 (the int32 sums of the product are exact).
+ * Not while `stream` is being captured.
  */
 fh_status fh_w8a8_create(const void* W, fh_dtype dtype, int64_t n, int64_t k, void* stream,
                          fh_w8a8** out);
@@ -480,7 +481,8 @@ fh_status fh_w8a8_create_codes(const int8_t* codes, const float* scales, int64_t
                                void* stream, fh_w8a8** out);
 
 /* fh_w8a8_destroy — release the handle (NULL is a no-op), after waiting for
- * the device to finish work that may still read it. */
+ * the device to finish work that may still read it.  Captured graphs that use
+ * it end with it. */
 void fh_w8a8_destroy(fh_w8a8* w);
 
 /* fh_w8a8_get — copy the codes [n x k] and scales [n] out (device). */

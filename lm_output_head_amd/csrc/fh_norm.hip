@@ -72,15 +72,27 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 // to nearest even, in the low bits of the sum.
 __device__ __forceinline__ uint32_t byte_of(float t) { return __float_as_uint(t + 12582912.f) & 0xFFu; }
 
-// Codes of one chunk; y r with r = 127 / max |y| (one multiplication for the
-// division, which only decides within a rounding of a half).
+// What y is multiplied by for its code: 127 / max |y| (one multiplication for the
+// division, which only decides within a rounding of a half), in two factors so
+// that it stays finite for the smallest rows.
+struct CodeScale {
+  float up, r;
+  __device__ explicit CodeScale(uint32_t top) {
+    const float t = __uint_as_float(top);
+    up = t < 0x1p-100f ? 0x1p64f : 1.f;
+    r = top ? 127.f / (t * up) : 0.f;
+  }
+  __device__ float of(float y) const { return y * up * r; }
+};
+
+// Codes of one chunk.
 template <int N>
-__device__ __forceinline__ void store_codes(int8_t* p, int64_t at, int64_t d, const float (&y)[N], float r) {
+__device__ __forceinline__ void store_codes(int8_t* p, int64_t at, int64_t d, const float (&y)[N], const CodeScale& c) {
   uint32_t w[N / 4];
 #pragma unroll
   for (int j = 0; j < N / 4; ++j)
-    w[j] = byte_of(y[4 * j] * r) | byte_of(y[4 * j + 1] * r) << 8 | byte_of(y[4 * j + 2] * r) << 16 |
-           byte_of(y[4 * j + 3] * r) << 24;
+    w[j] = byte_of(c.of(y[4 * j])) | byte_of(c.of(y[4 * j + 1])) << 8 | byte_of(c.of(y[4 * j + 2])) << 16 |
+           byte_of(c.of(y[4 * j + 3])) << 24;
   if (at + N <= d) {
     typedef uint32_t W __attribute__((ext_vector_type(N / 4), aligned(1)));
     W x;
@@ -113,7 +125,6 @@ __device__ __forceinline__ V across(V v, V* sh, Op op) {
 }
 
 __device__ __forceinline__ float scale_of(uint32_t top) { return __uint_as_float(top) / 127.f; }
-__device__ __forceinline__ float inverse_of(uint32_t top) { return top ? 127.f / __uint_as_float(top) : 0.f; }
 
 // W waves per row, C chunks per lane: the row stays in registers between its
 // one read and the writes.  A workgroup is max(4, W) waves.
@@ -173,10 +184,10 @@ __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void k_rmsnorm(NormArgs a, i
   if (!a.out_q) return;
   top = across<W>(wave_umax(top), top_sh, [](uint32_t p, uint32_t q) { return max(p, q); });
   if (lane == 0) a.out_scale[b] = scale_of(top);
-  const float rs = inverse_of(top);
+  const CodeScale cs(top);
 #pragma unroll
   for (int c = 0; c < C; ++c)
-    store_codes<N>(a.out_q + b * a.ld_q, (int64_t)N * (lane + 64 * W * c), d, y[c], rs);
+    store_codes<N>(a.out_q + b * a.ld_q, (int64_t)N * (lane + 64 * W * c), d, y[c], cs);
 }
 
 // Rows too long for the registers: three passes over the row, the later two from
@@ -201,21 +212,20 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_long(NormArgs a, int64_t B) {
     ss = across<W>(wave_sum(ss), sum_sh, [](float p, float q) { return p + q; });
     const float inv = 1.f / sqrtf(ss / (float)d + a.eps);
     auto norm_at = [&](int64_t i, float s) { return w ? s * inv * (a.offset + Elems<T>::get(w[i])) : s * inv; };
-    float rs = 0.f;
+    uint32_t top = 0u;
     if (a.out_q) {
-      uint32_t top = 0u;
       for (int64_t i = tid; i < d; i += 64 * W) top = max(top, abs_bits(norm_at(i, sum_at(i))));
       top = across<W>(wave_umax(top), top_sh, [](uint32_t p, uint32_t q) { return max(p, q); });
       if (tid == 0) a.out_scale[b] = scale_of(top);
-      rs = inverse_of(top);
     }
+    const CodeScale cs(top);
     // an element is read and written by one thread, x and residual before the
     // outputs that may be their own storage
     for (int64_t i = tid; i < d; i += 64 * W) {
       const float s = sum_at(i), y = norm_at(i, s);
       if (a.out) static_cast<T*>(a.out)[b * a.ld_out + i] = Elems<T>::put(y);
       if (a.out_residual) static_cast<T*>(a.out_residual)[b * a.ld_out_residual + i] = Elems<T>::put(s);
-      if (a.out_q) a.out_q[b * a.ld_q + i] = (int8_t)byte_of(y * rs);
+      if (a.out_q) a.out_q[b * a.ld_q + i] = (int8_t)byte_of(cs.of(y));
     }
     __syncthreads();  // sum_sh and top_sh are free for the next row
   }

@@ -142,32 +142,34 @@ __global__ __launch_bounds__(TH) void k_rules(RulesArgs a) {
   }
 
   // the first of the history and of the biases, on their way as well
-  const int32_t* h = a.history + b * a.ld_history;
+  const int32_t* h = a.history ? a.history + b * a.ld_history : nullptr;
+  // read to the row's capacity, so that the loads need not wait for its length
+  int32_t seen[kAhead][4];
+  auto load_history = [&](int64_t i) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      load_run<4, i32x4>(h, i + 4 * TH * u, a.history ? a.history_len : 0, (int32_t)-1, seen[u]);
+  };
+  load_history(4 * tid);
   int64_t nh = 0, np = 0, nb = 0;
   if (a.history) {
     nh = a.n_history ? (int64_t)a.n_history[b] : a.history_len;
     nh = min(max(nh, (int64_t)0), a.history_len);
     np = a.n_prompt ? min(max((int64_t)a.n_prompt[b], (int64_t)0), nh) : 0;
   }
-  int32_t seen[kAhead][4];
-  auto load_history = [&](int64_t i) {
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) load_run<4, i32x4>(h, i + 4 * TH * u, nh, (int32_t)-1, seen[u]);
-  };
-  load_history(4 * tid);
   int32_t bias_id = -1;
   float bias_add = 0.f;
   auto load_bias = [&](int64_t i) {
     bias_id = -1;
-    if (i < nb) {
+    if (i < a.bias_len) {
       bias_id = a.bias_ids[b * a.ld_bias + i];
       bias_add = a.bias[b * a.ld_bias + i];
     }
   };
   if (a.bias_ids) {
+    load_bias(tid);
     nb = a.n_bias ? (int64_t)a.n_bias[b] : a.bias_len;
     nb = min(max(nb, (int64_t)0), a.bias_len);
-    load_bias(tid);
   }
 
   int place[N];
@@ -190,7 +192,7 @@ __global__ __launch_bounds__(TH) void k_rules(RulesArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int p = sh.find(seen[u][e], base, width, a.v);
-          if (p >= 0) {
+          if (p >= 0 && i + 4 * TH * u + e < nh) {
             if (i + 4 * TH * u + e < np)
               atomicOr(&sh.count[p], kPrompt);
             else
@@ -225,7 +227,7 @@ __global__ __launch_bounds__(TH) void k_rules(RulesArgs a) {
     for (int64_t i0 = 0; i0 < nb; i0 += TH) {
       if (i0 > 0) load_bias(i0 + tid);
       __syncthreads();  // the logits are there, the list before is done with
-      const int mine = sh.find(bias_id, base, width, a.v);
+      const int mine = i0 + tid < nb ? sh.find(bias_id, base, width, a.v) : -1;
       const uint64_t in = __ballot(mine >= 0);
       const int at = 64 * wave + __popcll(in & ((1ull << lane) - 1));
       if (mine >= 0) {

@@ -9,7 +9,9 @@ non-OK status.  ``rmsnorm``, ``W8A8Head``, ``LogitRules`` and ``logits_apply``
 allocate outputs and workspaces on top of them.  Matrices may have any row
 stride; their rows are dense.  All tensors of a call are on one GPU, which need
 not be the current one; work goes to its current stream unless ``stream`` is
-given, and what the call allocates belongs to that stream.
+given, and what the call allocates belongs to that stream.  Inputs made on
+another stream have to be ready, and alive until the call's stream has passed
+it, as for any launch.
 """
 
 from __future__ import annotations

@@ -127,6 +127,22 @@ def test_zero_and_non_finite_rows():
     check(x[keep], None, None, 1e-6, 0.0, {k: v[keep] for k, v in got.items()})
 
 
+@pytest.mark.parametrize("d", [96, 40000])
+def test_smallest_rows_keep_their_codes(d):
+    """Rows whose largest |y| is near the smallest normal: 127 / max |y| is past
+    float32's range, the codes are not.  y's and the scale's last bits are of
+    2^-149, so the tolerances are absolute here."""
+    from lm_output_head_amd import rmsnorm
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(4, d, generator=g).cuda()
+    w = torch.full((d,), 1e-37, device="cuda")
+    got = rmsnorm(x, w, want_q=True)
+    y, _ = serve_oracle.rmsnorm(f64(x), None, f64(w), 1e-6, 0.0)
+    assert np.all(np.abs(f64(got["out"]) - y) <= 1e-4 * np.abs(y) + 2.0 ** -148)
+    q, top = f64(got["q"]), np.abs(y).max(1, keepdims=True)
+    assert np.all(np.abs(q - y * 127 / top) <= 0.5 + 0.02) and np.all(np.abs(q).max(1) == 127)
+
+
 def test_last_positions_of_a_batch():
     """x = hidden[:, -1] of [B x T x d] is taken without a copy."""
     from lm_output_head_amd import rmsnorm
