@@ -17,11 +17,11 @@ __device__ __forceinline__ float exp_from(float x, float m) {
   return x == m ? 1.f : __expf(x - m);
 }
 
-// z / T', held at the largest finite value where a finite z leaves the range (a
-// mask of the type's lowest value at a small T stays above -inf).
-__device__ __forceinline__ float scaled_logit(float z, float tprime) {
-  const float x = z / tprime;
-  return fabsf(x) == INFINITY && fabsf(z) < INFINITY ? copysignf(FLT_MAX, z) : x;
+// z / T' as z times 1 / T', held within the finite values where a finite z leaves
+// them (a mask of the type's lowest value at a small T stays above -inf).
+__device__ __forceinline__ float scaled_logit(float z, float inverse) {
+  const bool finite = fabsf(z) < INFINITY;  // false for NaN
+  return finite ? fminf(fmaxf(z * inverse, -FLT_MAX), FLT_MAX) : z;
 }
 
 __device__ __forceinline__ void choice_key(Part& p, float key, float z, int32_t id) {
@@ -61,53 +61,60 @@ __device__ __forceinline__ U4 token_words(uint64_t seed, uint32_t row, uint32_t 
   return U4{x, y, z, w};
 }
 
-// The exponential variate -ln u of a word (gumbel_from_word is -ln of it).
+// -log2 u of a word's uniform u (gumbel_from_word is -ln of it times ln 2); u is
+// exact and never below 2^-24, so the instruction needs no help.
 __device__ __forceinline__ float exponential_from_word(uint32_t w) {
-  return -logf(((float)(w >> 9) + 0.5f) * 1.1920928955078125e-07f);
+  return -__builtin_amdgcn_logf(fmaf((float)(w >> 9), 1.1920928955078125e-07f, 5.9604644775390625e-08f));
 }
 
-// A lane's N logits as a Part.  open(i): whether logit i counts; x(i): z / T';
-// word(i): its Philox word (sampling).  The largest x comes first, then the
+// A lane's N logits as a Part; what does not count is -inf.  word: Philox words
+// of the draws (sampling).  The largest x = z / T' comes first, then the
 // exponentials e = exp(x - m) that the LSE sums.  The draw is the same race in
-// another form: max of x - ln(-ln u) is max of e / (-ln u), so it needs one
-// logarithm more per logit and no division (e l' > e' l); the key itself is
-// formed for the winner alone, to be compared between lanes.  Logits come by
-// ascending id or compare ids; a tie stays with the smaller id.
-template <int N>
-__device__ __forceinline__ Part choose(const float (&z)[N], const int32_t (&id)[N], const bool (&open)[N],
-                                       bool sample, float tprime, const uint32_t (&word)[N]) {
+// another form: the largest x - ln(-ln u) is the largest e / (-ln u), so it needs
+// one logarithm more per logit and no division (e l' > e' l); the key itself is
+// formed for the winner alone, to be compared between lanes.  ORDERED: the ids
+// ascend, so a tie stays with the earlier one; else the ids are compared.
+template <int N, bool ORDERED>
+__device__ __forceinline__ Part choose(const float (&z)[N], const int32_t (&id)[N], bool sample, float inverse,
+                                       const uint32_t (&word)[N]) {
   Part p = part_empty();
-  float x[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    x[i] = open[i] ? (sample ? scaled_logit(z[i], tprime) : z[i]) : -INFINITY;
-    p.m = fmaxf(p.m, x[i]);
-  }
   if (sample) {
-    float be = 0.f, bl = 1.f, bx = -INFINITY;
+    float x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x[i] = scaled_logit(z[i], inverse);
+      p.m = fmaxf(p.m, x[i]);
+    }
+    const float shift = fabsf(p.m) < INFINITY ? p.m : 0.f;  // exp of +-inf is what it has to be
+    float be = 0.f, bl = 1.f;
     uint32_t bw = 0u;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float e = open[i] ? exp_from(x[i], p.m) : 0.f, l = exponential_from_word(word[i]);
+      const float e = __expf(x[i] - shift), l = exponential_from_word(word[i]);
       p.s += e;
       const float mine = e * bl, best = be * l;
-      if (mine > best || (mine == best && mine > 0.f && id[i] < p.id)) {
+      if (mine > best || (!ORDERED && mine == best && mine > 0.f && id[i] < p.id)) {
         be = e;
         bl = l;
-        bx = x[i];
         bw = word[i];
         p.z = z[i];
         p.id = id[i];
       }
     }
-    if (p.m == -INFINITY) p.id = 0x7FFFFFFF;  // nothing is left: all e are 1 by definition
-    p.key = p.id == 0x7FFFFFFF ? -INFINITY : bx + gumbel_from_word(bw);
+    if (be > 0.f) p.key = scaled_logit(p.z, inverse) + gumbel_from_word(bw);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      p.s += open[i] ? exp_from(x[i], p.m) : 0.f;
-      if (open[i]) choice_key(p, z[i], z[i], id[i]);
+      if (z[i] > p.key || (!ORDERED && z[i] == p.key && z[i] > -INFINITY && id[i] < p.id)) {
+        p.key = z[i];
+        p.id = id[i];
+      }
     }
+    p.z = p.key;
+    p.m = p.key;  // -inf or the largest; a NaN is neither
+    const float shift = fabsf(p.m) < INFINITY ? p.m : 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) p.s += __expf(z[i] - shift);
   }
   return p;
 }

@@ -71,14 +71,19 @@ struct Tables {
       for (int i = 4 * tid; i < kBits / 32; i += 4 * TH) *reinterpret_cast<i32x4a*>(&maybe[i]) = zero;
   }
   __device__ static uint32_t hash(int32_t id) { return ((uint32_t)id * 0x9E3779B1u) >> 16 & (kSize - 1); }
-  // the token's place, or -1
-  __device__ int find(int32_t t, int64_t base, int64_t width, int64_t v) const {
+  // whether the token may be in the tile: what most of a history fails
+  __device__ bool may_hold(int32_t t, int64_t base, int64_t width, int64_t v) const {
     if constexpr (DENSE) {
-      const uint32_t u = (uint32_t)t - (uint32_t)base;  // past width too where t is below base
-      return u < (uint32_t)width ? (int)u : -1;
+      return (uint32_t)t - (uint32_t)base < (uint32_t)width;  // past width too where t is below base
     } else {
-      if (t < 0 || (int64_t)t >= v) return -1;
-      if (!(maybe[(t & (kBits - 1)) >> 5] >> (t & 31) & 1u)) return -1;
+      return (uint32_t)t < (uint32_t)v && (maybe[(t & (kBits - 1)) >> 5] >> (t & 31) & 1u);
+    }
+  }
+  // the place of a token that may be in the tile, or -1
+  __device__ int find(int32_t t, int64_t base) const {
+    if constexpr (DENSE) {
+      return (int)((uint32_t)t - (uint32_t)base);
+    } else {
       for (uint32_t s = hash(t);; s = (s + 1) & (kSize - 1)) {
         const int32_t k = key[s];
         if (k == t) return (int)s;
@@ -187,12 +192,18 @@ __global__ __launch_bounds__(TH) void k_rules(RulesArgs a) {
   }
   if (a.history) {
     for (int64_t i = 4 * tid; i < nh; i += 4 * TH * kAhead) {
+      bool may[kAhead][4];  // all looked up before any is searched for
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          may[u][e] = sh.may_hold(seen[u][e], base, width, a.v) && i + 4 * TH * u + e < nh;
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int p = sh.find(seen[u][e], base, width, a.v);
-          if (p >= 0 && i + 4 * TH * u + e < nh) {
+          const int p = may[u][e] ? sh.find(seen[u][e], base) : -1;
+          if (p >= 0) {
             if (i + 4 * TH * u + e < np)
               atomicOr(&sh.count[p], kPrompt);
             else
@@ -227,7 +238,7 @@ __global__ __launch_bounds__(TH) void k_rules(RulesArgs a) {
     for (int64_t i0 = 0; i0 < nb; i0 += TH) {
       if (i0 > 0) load_bias(i0 + tid);
       __syncthreads();  // the logits are there, the list before is done with
-      const int mine = i0 + tid < nb ? sh.find(bias_id, base, width, a.v) : -1;
+      const int mine = i0 + tid < nb && sh.may_hold(bias_id, base, width, a.v) ? sh.find(bias_id, base) : -1;
       const uint64_t in = __ballot(mine >= 0);
       const int at = 64 * wave + __popcll(in & ((1ull << lane) - 1));
       if (mine >= 0) {
@@ -288,7 +299,7 @@ __global__ __launch_bounds__(TH) void k_rules(RulesArgs a) {
         }
       }
     }
-    Part part = wave_choice(choose<N>(z, id, open, a.token_sample != 0, a.tprime, word));
+    Part part = wave_choice(choose<N, DENSE>(z, id, a.token_sample != 0, a.inverse_t, word));
     if (lane == 0) sh.parts[wave] = part;
     __syncthreads();
     if (wave == 0) {

@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstdint>
 #include <exception>
+#include <limits>
 #include <new>
 #include <string>
 
@@ -63,6 +64,10 @@ fh_status check_choice(int mode, float temperature) {
   if (mode == FH_TOKEN_SAMPLE && !(temperature > 0.f && std::isfinite(temperature)))
     return fail(FH_EINVAL, "sampling needs a finite temperature > 0");
   return FH_OK;
+}
+
+float inverse_of(float temperature) {
+  return (float)std::min(1.0 / (double)temperature, (double)std::numeric_limits<float>::max());
 }
 
 fh_status check_workspace(const void* workspace, int64_t bytes, int64_t need) {
@@ -306,7 +311,7 @@ fh_status fh_w8a8_forward(const fh_w8a8* w, const int8_t* q, int64_t ld_q, const
     a.out = out_logits;
     a.ld_out = ld_logits;
     a.token_sample = mode == FH_TOKEN_SAMPLE;
-    a.tprime = a.token_sample ? temperature : 1.f;
+    a.inverse_t = a.token_sample ? inverse_of(temperature) : 1.f;
     a.seed = seed;
     a.parts = reinterpret_cast<fh::Part*>(static_cast<char*>(workspace) + copy_bytes(w, q, ld_q, B));
     if (r == hipSuccess) r = fh::launch_w8a8(a, false, true, st);
@@ -398,7 +403,7 @@ fh_status fh_logits_apply(const float* logits, int64_t ld_logits, const int32_t*
     a.mask_rows = l.mask_rows;
     a.mask_row = l.mask_row;
     a.token_sample = mode == FH_TOKEN_SAMPLE;
-    a.tprime = a.token_sample ? temperature : 1.f;
+    a.inverse_t = a.token_sample ? inverse_of(temperature) : 1.f;
     a.seed = seed;
     a.out = out_logits;
     a.ld_out = ld_out;

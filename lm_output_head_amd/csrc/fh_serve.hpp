@@ -41,7 +41,7 @@ struct W8A8Args {
   int64_t ld_out;
   // head
   int token_sample;
-  float tprime;
+  float inverse_t;       // 1 / T'
   uint64_t seed;
   Part* parts;           // [B x w8a8_parts]
 };
@@ -80,7 +80,7 @@ struct RulesArgs {
   int64_t ld_mask, mask_rows;
   const int32_t* mask_row;
   int token_sample;
-  float tprime;
+  float inverse_t;       // 1 / T'
   uint64_t seed;
   float* out;            // or null
   int64_t ld_out;

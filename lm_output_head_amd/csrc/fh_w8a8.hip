@@ -79,7 +79,6 @@ template <int FN>
 __device__ __forceinline__ Part choose_tile(const W8A8Args& a, const float (&z)[FN][4], int64_t q, int64_t t0, int g) {
   float v[4 * FN];
   int32_t id[4 * FN];
-  bool open[4 * FN];
   uint32_t word[4 * FN];
 #pragma unroll
   for (int m = 0; m < FN; ++m) {
@@ -88,13 +87,12 @@ __device__ __forceinline__ Part choose_tile(const W8A8Args& a, const float (&z)[
     if (a.token_sample) words = token_words(a.seed, (uint32_t)q, (uint32_t)(j >> 2));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[4 * m + i] = z[m][i];
+      v[4 * m + i] = j + i < a.n ? z[m][i] : -INFINITY;
       id[4 * m + i] = (int32_t)(j + i);
-      open[4 * m + i] = j + i < a.n;
       word[4 * m + i] = u4_word(words, i);
     }
   }
-  return choose<4 * FN>(v, id, open, a.token_sample != 0, a.tprime, word);
+  return choose<4 * FN, true>(v, id, a.token_sample != 0, a.inverse_t, word);
 }
 
 // Few tokens, or too few rows for a tile per CU: 16 FN rows of W are streamed by
