@@ -310,9 +310,14 @@ __global__ __launch_bounds__(TH) void k_rules(RulesArgs a) {
 }
 
 // Tiles of a call: large ones walk the history less often, small ones spread few
-// rows over the CUs; the large one where it leaves two workgroups per CU.
+// rows over the CUs; the large one where it leaves two workgroups per CU (64 x
+// 151936 sampled: 37 us with tiles of 4096; 1 x 128256: 6.5 us with 1024, 12.9
+// with 4096).  Candidates' tiles have a thread per candidate or two, so that the
+// history, which each of them searches for, is short per thread (8 x 8192 with
+// 32768 of history: 36 us with 512 threads for 512 candidates, 69 with 256 for
+// 256; 64 x 8192 with 8192: 27 us with 512 threads for 1024, 37 with 256).
 int tile_of(int64_t B, int64_t n, bool dense) {
-  const int large = dense ? 4096 : 1024, small = dense ? 1024 : 256;
+  const int large = dense ? 4096 : 1024, small = dense ? 1024 : 512;
   return B * ((n + large - 1) / large) >= 512 ? large : small;
 }
 
@@ -329,11 +334,11 @@ hipError_t launch_rules(const RulesArgs& a, int64_t B, hipStream_t st) {
     case 4096: hipLaunchKernelGGL((k_rules<true, 256, 4, 4>), grid, dim3(256), 0, st, a); break;
     case 1024:
       if (a.ids)
-        hipLaunchKernelGGL((k_rules<false, 256, 4, 1>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((k_rules<false, 512, 1, 2>), grid, dim3(512), 0, st, a);
       else
         hipLaunchKernelGGL((k_rules<true, 256, 4, 1>), grid, dim3(256), 0, st, a);
       break;
-    default: hipLaunchKernelGGL((k_rules<false, 256, 1, 1>), grid, dim3(256), 0, st, a);
+    default: hipLaunchKernelGGL((k_rules<false, 512, 1, 1>), grid, dim3(512), 0, st, a);
   }
   return hipGetLastError();
 }
