@@ -472,7 +472,7 @@ typedef struct fh_w8a8 fh_w8a8; /* opaque */
  * [n] float as they are, both device and dense.
  * Both copy into the handle's own layout (n k bytes, n rounded up to 16 and k
  * to 128, plus 4 n), wait for `stream`, and keep nothing of their arguments.
- * 1 <= n <= 2^30, 1 <= k < 131072 (the int32 sums of the product are exact).
+ * 1 <= n <= 2^27, 1 <= k < 131072 (the int32 sums of the product are exact).
  * Not while `stream` is being captured.
  */
 fh_status fh_w8a8_create(const void* W, fh_dtype dtype, int64_t n, int64_t k, void* stream,

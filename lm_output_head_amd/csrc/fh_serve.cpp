@@ -45,7 +45,8 @@ R guarded(R failed, F&& body) noexcept {
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxWidth = int64_t(1) << 30;    // n and v: grids stay below 2^32 threads
+constexpr int64_t kMaxWidth = int64_t(1) << 30;    // n and v: grids stay below 2^32 threads,
+constexpr int64_t kMaxChannels = int64_t(1) << 27;  // and the product's, a wave or more per 16 channels
 constexpr int64_t kMaxK = (int64_t(1) << 17) - 1;  // 128^2 k < 2^31
 constexpr int64_t kMaxElems = int64_t(1) << 60;    // rows * stride stays far inside int64
 
@@ -88,7 +89,7 @@ void free_w8a8(fh_w8a8* w) {
 fh_status create_w8a8(const int8_t* codes, const float* scales, const void* W, fh_dtype dtype, int64_t n, int64_t k,
                       hipStream_t st, fh_w8a8** out) {
   if (!out) return fail(FH_EINVAL, "out is NULL");
-  if (n < 1 || n > kMaxWidth) return fail(FH_EINVAL, "n outside [1, 2^30]");
+  if (n < 1 || n > kMaxChannels) return fail(FH_EINVAL, "n outside [1, 2^27]");
   if (k < 1 || k > kMaxK) return fail(FH_EINVAL, "k outside [1, 131071]");
   fh_w8a8* w = new (std::nothrow) fh_w8a8();
   if (!w) return fail(FH_ENOMEM, "host allocation failed");

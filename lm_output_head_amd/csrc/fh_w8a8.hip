@@ -32,7 +32,7 @@ __device__ __forceinline__ i32x4 mfma_i8(i32x4 a, i32x4 b, i32x4 c) {
 
 // N results of one token from channel j up, those below n, in 16 (or 8) bytes.
 // STREAM: past the caches, which the operands need (64 x 151936 float results
-// beside 389 MB of weights: 95 -> 85 us; 4096 x 10240 bf16: 138 -> 128 us).
+// beside 389 MB of weights: 95 -> 85 us; 4096 x 10240 bf16: 144 -> 132 us).
 template <typename T, int N, bool STREAM>
 __device__ __forceinline__ void store_run(T* o, int64_t j, int64_t n, const T* v) {
   typedef T V __attribute__((ext_vector_type(N), aligned(sizeof(T))));
@@ -200,27 +200,28 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// More tokens: a workgroup of WN x WM waves covers 16 FN WN rows by 16 FT WM
-// tokens.  The tokens' block of kStage steps of k is staged in LDS in fragment
+// More tokens: a workgroup of WN waves covers 16 FN WN rows by 16 FT tokens.  The tokens' block of kStage steps of k is staged in LDS in fragment
 // order (a fragment is read as one contiguous 1 KB), double buffered and loaded
 // one block ahead; each wave's rows of W go straight to registers (fragment
 // order, one contiguous 1 KB per load), two blocks ahead.  ONCE: the rows are
 // read by this workgroup alone and pass the caches by (128 x 128256 x 2048:
-// 65 -> 62 us; where token tiles share them it costs 10 to 20%).
+// 65 -> 62 us; where token tiles share them it costs 10%).
 //
-// The 128-token tile is held to 128 registers, two workgroups per CU: one's
-// results overlap the other's products (head of 128 x 128256 sampled 102 -> 88 us).
-template <int FT, int FN, int WN, int WM, bool ONCE, bool BF16, bool HEAD>
-__global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(WN == 8 ? 4 : 1))) void k_w8a8_tile(W8A8Args a, int n_tiles, int q_tiles) {
-  constexpr int kStage = kStepPad, kW = WN * WM, kFrags = FT * WM * kStage;  // fragments of a token block
-  constexpr int kOwn = (kFrags + kW - 1) / kW;            // of them, this wave's to stage
+// Tiles of eight waves are held to 128 registers, two workgroups per CU: one's
+// results overlap the other's products (head of 128 x 128256 sampled 102 -> 88
+// us; with the 250 registers of a 256 x 256 tile, one per CU, 4096 x 10240 x 2560
+// took 137 us, not 119).
+template <int FT, int FN, int WN, bool ONCE, bool BF16, bool HEAD>
+__global__ __launch_bounds__(64 * WN) __attribute__((amdgpu_waves_per_eu(WN == 8 ? 4 : 1))) void k_w8a8_tile(W8A8Args a, int n_tiles, int q_tiles) {
+  constexpr int kStage = kStepPad, kFrags = FT * kStage;  // fragments of a token block
+  constexpr int kOwn = (kFrags + WN - 1) / WN;       // of them, this wave's to stage
   constexpr int kBlock = kFrags * 64;
   typedef typename Out<BF16>::T T;
-  // results of 16 tokens of each token group on their way out, two buffers
-  constexpr int kRow = 16 * FN * WN + 16 / (int)sizeof(T), kTurn = 16 * WM * kRow;
+  // results of 16 tokens on their way out, two buffers
+  constexpr int kRow = 16 * FN * WN + 16 / (int)sizeof(T), kTurn = 16 * kRow;
   constexpr int kShared = 2 * kBlock * 16, kStaged = 2 * kTurn * (int)sizeof(T);
   __shared__ __attribute__((aligned(16))) char smem[kShared > kStaged ? kShared : kStaged];
-  __shared__ Part sP[HEAD ? kW : 1][HEAD ? 16 * FT : 1];
+  __shared__ Part sP[HEAD ? WN : 1][HEAD ? 16 * FT : 1];
   i32x4* sQ = reinterpret_cast<i32x4*>(smem);
 
   // workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles, token
@@ -231,25 +232,24 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(WN
   const int nt = tile / q_tiles, qt = tile % q_tiles;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wn = wave % WN, wm = wave / WN;
   const int g = lane >> 4, col = lane & 15;
   const int64_t rows = (a.n + 15) / 16;
-  const int64_t t0 = ((int64_t)nt * WN + wn) * FN;
-  const int q0 = qt * 16 * FT * WM;
+  const int64_t t0 = ((int64_t)nt * WN + wave) * FN;
+  const int q0 = qt * 16 * FT;
   const int steps = w_steps(a.k), chunks = (a.k + 15) / 16, blocks = steps / kStage;
 
   const i32x4* wp[FN];
 #pragma unroll
   for (int m = 0; m < FN; ++m) wp[m] = static_cast<const i32x4*>(a.W) + min(t0 + m, rows - 1) * steps * 64 + lane;
-  // this wave's fragments of a block: f = step * FT WM + token tile
+  // this wave's fragments of a block: f = step * FT + token tile
   const int8_t* qp[kOwn];
   int qs[kOwn];
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
-    const int f = min(wave + i * kW, kFrags - 1);
+    const int f = min(wave + i * WN, kFrags - 1);
     // a token past the last stands in as the last, its results are dropped
-    qp[i] = a.q + (int64_t)min(q0 + 16 * (f % (FT * WM)) + col, a.B - 1) * a.ld_q;
-    qs[i] = f / (FT * WM);
+    qp[i] = a.q + (int64_t)min(q0 + 16 * (f % FT) + col, a.B - 1) * a.ld_q;
+    qs[i] = f / FT;
   }
   i32x4 qr[kOwn];
   auto load_q = [&](int blk) {
@@ -263,7 +263,7 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(WN
   auto store_q = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < kOwn; ++i)
-      if (kFrags % kW == 0 || wave + i * kW < kFrags) sQ[buf * kBlock + (wave + i * kW) * 64 + lane] = qr[i];
+      if (kFrags % WN == 0 || wave + i * WN < kFrags) sQ[buf * kBlock + (wave + i * WN) * 64 + lane] = qr[i];
   };
   i32x4 wf[2][kStage][FN];
   auto load_w = [&](int blk, i32x4 (&dst)[kStage][FN]) {
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(WN
     for (int s = 0; s < kStage; ++s) {
       i32x4 qf[FT];
 #pragma unroll
-      for (int t = 0; t < FT; ++t) qf[t] = sQ[buf * kBlock + ((s * WM + wm) * FT + t) * 64 + lane];
+      for (int t = 0; t < FT; ++t) qf[t] = sQ[buf * kBlock + (s * FT + t) * 64 + lane];
 #pragma unroll
       for (int t = 0; t < FT; ++t)
 #pragma unroll
@@ -331,12 +331,11 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(WN
   float ws[FN][4];
   load_scales<FN>(a, t0, g, ws);
   T* turn = reinterpret_cast<T*>(smem);
-  const int qw = q0 + 16 * FT * wm;
 #pragma unroll
   for (int t = 0; t < FT; ++t) {
-    const int64_t q = qw + 16 * t + col;
+    const int64_t q = q0 + 16 * t + col;
     const float qsc = q < a.B ? a.qs[q] : 0.f;
-    T* row = turn + (t & 1) * kTurn + (16 * wm + col) * kRow + 16 * FN * wn + 4 * g;
+    T* row = turn + (t & 1) * kTurn + col * kRow + 16 * FN * wave + 4 * g;
     float z[FN][4];
 #pragma unroll
     for (int m = 0; m < FN; ++m) {
@@ -356,23 +355,21 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(WN
       lds_barrier();  // the other buffer is read until the barrier after this one
       constexpr int kPer = 16 / (int)sizeof(T), kRuns = 16 * FN * WN / kPer;  // 16-byte runs of a token
 #pragma unroll
-      for (int c = 64 * wn + lane; c < 16 * kRuns; c += 64 * WN) {
+      for (int c = tid; c < 16 * kRuns; c += 64 * WN) {
         const int tok = c / kRuns, at = c % kRuns * kPer;
-        const int64_t b = qw + 16 * t + tok;
+        const int64_t b = q0 + 16 * t + tok;
         if (b < a.B)
           store_run<T, kPer, true>(static_cast<T*>(a.out) + b * a.ld_out, (int64_t)nt * (16 * FN * WN) + at, a.n,
-                             turn + (t & 1) * kTurn + (16 * wm + tok) * kRow + at);
+                             turn + (t & 1) * kTurn + tok * kRow + at);
       }
     }
   }
   if (HEAD) {
     __syncthreads();
-    for (int i = tid; i < 16 * FT * WM; i += 64 * kW) {
-      const int m = i / (16 * FT), c = i % (16 * FT);
-      if (q0 + i >= a.B) break;
-      Part p = sP[m * WN][c];
+    for (int i = tid; i < 16 * FT && q0 + i < a.B; i += 64 * WN) {
+      Part p = sP[0][i];
 #pragma unroll
-      for (int w = 1; w < WN; ++w) p = choice_merge(p, sP[m * WN + w][c]);
+      for (int w = 1; w < WN; ++w) p = choice_merge(p, sP[w][i]);
       a.parts[(int64_t)(q0 + i) * n_tiles + nt] = p;
     }
   }
@@ -486,7 +483,7 @@ unsigned grid_of(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256
 
 // How a call is cut up: a tile of k_w8a8_tile (named by its tokens), or a shape
 // of k_w8a8_few.
-enum Kind { kFew16Rows8, kFew16Rows4, kFew32Rows2, kTokens32Rows8, kTokens32Rows4, k32, k64, k128, k256 };
+enum Kind { kFew16Rows8, kFew16Rows4, kFew32Rows2, kTokens32Rows8, kTokens32Rows4, k32, k64, k128 };
 struct Plan {
   Kind kind;
   int rows, tokens;  // of a workgroup
@@ -498,22 +495,22 @@ struct Plan {
 // rows reads its tokens once per KB of W, one of 32 half as often: 42.0 and 46.8
 // us for 1 x 128256 x 2048, 59.3 and 49.9 for 16; the head, whose choice one wave
 // of a group makes, 1 x 262144 x 1152 66.6 and 58.5.
-// More: the largest tile that leaves a workgroup for every CU and less than half
-// its tokens empty; the head's choice does not fit the registers beside the sums
-// of k256.  Where even the smallest leaves CUs idle, waves share k (32 x 4096 x
+// More: the largest tile that about fills the CUs and leaves less than half its
+// tokens empty (4096 x 10240 x 2560: 119 us with 256 rows x 128 tokens, 146 with
+// 256 x 64, 251 with 128 x 32; 512 x 4096 x 4096, 64, 128 and 512 tiles: 36, 24
+// and 22).  Where even the smallest leaves CUs idle, waves share k (32 x 4096 x
 // 4096 18.4 and 8.1 us, 128 x 4096 x 4096 18.6 and 12.7; with 224 tiles the
 // smallest is the better one, 23.5 and 33.8 for 32 x 28672 x 4096).
 Plan plan_of(int64_t n, int64_t B, bool head) {
+  constexpr int kFull = 180;  // workgroups that about fill the 256 CUs
   if (B <= 16) {
     const int64_t tiles = (n + 15) / 16;
     if (tiles < 512) return Plan{kFew16Rows8, 16, 16};
     if (tiles < 2048 || (B <= 4 && !head)) return Plan{kFew16Rows4, 16, 16};
     return Plan{kFew32Rows2, 64, 16};
   }
-  for (const Plan& p : {Plan{k256, 256, 256}, Plan{k128, 256, 128}, Plan{k64, 128, 64}})
-    if (!(head && p.kind == k256) && 2 * B > p.tokens && p.tiles(n, B) >= 256) return p;
-  const Plan least{k32, 128, 32};
-  if (least.tiles(n, B) >= 192) return least;
+  for (const Plan& p : {Plan{k128, 256, 128}, Plan{k64, 256, 64}, Plan{k32, 128, 32}})
+    if (2 * B > p.tokens && p.tiles(n, B) >= kFull) return p;
   return B <= 32 ? Plan{kTokens32Rows8, 16, 32} : Plan{kTokens32Rows4, 32, 32};
 }
 
@@ -524,15 +521,15 @@ void launch_few(const W8A8Args& a, hipStream_t st) {
   hipLaunchKernelGGL((k_w8a8_few<FT, FN, KW, G, BF16, HEAD>), grid, dim3(64 * KW * G), 0, st, a);
 }
 
-template <int FT, int FN, int WN, int WM, bool BF16, bool HEAD>
+template <int FT, int FN, int WN, bool BF16, bool HEAD>
 void launch_tile(const W8A8Args& a, hipStream_t st) {
-  constexpr int kRows = 16 * FN * WN, kTokens = 16 * FT * WM;
+  constexpr int kRows = 16 * FN * WN, kTokens = 16 * FT;
   const int nt = (int)((a.n + kRows - 1) / kRows), qt = (a.B + kTokens - 1) / kTokens;
-  const dim3 grid((unsigned)(((int64_t)nt * qt + 7) / 8 * 8)), block(64 * WN * WM);
+  const dim3 grid((unsigned)(((int64_t)nt * qt + 7) / 8 * 8)), block(64 * WN);
   if (qt == 1)
-    hipLaunchKernelGGL((k_w8a8_tile<FT, FN, WN, WM, true, BF16, HEAD>), grid, block, 0, st, a, nt, qt);
+    hipLaunchKernelGGL((k_w8a8_tile<FT, FN, WN, true, BF16, HEAD>), grid, block, 0, st, a, nt, qt);
   else
-    hipLaunchKernelGGL((k_w8a8_tile<FT, FN, WN, WM, false, BF16, HEAD>), grid, block, 0, st, a, nt, qt);
+    hipLaunchKernelGGL((k_w8a8_tile<FT, FN, WN, false, BF16, HEAD>), grid, block, 0, st, a, nt, qt);
 }
 
 template <bool BF16, bool HEAD>
@@ -543,11 +540,9 @@ void launch_kind(const W8A8Args& a, hipStream_t st) {
     case kFew32Rows2: return launch_few<1, 2, 2, 2, BF16, HEAD>(a, st);
     case kTokens32Rows8: return launch_few<2, 1, 8, 1, BF16, HEAD>(a, st);
     case kTokens32Rows4: return launch_few<2, 2, 4, 1, BF16, HEAD>(a, st);
-    case k32: return launch_tile<2, 2, 4, 1, BF16, HEAD>(a, st);
-    case k64: return launch_tile<4, 2, 4, 1, BF16, HEAD>(a, st);
-    case k128: return launch_tile<8, 2, 8, 1, BF16, HEAD>(a, st);
-    case k256:
-      if constexpr (!HEAD) launch_tile<8, 4, 4, 2, BF16, HEAD>(a, st);
+    case k32: return launch_tile<2, 2, 4, BF16, HEAD>(a, st);
+    case k64: return launch_tile<4, 2, 8, BF16, HEAD>(a, st);
+    case k128: return launch_tile<8, 2, 8, BF16, HEAD>(a, st);
   }
 }
 

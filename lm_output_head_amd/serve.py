@@ -270,6 +270,13 @@ def fh_w8a8_forward(w, q, q_scale, mode, temperature, seed, out_token, out_token
                                           _ptr(out_logits), ld_out, ws, ws_bytes, _stream(dev)))
 
 
+def _choice_outputs(t, B):
+    """token [B] int32, token_logit and lse [B] float32 on t's GPU, rows of one
+    allocation (a third of the host's time of three)."""
+    token, logit, lse = t.new_empty((3, B), dtype=torch.float32).unbind(0)
+    return token.view(torch.int32), logit, lse
+
+
 class W8A8Head:
     """A dense head (or any linear layer) with int8 weights and activations:
     the rows of E quantised here, or int8 codes and scales as they are."""
@@ -335,9 +342,7 @@ class W8A8Head:
         ld_q, size = self._inputs(q, q_scale, 1)
         B = q.shape[0]
         with _on(self.device, stream):
-            token = q.new_empty((B,), dtype=torch.int32)
-            logit = q.new_empty((B,), dtype=torch.float32)
-            lse = q.new_empty((B,), dtype=torch.float32)
+            token, logit, lse = _choice_outputs(q, B)
             out = {"token": token, "token_logit": logit, "lse": lse}
             logits = None
             if want_logits:
@@ -483,12 +488,11 @@ def logits_apply(logits, rules=None, *, ids=None, v=None, mode: int = 0, tempera
     size = 0
     with _on(dev, stream):
         if out is None:
-            out = logits.new_empty((B, n))
+            out = torch.empty_like(logits)
         got = {"logits": out}
         if want_token:
-            got["token"] = token = logits.new_empty((B,), dtype=torch.int32)
-            got["token_logit"] = logit = logits.new_empty((B,))
-            got["lse"] = lse = logits.new_empty((B,))
+            token, logit, lse = _choice_outputs(logits, B)
+            got["token"], got["token_logit"], got["lse"] = token, logit, lse
             size = _size(lib.fh_logits_workspace(B, n))
             ws = logits.new_empty((size,), dtype=torch.uint8)
         check(lib.fh_logits_apply(logits.data_ptr(), ld_z, _ptr(ids), ld_ids, B, n, v, struct, mode, temperature, seed,

@@ -65,7 +65,7 @@ def test_norm_refusals(lib, kw, needle):
     ((A, 3, 8, 64), "dtype"),
     ((P((1 << 20) + 1), 1, 8, 64), "aligned"),
     ((A, 1, 0, 64), "n outside"),
-    ((A, 1, (1 << 30) + 1, 64), "n outside"),
+    ((A, 1, (1 << 27) + 1, 64), "n outside"),
     ((A, 1, 8, 0), "k outside"),
     ((A, 1, 8, 1 << 17), "k outside"),
 ])
