@@ -21,7 +21,7 @@ namespace {
 
 constexpr uint32_t kPrompt = 0x80000000u;
 constexpr int32_t kFree = -1;
-constexpr int kAhead = 4;  // groups of four history ids that a thread loads at once
+constexpr int kAhead = 3;  // groups of four history ids that a thread loads at once
 
 typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4), aligned(4)));
@@ -103,7 +103,7 @@ struct Tables {
 
 // G runs of W consecutive logits per thread: a tile is TH W G.
 template <bool DENSE, int TH, int W, int G>
-__global__ __launch_bounds__(TH) void k_rules(RulesArgs a) {
+__global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(6))) void k_rules(RulesArgs a) {
   constexpr int kTile = TH * W * G, N = W * G;
   typedef Tables<DENSE, kTile, TH> Table;
   static_assert((Table::kSize & (Table::kSize - 1)) == 0 && Table::kSize <= 65536, "the hash masks 16 bits");
@@ -278,7 +278,9 @@ __global__ __launch_bounds__(TH) void k_rules(RulesArgs a) {
     for (int j = 0; j < G; ++j) {
       const int64_t at = W * (tid + (int64_t)TH * j);
       if (W == 4 && at + 4 <= width)
-        *reinterpret_cast<f32x4*>(out + at) = f32x4{z[W * j], z[W * j + 1 % W], z[W * j + 2 % W], z[W * j + 3 % W]};
+        // past the caches: the logits are looked at seldom, once the token is chosen
+        __builtin_nontemporal_store(f32x4{z[W * j], z[W * j + 1 % W], z[W * j + 2 % W], z[W * j + 3 % W]},
+                                    reinterpret_cast<f32x4*>(out + at));
       else
 #pragma unroll
         for (int e = 0; e < W; ++e)
