@@ -584,7 +584,8 @@ int64_t fh_logits_workspace(int64_t B, int64_t n);
  *   out_token_logit, out_lse  [B] float or NULL: its logit after the rules
  *            (-inf for token -1); log sum exp(z / T') over the row (-inf where
  *            nothing is left, NaN where an allowed logit is NaN).
- * 1 <= B <= 65535, 1 <= n, v <= 2^30.  At least one output.
+ * 1 <= B <= 65535, 1 <= n, v <= 2^30, lists of at most 2^30 places.  At least
+ * one output.
  */
 fh_status fh_logits_apply(const float* logits, int64_t ld_logits, const int32_t* ids,
                           int64_t ld_ids, int64_t B, int64_t n, int64_t v,

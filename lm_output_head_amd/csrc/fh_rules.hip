@@ -13,6 +13,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "fh_choice.hpp"
 #include "fh_serve.hpp"
 
@@ -21,23 +23,26 @@ namespace {
 
 constexpr uint32_t kPrompt = 0x80000000u;
 constexpr int32_t kFree = -1;
-constexpr int kAhead = 3;  // groups of four history ids that a thread loads at once
+constexpr int kAhead = 2;  // groups of four history ids that a thread loads at once
 
 typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef int32_t i32x4a __attribute__((ext_vector_type(4)));
 
-// W (1 or 4) consecutive elements at i, those below n; `other` past it.
-template <int W, typename V, typename T>
-__device__ __forceinline__ void load_run(const T* p, int64_t i, int64_t n, T other, T (&v)[W]) {
-  if (W == 4 && i + 4 <= n) {
-    const V x = *reinterpret_cast<const V*>(p + i);
+// W (1 or 4) consecutive elements at i, those below n; `other` past it.  ALL: n
+// reaches past them.
+template <int W, bool ALL, typename V, typename T>
+__device__ __forceinline__ void load_run(const T* p, int i, int n, T other, T (&v)[W]) {
+  if constexpr (W == 4) {
+    if (ALL || i + 4 <= n) {
+      const V x = *reinterpret_cast<const V*>(p + i);
 #pragma unroll
-    for (int e = 0; e < W; ++e) v[e] = x[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < W; ++e) v[e] = i + e < n ? p[i + e] : other;
+      for (int e = 0; e < 4; ++e) v[e] = x[e];
+      return;
+    }
   }
+#pragma unroll
+  for (int e = 0; e < W; ++e) v[e] = ALL || i + e < n ? p[i + e] : other;
 }
 
 // DENSE: a word per token of the tile, its count and later its logit.  Else a
@@ -72,7 +77,7 @@ struct Tables {
   }
   __device__ static uint32_t hash(int32_t id) { return ((uint32_t)id * 0x9E3779B1u) >> 16 & (kSize - 1); }
   // whether the token may be in the tile: what most of a history fails
-  __device__ bool may_hold(int32_t t, int64_t base, int64_t width, int64_t v) const {
+  __device__ bool may_hold(int32_t t, int base, int width, int v) const {
     if constexpr (DENSE) {
       return (uint32_t)t - (uint32_t)base < (uint32_t)width;  // past width too where t is below base
     } else {
@@ -80,7 +85,7 @@ struct Tables {
     }
   }
   // the place of a token that may be in the tile, or -1
-  __device__ int find(int32_t t, int64_t base) const {
+  __device__ int find(int32_t t, int base) const {
     if constexpr (DENSE) {
       return (int)((uint32_t)t - (uint32_t)base);
     } else {
@@ -101,80 +106,96 @@ struct Tables {
   }
 };
 
-// G runs of W consecutive logits per thread: a tile is TH W G.
+// G runs of W consecutive logits per thread: a tile is TH W G.  Held to the
+// registers of six waves per SIMD (64 x 151936 sampled: 41 us at five, 37 at six).
 template <bool DENSE, int TH, int W, int G>
 __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(6))) void k_rules(RulesArgs a) {
-  constexpr int kTile = TH * W * G, N = W * G;
+  constexpr int kTile = TH * W * G, N = W * G, kBatch = 4 * TH * kAhead;  // ids of the history at once
   typedef Tables<DENSE, kTile, TH> Table;
   static_assert((Table::kSize & (Table::kSize - 1)) == 0 && Table::kSize <= 65536, "the hash masks 16 bits");
   static_assert(!DENSE || W == 4, "a Philox block and a mask word serve four tokens of a dense row");
   __shared__ Table sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t b = blockIdx.y, base = (int64_t)blockIdx.x * kTile;
-  const int64_t width = min((int64_t)kTile, a.n - base);
+  const int64_t b = blockIdx.y;
+  const int base = (int)blockIdx.x * kTile, v = a.v;
+  const int width = min(kTile, a.n - base);
+  const bool full = width == kTile;
 
-  // this thread's logits W (tid + TH j) .. + W - 1 of the tile and their ids
+  // this thread's logits W (tid + TH j) .. + W - 1 of the tile and their ids;
+  // what is past the tile or no token is -inf from here on
   float z[N];
   int32_t id[N];
-#pragma unroll
-  for (int j = 0; j < G; ++j) {
-    const int64_t at = W * (tid + (int64_t)TH * j);
-    float v[W];
-    int32_t t[W];
-    load_run<W, f32x4>(a.z + b * a.ld_z + base, at, width, -INFINITY, v);
-    if constexpr (!DENSE) load_run<W, i32x4>(a.ids + b * a.ld_ids + base, at, width, (int32_t)-1, t);
-#pragma unroll
-    for (int e = 0; e < W; ++e) {
-      z[W * j + e] = v[e];
-      id[W * j + e] = DENSE ? (int32_t)(base + at + e) : t[e];
-    }
-  }
   bool open[N];
+  const float* zb = a.z + b * a.ld_z + base;
+  auto load_tile = [&](auto all) {
+    constexpr bool ALL = decltype(all)::value;
 #pragma unroll
-  for (int i = 0; i < N; ++i) open[i] = DENSE ? id[i] < a.n : id[i] >= 0 && (int64_t)id[i] < a.v;
+    for (int j = 0; j < G; ++j) {
+      const int at = W * (tid + TH * j);
+      float x[W];
+      int32_t t[W];
+      load_run<W, ALL, f32x4>(zb, at, width, -INFINITY, x);
+      if constexpr (!DENSE) load_run<W, ALL, i32x4>(a.ids + b * a.ld_ids + base, at, width, (int32_t)-1, t);
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        const int i = W * j + e;
+        z[i] = x[e];
+        id[i] = DENSE ? base + at + e : t[e];
+        open[i] = DENSE ? ALL || at + e < width : (uint32_t)t[e] < (uint32_t)v;
+      }
+    }
+  };
+  if (full)
+    load_tile(std::true_type());
+  else
+    load_tile(std::false_type());
 
   // the row's mask, a word for four consecutive tokens of a dense row
   const uint32_t* mask = nullptr;
   if (a.mask) {
-    const int64_t r = a.mask_row ? (int64_t)a.mask_row[b] : b;
+    const int r = a.mask_row ? a.mask_row[b] : (int)b;
     if (r >= 0 && r < a.mask_rows) mask = a.mask + r * a.ld_mask;
   }
   uint32_t allow[DENSE ? G : N];
 #pragma unroll
   for (int i = 0; i < (DENSE ? G : N); ++i) {
     const int e = DENSE ? W * i : i;
-    allow[i] = mask && open[e] ? mask[id[e] >> 5] >> (id[e] & 31) : 0xFFFFFFFFu;
+    allow[i] = mask ? mask[open[e] ? id[e] >> 5 : 0] >> (id[e] & 31) : 0xFFFFFFFFu;
   }
 
-  // the first of the history and of the biases, on their way as well
+  // the first of the history and of the biases, on their way as well, to the
+  // row's capacity: the loads need not wait for its length
   const int32_t* h = a.history ? a.history + b * a.ld_history : nullptr;
-  // read to the row's capacity, so that the loads need not wait for its length
   int32_t seen[kAhead][4];
-  auto load_history = [&](int64_t i) {
+  auto load_history = [&](int i0) {
+    if (i0 + kBatch <= a.history_len) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      load_run<4, i32x4>(h, i + 4 * TH * u, a.history ? a.history_len : 0, (int32_t)-1, seen[u]);
+      for (int u = 0; u < kAhead; ++u)
+        load_run<4, true, i32x4>(h, i0 + 4 * (tid + TH * u), 0, (int32_t)-1, seen[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        load_run<4, false, i32x4>(h, i0 + 4 * (tid + TH * u), a.history_len, (int32_t)-1, seen[u]);
+    }
   };
-  load_history(4 * tid);
-  int64_t nh = 0, np = 0, nb = 0;
-  if (a.history) {
-    nh = a.n_history ? (int64_t)a.n_history[b] : a.history_len;
-    nh = min(max(nh, (int64_t)0), a.history_len);
-    np = a.n_prompt ? min(max((int64_t)a.n_prompt[b], (int64_t)0), nh) : 0;
-  }
+  if (a.history) load_history(0);
   int32_t bias_id = -1;
   float bias_add = 0.f;
-  auto load_bias = [&](int64_t i) {
+  auto load_bias = [&](int i) {
     bias_id = -1;
     if (i < a.bias_len) {
       bias_id = a.bias_ids[b * a.ld_bias + i];
       bias_add = a.bias[b * a.ld_bias + i];
     }
   };
+  int nh = 0, np = 0, nb = 0;
+  if (a.history) {
+    nh = min(max(a.n_history ? a.n_history[b] : a.history_len, 0), a.history_len);
+    np = a.n_prompt ? min(max(a.n_prompt[b], 0), nh) : 0;
+  }
   if (a.bias_ids) {
     load_bias(tid);
-    nb = a.n_bias ? (int64_t)a.n_bias[b] : a.bias_len;
-    nb = min(max(nb, (int64_t)0), a.bias_len);
+    nb = min(max(a.n_bias ? a.n_bias[b] : a.bias_len, 0), a.bias_len);
   }
 
   int place[N];
@@ -191,26 +212,38 @@ __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(6))) void k_
     }
   }
   if (a.history) {
-    for (int64_t i = 4 * tid; i < nh; i += 4 * TH * kAhead) {
-      bool may[kAhead][4];  // all looked up before any is searched for
+    // a batch: what may be in the tile is found out for all before any is looked
+    // for.  Most batches are all prompt or all output and wholly inside nh.
+    auto count_batch = [&](int i0, auto inside, auto prompt, auto output) {
+      bool may[kAhead][4];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          may[u][e] = sh.may_hold(seen[u][e], base, width, a.v) && i + 4 * TH * u + e < nh;
+          may[u][e] = sh.may_hold(seen[u][e], base, width, v) &&
+                      (decltype(inside)::value || i0 + 4 * (tid + TH * u) + e < nh);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int p = may[u][e] ? sh.find(seen[u][e], base) : -1;
-          if (p >= 0) {
-            if (i + 4 * TH * u + e < np)
-              atomicOr(&sh.count[p], kPrompt);
-            else
-              atomicAdd(&sh.count[p], 1u);
-          }
+          if (p < 0) continue;
+          if (decltype(output)::value || (!decltype(prompt)::value && i0 + 4 * (tid + TH * u) + e >= np))
+            atomicAdd(&sh.count[p], 1u);
+          else
+            atomicOr(&sh.count[p], kPrompt);
         }
-      if (i + 4 * TH * kAhead < nh) load_history(i + 4 * TH * kAhead);
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    for (int i0 = 0; i0 < nh; i0 += kBatch) {
+      if (i0 + kBatch <= np)
+        count_batch(i0, yes, yes, no);
+      else if (i0 >= np && i0 + kBatch <= nh)
+        count_batch(i0, yes, no, yes);
+      else
+        count_batch(i0, no, no, no);
+      if (i0 + kBatch < nh) load_history(i0 + kBatch);
     }
     __syncthreads();
     const float rep = a.repetition ? a.repetition[b] : 1.f;
@@ -235,10 +268,10 @@ __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(6))) void k_
 #pragma unroll
       for (int i = 0; i < N; ++i) sums[place[i]] = z[i];
     }
-    for (int64_t i0 = 0; i0 < nb; i0 += TH) {
+    for (int i0 = 0; i0 < nb; i0 += TH) {
       if (i0 > 0) load_bias(i0 + tid);
       __syncthreads();  // the logits are there, the list before is done with
-      const int mine = i0 + tid < nb && sh.may_hold(bias_id, base, width, a.v) ? sh.find(bias_id, base) : -1;
+      const int mine = i0 + tid < nb && sh.may_hold(bias_id, base, width, v) ? sh.find(bias_id, base) : -1;
       const uint64_t in = __ballot(mine >= 0);
       const int at = 64 * wave + __popcll(in & ((1ull << lane) - 1));
       if (mine >= 0) {
@@ -276,8 +309,8 @@ __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(6))) void k_
     float* out = a.out + b * a.ld_out + base;
 #pragma unroll
     for (int j = 0; j < G; ++j) {
-      const int64_t at = W * (tid + (int64_t)TH * j);
-      if (W == 4 && at + 4 <= width)
+      const int at = W * (tid + TH * j);
+      if (W == 4 && (full || at + 4 <= width))
         // past the caches: the logits are looked at seldom, once the token is chosen
         __builtin_nontemporal_store(f32x4{z[W * j], z[W * j + 1 % W], z[W * j + 2 % W], z[W * j + 3 % W]},
                                     reinterpret_cast<f32x4*>(out + at));

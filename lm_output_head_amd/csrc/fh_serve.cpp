@@ -47,6 +47,7 @@ bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p)
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxWidth = int64_t(1) << 30;    // n and v: grids stay below 2^32 threads,
 constexpr int64_t kMaxChannels = int64_t(1) << 27;  // and the product's, a wave or more per 16 channels
+constexpr int64_t kMaxList = int64_t(1) << 30;     // places of a history or list, in 32 bits with a batch past them
 constexpr int64_t kMaxK = (int64_t(1) << 17) - 1;  // 128^2 k < 2^31
 constexpr int64_t kMaxElems = int64_t(1) << 60;    // rows * stride stays far inside int64
 
@@ -357,7 +358,7 @@ fh_status fh_logits_apply(const float* logits, int64_t ld_logits, const int32_t*
                           (const void*)l.bias, (const void*)l.n_bias, (const void*)l.mask, (const void*)l.mask_row})
       if (!aligned_to(p, 4)) return fail(FH_EINVAL, "logits, rules and outputs must be aligned to 4 bytes");
     if (l.history) {
-      if (l.history_len < 0) return fail(FH_EINVAL, "history_len is negative");
+      if (l.history_len < 0 || l.history_len > kMaxList) return fail(FH_EINVAL, "history_len outside [0, 2^30]");
       s = check_ld("ld_history", l.ld_history, l.history_len, B);
     } else if (l.n_history || l.n_prompt) {
       return fail(FH_EINVAL, "n_history and n_prompt need a history");
@@ -365,7 +366,7 @@ fh_status fh_logits_apply(const float* logits, int64_t ld_logits, const int32_t*
     if (s != FH_OK) return s;
     if (!l.bias_ids != !l.bias) return fail(FH_EINVAL, "bias_ids and bias go together");
     if (l.bias_ids) {
-      if (l.bias_len < 0) return fail(FH_EINVAL, "bias_len is negative");
+      if (l.bias_len < 0 || l.bias_len > kMaxList) return fail(FH_EINVAL, "bias_len outside [0, 2^30]");
       s = check_ld("ld_bias", l.ld_bias, l.bias_len, B);
     } else if (l.n_bias) {
       return fail(FH_EINVAL, "n_bias needs a list of biases");
@@ -384,11 +385,11 @@ fh_status fh_logits_apply(const float* logits, int64_t ld_logits, const int32_t*
     a.ld_z = ld_logits;
     a.ids = ids;
     a.ld_ids = ld_ids;
-    a.n = n;
-    a.v = v;
+    a.n = (int)n;
+    a.v = (int)v;
     a.history = l.history_len > 0 ? l.history : nullptr;
     a.ld_history = l.ld_history;
-    a.history_len = l.history_len;
+    a.history_len = (int)l.history_len;
     a.n_prompt = l.n_prompt;
     a.n_history = l.n_history;
     a.repetition = l.repetition;
@@ -397,11 +398,11 @@ fh_status fh_logits_apply(const float* logits, int64_t ld_logits, const int32_t*
     a.bias_ids = l.bias_len > 0 ? l.bias_ids : nullptr;
     a.bias = l.bias;
     a.ld_bias = l.ld_bias;
-    a.bias_len = l.bias_len;
+    a.bias_len = (int)l.bias_len;
     a.n_bias = l.n_bias;
     a.mask = l.mask;
     a.ld_mask = l.ld_mask;
-    a.mask_rows = l.mask_rows;
+    a.mask_rows = (int)l.mask_rows;
     a.mask_row = l.mask_row;
     a.token_sample = mode == FH_TOKEN_SAMPLE;
     a.inverse_t = a.token_sample ? inverse_of(temperature) : 1.f;

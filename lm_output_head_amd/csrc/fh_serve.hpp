@@ -64,9 +64,10 @@ struct RulesArgs {
   int64_t ld_z;
   const int32_t* ids;    // or null
   int64_t ld_ids;
-  int64_t n, v;
+  int n, v;
   const int32_t* history;  // or null
-  int64_t ld_history, history_len;
+  int64_t ld_history;
+  int history_len;
   const int32_t* n_prompt;
   const int32_t* n_history;
   const float* repetition;
@@ -74,10 +75,12 @@ struct RulesArgs {
   const float* presence;
   const int32_t* bias_ids;  // or null
   const float* bias;
-  int64_t ld_bias, bias_len;
+  int64_t ld_bias;
+  int bias_len;
   const int32_t* n_bias;
   const uint32_t* mask;  // or null
-  int64_t ld_mask, mask_rows;
+  int64_t ld_mask;
+  int mask_rows;
   const int32_t* mask_row;
   int token_sample;
   float inverse_t;       // 1 / T'

@@ -119,6 +119,7 @@ CALL = dict(z=A, ld=100, ids=None, ld_ids=0, B=3, n=100, v=100, rules=None, mode
     ({"ws": P((1 << 20) + 4)}, "16-byte aligned"),
     ({"rules": {"ld_history": 9}}, "ld_history"),
     ({"rules": {"history_len": -1}}, "history_len"),
+    ({"rules": {"history_len": (1 << 30) + 1, "ld_history": 1 << 31}}, "history_len"),
     ({"rules": {"history": None, "n_history": A.value}}, "need a history"),
     ({"rules": {"bias": A.value}}, "go together"),
     ({"rules": {"bias": A.value, "bias_ids": A.value, "bias_len": 4, "ld_bias": 3}}, "ld_bias"),
