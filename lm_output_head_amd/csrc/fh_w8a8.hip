@@ -411,6 +411,12 @@ __global__ __launch_bounds__(256) void k_w8a8_pack(const int8_t* codes, const vo
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     if (j < n) {
       const float sc = codes ? 0.f : scales[j];
+      if (codes && i0 + 16 <= k) {  // 16 codes as they are, at any alignment
+        typedef uint32_t V __attribute__((ext_vector_type(4), aligned(1)));
+        const V x = *reinterpret_cast<const V*>(codes + j * k + i0);
+        out[c] = uint4{x[0], x[1], x[2], x[3]};
+        continue;
+      }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         if (i0 + e >= k) break;
