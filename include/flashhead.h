@@ -503,7 +503,8 @@ int64_t fh_w8a8_workspace(const fh_w8a8* w, const int8_t* q, int64_t ld_q, int64
  *   q_scale  device [B] float.
  *   out      device [B x n] of out_dtype, row stride ld_out >= n.
  *   workspace, workspace_bytes  see fh_w8a8_workspace (NULL, 0 if that is 0).
- * 1 <= B <= 65535.  q and out may have any alignment of their elements' size.
+ * 1 <= B <= 65535, and ceil(n / 256) ceil(B / 128) < 2^23 for B > 64 (a launch's
+ * threads).  q and out may have any alignment of their elements' size.
  */
 fh_status fh_w8a8_matmul(const fh_w8a8* w, const int8_t* q, int64_t ld_q, const float* q_scale,
                          int64_t B, void* out, int64_t ld_out, fh_dtype out_dtype, void* workspace,

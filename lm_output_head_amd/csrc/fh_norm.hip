@@ -236,6 +236,7 @@ bool launch_w(const NormArgs& a, int64_t B, hipStream_t st) {
   const int64_t chunks = (a.d + Elems<T>::N - 1) / Elems<T>::N, c = (chunks + 64 * W - 1) / (64 * W);
   const int64_t rows = W == 1 ? 4 : 1;
   const dim3 grid((unsigned)((B + rows - 1) / rows)), block(W <= 4 ? 256 : 64 * W);
+  if ((int64_t)grid.x * block.x >= int64_t(1) << 32) return false;  // more threads than a launch holds
   switch (c) {
 #define FH_CASE(CC) \
   case CC: hipLaunchKernelGGL((k_rmsnorm<T, W, CC>), grid, block, 0, st, a, B); return true;
@@ -248,15 +249,10 @@ bool launch_w(const NormArgs& a, int64_t B, hipStream_t st) {
 template <typename T>
 void launch(const NormArgs& a, int64_t B, hipStream_t st) {
   // a wave per row while rows are many and fit its lanes' 8 chunks; else the
-  // row's waves share it.  Grids stay below 2^32 threads.
+  // row's waves share it
   const int64_t chunks = (a.d + Elems<T>::N - 1) / Elems<T>::N;
-  if (B <= (int64_t(1) << 21)) {
-    if (chunks <= 64 || (B > 2048 && chunks <= 64 * 8)) {
-      if (launch_w<T, 1>(a, B, st)) return;
-    }
-    if (chunks <= 256 * 8 && launch_w<T, 4>(a, B, st)) return;
-    if (launch_w<T, 16>(a, B, st)) return;
-  }
+  if ((chunks <= 64 || (B > 2048 && chunks <= 64 * 8)) && launch_w<T, 1>(a, B, st)) return;
+  if (launch_w<T, 4>(a, B, st) || launch_w<T, 16>(a, B, st)) return;
   hipLaunchKernelGGL((k_rmsnorm_long<T>), dim3((unsigned)std::min<int64_t>(B, 1 << 20)), dim3(1024), 0, st, a, B);
 }
 

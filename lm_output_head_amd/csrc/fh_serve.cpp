@@ -143,11 +143,17 @@ int64_t need_bytes(const fh_w8a8* w, const int8_t* q, int64_t ld_q, int64_t B, b
   return copy_bytes(w, q, ld_q, B) + parts;
 }
 
-fh_status check_product(const fh_w8a8* w, const int8_t* q, int64_t ld_q, const float* q_scale, int64_t B) {
+fh_status check_rows(const fh_w8a8* w, int64_t ld_q, int64_t B) {
   if (!w) return fail(FH_EINVAL, "w is NULL");
-  if (!q || !q_scale) return fail(FH_EINVAL, "q and q_scale must not be NULL");
   if (B < 1 || B > 65535) return fail(FH_EINVAL, "B outside [1, 65535]");
+  if (!fh::w8a8_fits(w->n, B)) return fail(FH_EINVAL, "n and B together too large for one call");
   return check_ld("ld_q", ld_q, w->k, B);
+}
+
+fh_status check_product(const fh_w8a8* w, const int8_t* q, int64_t ld_q, const float* q_scale, int64_t B) {
+  const fh_status s = check_rows(w, ld_q, B);
+  if (s == FH_OK && (!q || !q_scale)) return fail(FH_EINVAL, "q and q_scale must not be NULL");
+  return s;
 }
 
 // q's rows where the kernel can read them, in fields q and ld_q of a.
@@ -257,9 +263,7 @@ fh_status fh_w8a8_get(const fh_w8a8* w, int8_t* codes, float* scales, void* stre
 
 int64_t fh_w8a8_workspace(const fh_w8a8* w, const int8_t* q, int64_t ld_q, int64_t B, int forward) {
   return guarded<int64_t>(FH_ENOMEM, [&]() -> int64_t {
-    if (!w) return fail(FH_EINVAL, "w is NULL");
-    if (B < 1 || B > 65535) return fail(FH_EINVAL, "B outside [1, 65535]");
-    const fh_status s = check_ld("ld_q", ld_q, w->k, B);
+    const fh_status s = check_rows(w, ld_q, B);
     return s != FH_OK ? (int64_t)s : need_bytes(w, q, ld_q, B, forward != 0);
   });
 }

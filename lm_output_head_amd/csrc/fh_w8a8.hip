@@ -558,9 +558,13 @@ int64_t w8a8_packed_bytes(int64_t n, int64_t k) { return (n + 15) / 16 * w_steps
 
 int64_t w8a8_parts(int64_t n, int64_t B) { return plan_of(n, B, true).row_tiles(n); }
 
+bool w8a8_fits(int64_t n, int64_t B) {
+  // tiles of 512 threads; the few-token kernels' grids have the tokens in y
+  const Plan p = plan_of(n, B, false);
+  return p.kind < k32 || p.tiles(n, B) < (int64_t(1) << 23);
+}
+
 hipError_t launch_w8a8(const W8A8Args& a, bool out_bf16, bool head, hipStream_t st) {
-  // tiles are numbered in 32 bits
-  if (plan_of(a.n, a.B, head).tiles(a.n, a.B) >= (int64_t(1) << 30)) return hipErrorInvalidValue;
   if (head)
     launch_kind<false, true>(a, st);
   else if (out_bf16)

@@ -378,8 +378,8 @@ class LogitRules:
     (or a captured graph) updates them in place.
 
     history [B x L] int32 with n_prompt, n_history [B] int32; repetition,
-    frequency, presence [B] float32 (without a history they do nothing); bias_ids [B x N] int32 with bias float32
-    and n_bias [B] int32; mask [R x ceil(v / 32)] int32 words (bit t % 32 of
+    frequency, presence [B] float32 (without a history they do nothing);
+    bias_ids [B x N] int32 with bias float32 and n_bias [B] int32; mask [R x ceil(v / 32)] int32 words (bit t % 32 of
     word t / 32 allows token t) with mask_row [B] int32 (outside [0, R): all
     allowed; without it row b takes mask row b).  Each may be None.
     """
@@ -404,10 +404,14 @@ class LogitRules:
         self.v = v
         self.B = sized[0].shape[0] if sized else (mask.shape[0] if mask is not None else None)
         s = _abi.FhLogitRules()
+        # an empty list has no address: the rows that count in it go with it
+        empty = {name for name, t in (("n_prompt", history), ("n_history", history), ("n_bias", bias))
+                 if t is not None and t.shape[1] == 0}
         for name, (t, dt) in vectors.items():
             if t is not None:
                 _vector(t, dt, self.B, name)
-                setattr(s, name, t.data_ptr())
+                if name not in empty:
+                    setattr(s, name, t.data_ptr())
         if history is not None:
             s.ld_history = _rows(history, torch.int32, (self.B, history.shape[1]), "history")
             s.history, s.history_len = history.data_ptr(), history.shape[1]

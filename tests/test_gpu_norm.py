@@ -152,3 +152,19 @@ def test_last_positions_of_a_batch():
     a, b = rmsnorm(hidden[:, -1], w, want_q=True), rmsnorm(hidden[:, -1].contiguous(), w, want_q=True)
     assert all(torch.equal(a[k], b[k]) for k in a)
     check(hidden[:, -1], None, w, 1e-6, 0.0, a)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [5, 600])
+def test_millions_of_rows(dt, d):
+    """More rows than a launch holds workgroups of 1024 threads: the first and
+    the last are as a call of their own gives them."""
+    from lm_output_head_amd import rmsnorm
+    B = (1 << 22) + 3
+    x = torch.randn(1 << 12, d, device="cuda").to(dt).repeat((1 << 10) + 1, 1)[:B]
+    say("norm of millions of rows", dt, d)
+    a = rmsnorm(x, want_q=True)
+    for lo in (0, B - 700):
+        b = rmsnorm(x[lo:lo + 700], want_q=True)
+        for k in b:
+            assert torch.all((a[k][lo:lo + 700].double() - b[k].double()).abs() <= (1 if k == "q" else 2.0 ** -7) * b[k].double().abs().clamp(min=1))

@@ -202,6 +202,17 @@ def test_penalties_without_a_history_do_nothing():
         assert torch.equal(o["logits"], z) and torch.equal(o["token"].long(), z.argmax(1))
 
 
+def test_empty_lists_with_their_lengths_do_nothing():
+    from lm_output_head_amd import LogitRules, logits_apply
+    z = torch.randn(3, 4000, device="cuda")
+    n = torch.tensor([0, 5, -1], dtype=torch.int32, device="cuda")
+    ids = torch.zeros(3, 6, dtype=torch.int32, device="cuda")
+    r = LogitRules(4000, history=ids[:, :0], n_prompt=n, n_history=n, repetition=torch.full((3,), 2.0, device="cuda"),
+                   bias_ids=ids[:, :0], bias=ids.float()[:, :0], n_bias=n)
+    out = logits_apply(z, r)
+    assert torch.equal(out["logits"], z) and torch.equal(out["token"].long(), z.argmax(1))
+
+
 def test_same_choice_as_the_dense_head():
     """Without rules the choice over fh_dense_forward's logits is its own."""
     from lm_output_head_amd import FlashHead, logits_apply

@@ -181,3 +181,15 @@ def test_workspace_of_the_call_is_checked():
     head.close()
     with pytest.raises(ValueError, match="unknown int8 weight|either"):
         head.matmul(dev(q), dev(qs))
+
+
+def test_more_than_one_launch_holds_is_refused():
+    from lm_output_head_amd import FlashHeadError, W8A8Head
+    n = 256 * (1 << 14) + 1
+    head = W8A8Head(codes=torch.ones(n, 1, dtype=torch.int8, device="cuda"), scales=torch.ones(n, device="cuda"))
+    q, qs = torch.ones(65535, 1, dtype=torch.int8, device="cuda"), torch.ones(65535, device="cuda")
+    say("too many tiles")
+    with pytest.raises(FlashHeadError, match="too large for one call"):
+        head.forward(q, qs)
+    got = head.forward(q[:3], qs[:3])
+    assert got["token"].tolist() == [0, 0, 0] and got["token_logit"].tolist() == [1.0] * 3
