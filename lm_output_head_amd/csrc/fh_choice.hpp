@@ -44,6 +44,10 @@ __device__ __forceinline__ Part choice_merge(Part a, const Part& b) {
   return a;
 }
 
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+  return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);  // the truth table of a ^ b ^ c
+}
+
 // Philox4x32-10 of philox_block's counter for token draws (stage 1), both halves
 // of each 32 x 32 product from one instruction.
 __device__ __forceinline__ U4 token_words(uint64_t seed, uint32_t row, uint32_t blk) {
@@ -51,9 +55,9 @@ __device__ __forceinline__ U4 token_words(uint64_t seed, uint32_t row, uint32_t 
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = (uint64_t)0xD2511F53u * x, c = (uint64_t)0xCD9E8D57u * z;
-    x = (uint32_t)(c >> 32) ^ y ^ k0;
+    x = xor3((uint32_t)(c >> 32), y, k0);
     y = (uint32_t)c;
-    z = (uint32_t)(a >> 32) ^ w ^ k1;
+    z = xor3((uint32_t)(a >> 32), w, k1);
     w = (uint32_t)a;
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;

@@ -10,6 +10,11 @@
 // candidates through a hash of their ids.  Counts are integer sums, and one
 // thread adds all biases of a token in the list's order, so results do not
 // depend on the order of execution.
+//
+// Many rows are bound by the logits' bytes: 64 rows of 151936 take 30 us (with
+// the choice's second launch), 128 rows 47, so 64 more cost 16.5 us, 4.7 TB/s,
+// a copy's rate.  Few rows are bound by latency: the chain of history, table and
+// reductions, 6 us at 1 x 128256 with 1000 of history.
 
 #include <hip/hip_runtime.h>
 
@@ -107,12 +112,13 @@ struct Tables {
 };
 
 // G runs of W consecutive logits per thread: a tile is TH W G.  Held to the
-// registers of six waves per SIMD (64 x 151936 sampled: 41 us at five, 37 at six).
+// registers of six waves per SIMD (64 x 151936 sampled, the whole call: 30.8 us at
+// five, 30.5 at six, 31.6 at seven).
 template <bool DENSE, int TH, int W, int G>
 __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(6))) void k_rules(RulesArgs a) {
   constexpr int kTile = TH * W * G, N = W * G, kBatch = 4 * TH * kAhead;  // ids of the history at once
   typedef Tables<DENSE, kTile, TH> Table;
-  static_assert((Table::kSize & (Table::kSize - 1)) == 0 && Table::kSize <= 65536, "the hash masks 16 bits");
+  static_assert(DENSE || ((Table::kSize & (Table::kSize - 1)) == 0 && Table::kSize <= 65536), "the hash masks 16 bits");
   static_assert(!DENSE || W == 4, "a Philox block and a mask word serve four tokens of a dense row");
   __shared__ Table sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -226,8 +232,9 @@ __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(6))) void k_
       for (int u = 0; u < kAhead; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int p = may[u][e] ? sh.find(seen[u][e], base) : -1;
-          if (p < 0) continue;
+          if (!may[u][e]) continue;
+          const int p = sh.find(seen[u][e], base);
+          if (!DENSE && p < 0) continue;
           if (decltype(output)::value || (!decltype(prompt)::value && i0 + 4 * (tid + TH * u) + e >= np))
             atomicAdd(&sh.count[p], 1u);
           else
@@ -246,17 +253,19 @@ __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(6))) void k_
       if (i0 + kBatch < nh) load_history(i0 + kBatch);
     }
     __syncthreads();
-    const float rep = a.repetition ? a.repetition[b] : 1.f;
+    // a positive logit is multiplied by 1 / rep, itself rounded once per row (a
+    // division per logit rounds once less and cost 1.5 us at 64 x 151936 with 8192
+    // of history, where nearly every wave has a repeated token at each of its places)
+    const float rep = a.repetition ? a.repetition[b] : 1.f, per = 1.f / rep;
     const float freq = a.frequency ? a.frequency[b] : 0.f;
     const float pres = a.presence ? a.presence[b] : 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const uint32_t c = sh.count[place[i]];
       if (c && open[i]) {
-        z[i] = z[i] > 0.f ? z[i] / rep : z[i] * rep;
         const uint32_t made = c & ~kPrompt;
-        z[i] -= freq * (float)made;
-        if (made) z[i] -= pres;
+        z[i] = fmaf(-freq, (float)made, z[i] * (z[i] > 0.f ? per : rep));
+        z[i] -= made ? pres : 0.f;
       }
     }
   }
@@ -346,8 +355,9 @@ __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(6))) void k_
 
 // Tiles of a call: large ones walk the history less often, small ones spread few
 // rows over the CUs; the large one where it leaves two workgroups per CU (64 x
-// 151936 sampled: 37 us with tiles of 4096; 1 x 128256: 6.5 us with 1024, 12.9
-// with 4096).  Candidates' tiles have a thread per candidate or two, so that the
+// 151936 with 8192 of history, sampled, the whole call: 30.5 us with tiles of
+// 4096, 32.9 with 2048, 38.4 with 8192; 1 x 128256: the kernel 6.5 us with 1024,
+// 12.9 with 4096).  Candidates' tiles have a thread per candidate or two, so that the
 // history, which each of them searches for, is short per thread (8 x 8192 with
 // 32768 of history: 36 us with 512 threads for 512 candidates, 69 with 256 for
 // 256; 64 x 8192 with 8192: 27 us with 512 threads for 1024, 37 with 256).

@@ -1,10 +1,10 @@
 """GPU parity of fh_logits_apply against the float64 definition.
 
-Tolerances, u = 2^-24: the repetition, the penalty's product and subtraction,
-the presence, each bias's addition and the bias's own round once each; the
-oracle returns the sum of magnitudes they are relative to (a bias counted four
-times, for its running sum over the few entries of one token), so 8 u of it
-covers up to eight roundings.  The choice: serve_oracle.check_choice."""
+Tolerances, u = 2^-24: the repetition rounds twice (its reciprocal and the
+product), the penalty, the presence, each bias's addition and the bias's own
+once each; the oracle returns the sum of magnitudes they are relative to (a bias
+counted four times, for its running sum over the few entries of one token), so
+8 u of it covers up to eight roundings.  The choice: serve_oracle.check_choice."""
 
 import numpy as np
 import pytest
