@@ -139,14 +139,14 @@ int64_t copy_bytes(const fh_w8a8* w, const int8_t* q, int64_t ld_q, int64_t B) {
   return rows_aligned(w, q, ld_q, B) ? 0 : round16(w->k) * B;
 }
 int64_t need_bytes(const fh_w8a8* w, const int8_t* q, int64_t ld_q, int64_t B, bool forward) {
-  const int64_t parts = forward ? (int64_t)sizeof(fh::Part) * B * fh::w8a8_parts(w->n, B) : 0;
+  const int64_t parts = forward ? (int64_t)sizeof(fh::Part) * B * fh::w8a8_parts(w->n, w->k, B) : 0;
   return copy_bytes(w, q, ld_q, B) + parts;
 }
 
 fh_status check_rows(const fh_w8a8* w, int64_t ld_q, int64_t B) {
   if (!w) return fail(FH_EINVAL, "w is NULL");
   if (B < 1 || B > 65535) return fail(FH_EINVAL, "B outside [1, 65535]");
-  if (!fh::w8a8_fits(w->n, B)) return fail(FH_EINVAL, "n and B together too large for one call");
+  if (!fh::w8a8_fits(w->n, w->k, B)) return fail(FH_EINVAL, "n and B together too large for one call");
   return check_ld("ld_q", ld_q, w->k, B);
 }
 
@@ -322,7 +322,7 @@ fh_status fh_w8a8_forward(const fh_w8a8* w, const int8_t* q, int64_t ld_q, const
     a.parts = reinterpret_cast<fh::Part*>(static_cast<char*>(workspace) + copy_bytes(w, q, ld_q, B));
     if (r == hipSuccess) r = fh::launch_w8a8(a, false, true, st);
     if (r == hipSuccess)
-      r = fh::launch_choice(a.parts, B, fh::w8a8_parts(w->n, B), out_token, out_token_logit, out_lse, st);
+      r = fh::launch_choice(a.parts, B, fh::w8a8_parts(w->n, w->k, B), out_token, out_token_logit, out_lse, st);
     return r == hipSuccess ? FH_OK : hip_fail(r, "int8 head launch");
   });
 }

@@ -55,8 +55,8 @@ hipError_t launch_w8a8_unpack(const void* packed, int64_t n, int64_t k, int8_t* 
 // rows of k bytes at any alignment -> rows of ld bytes (a multiple of 16), zero past k
 hipError_t launch_w8a8_align(const int8_t* q, int64_t ld_q, int64_t B, int64_t k, int8_t* out,
                              int64_t ld, hipStream_t st);
-int64_t w8a8_parts(int64_t n, int64_t B);  // partials per row of the head
-bool w8a8_fits(int64_t n, int64_t B);  // a launch holds fewer than 2^32 threads
+int64_t w8a8_parts(int64_t n, int64_t k, int64_t B);  // partials per row of the head
+bool w8a8_fits(int64_t n, int64_t k, int64_t B);  // a launch holds fewer than 2^32 threads
 hipError_t launch_w8a8(const W8A8Args& a, bool out_bf16, bool head, hipStream_t st);
 
 // The rules on logits (fh_rules.hip): fh_logits_apply's arguments as checked.

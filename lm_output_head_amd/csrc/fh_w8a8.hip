@@ -7,8 +7,8 @@
 // 4 (l / 16) .. + 3.  W is kept in that order (fragment order), so one
 // instruction's operand is one contiguous 1 KB.
 //
-// Few tokens are bound by the bytes of W: 1 x 128256 x 2048 in 42 us, 6.25 TB/s,
-// where a plain read reaches 6.3; 64 x 151936 x 2560 with float results in 84 us,
+// Few tokens are bound by the bytes of W: 1 x 128256 x 2048 in 37.8 us, 6.97 TB/s
+// (a read through the caches reaches 6.3); 64 x 151936 x 2560 with float results in 84 us,
 // 5.1 TB/s.  Many by the matrix cores: 4096 x 10240 x 2560 in 114 to 119 us, 1.8
 // to 1.9 POP/s, where the library's product reaches 2.1 at 8192^3.
 
@@ -105,8 +105,8 @@ __device__ __forceinline__ Part choose_tile(const W8A8Args& a, const float (&z)[
 // caches and add up their sums in LDS (exact, so in any order).  A workgroup is
 // G such groups.  One wave per 32 rows left loads of one step in flight: 1 x
 // 128256 x 2048 45.7 -> 42.0 us, 1 x 4096 x 4096 20.8 -> 5.8, 1 x 1000 x 8192
-// 41.7 -> 5.2.
-template <int FT, int FN, int KW, int G, bool BF16, bool HEAD>
+// 41.7 -> 5.2.  PAST: the rows pass the caches by (42.0 -> 37.7).
+template <int FT, int FN, int KW, int G, bool PAST, bool BF16, bool HEAD>
 __global__ __launch_bounds__(64 * KW * G) void k_w8a8_few(W8A8Args a) {
   constexpr int kAhead = FN == 1 ? 4 : 2;  // steps whose loads go out together
   typedef typename Out<BF16>::T T;
@@ -139,7 +139,10 @@ __global__ __launch_bounds__(64 * KW * G) void k_w8a8_few(W8A8Args a) {
     for (int u = 0; u < N; ++u) {
       const int ch = 4 * (s + u) + g < chunks ? 4 * (s + u) + g : 0;
 #pragma unroll
-      for (int m = 0; m < FN; ++m) wf[u][m] = wp[m][(s + u) * 64];
+      for (int m = 0; m < FN; ++m) {
+        const i32x4* p = wp[m] + (s + u) * 64;
+        wf[u][m] = PAST ? __builtin_nontemporal_load(p) : *p;
+      }
 #pragma unroll
       for (int t = 0; t < FT; ++t) qf[u][t] = *reinterpret_cast<const i32x4*>(qp[t] + 16 * ch);
     }
@@ -209,15 +212,14 @@ __device__ __forceinline__ void lds_barrier() {
 // tokens' block of kStage steps of k is staged in LDS in fragment order (a
 // fragment is read as one contiguous 1 KB), double buffered and loaded one block
 // ahead; each wave's rows of W go straight to registers (fragment
-// order, one contiguous 1 KB per load), two blocks ahead.  ONCE: the rows are
-// read by this workgroup alone and pass the caches by (128 x 128256 x 2048:
-// 65 -> 62 us; where token tiles share them it costs 10%).
+// order, one contiguous 1 KB per load), two blocks ahead.  PAST: the rows pass
+// the caches by (64 x 151936 x 2560: 87.5 -> 83.8 us).
 //
 // Tiles of eight waves are held to 128 registers, two workgroups per CU: one's
 // results overlap the other's products (head of 128 x 128256 sampled 102 -> 88
 // us; with the 250 registers of a 256 x 256 tile, one per CU, 4096 x 10240 x 2560
 // took 137 us, not 119).
-template <int FT, int FN, int WN, bool ONCE, bool BF16, bool HEAD>
+template <int FT, int FN, int WN, bool PAST, bool BF16, bool HEAD>
 __global__ __launch_bounds__(64 * WN) __attribute__((amdgpu_waves_per_eu(WN == 8 ? 4 : 1))) void k_w8a8_tile(W8A8Args a, int n_tiles, int q_tiles) {
   constexpr int kStage = kStepPad, kFrags = FT * kStage;  // fragments of a token block
   constexpr int kOwn = (kFrags + WN - 1) / WN;       // of them, this wave's to stage
@@ -278,7 +280,7 @@ __global__ __launch_bounds__(64 * WN) __attribute__((amdgpu_waves_per_eu(WN == 8
 #pragma unroll
       for (int m = 0; m < FN; ++m) {
         const i32x4* p = wp[m] + (int64_t)min(kStage * blk + s, steps - 1) * 64;
-        dst[s][m] = ONCE ? __builtin_nontemporal_load(p) : *p;
+        dst[s][m] = PAST ? __builtin_nontemporal_load(p) : *p;
       }
   };
   i32x4 acc[FN][FT];
@@ -495,88 +497,110 @@ unsigned grid_of(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256
 
 // How a call is cut up: a tile of k_w8a8_tile (named by its tokens), or a shape
 // of k_w8a8_few.
-enum Kind { kFew16Rows8, kFew16Rows4, kFew32Rows2, kTokens32Rows8, kTokens32Rows4, k32, k64, k128 };
+enum Kind { kFew16Rows8, kFew16Rows4, kFew16Rows2, kTokens32Rows8, kTokens32Rows4, k16, k32, k64, k128 };
 struct Plan {
   Kind kind;
   int rows, tokens;  // of a workgroup
   int64_t row_tiles(int64_t n) const { return (n + rows - 1) / rows; }
-  int64_t tiles(int64_t n, int64_t B) const { return row_tiles(n) * ((B + tokens - 1) / tokens); }
+  int64_t token_tiles(int64_t B) const { return (B + tokens - 1) / tokens; }
+  int64_t tiles(int64_t n, int64_t B) const { return row_tiles(n) * token_tiles(B); }
 };
-// Up to 16 tokens: the fewer rows, the more waves share one's k (1 x 1000 x 8192
-// with 8 waves 5.2 us, with 4 7.5; 1 x 65536 x 512 9.5 and 7.9).  A wave of 16
-// rows reads its tokens once per KB of W, one of 32 half as often: 42.0 and 46.8
-// us for 1 x 128256 x 2048, 59.3 and 49.9 for 16; the head, whose choice one wave
-// of a group makes, 1 x 262144 x 1152 66.6 and 58.5.
+// Up to 4 tokens: waves of some 8 steps of k each (1 token: 128256 x 2048 in 37.8,
+// 40.9 and 40.8 us with 4, 2 and 8 waves, 262144 x 1152 in 46.9, 44.7 and 51, 40000
+// x 4096 in 27.0, 27.9 and 25.9); the fewer rows, the more waves (1000 x 8192 with
+// 8 waves 5.2 us, with 4 7.5).
+// Up to 16: a wave reads its tokens once per KB of W, so they are staged in LDS
+// where rows are many (16 tokens, 151936 x 2560: 70 us, with two waves on 32 rows
+// 81; 128256 x 2048 47 and 48; 30001 x 6144 34 and 36).
 // More: the largest tile that about fills the CUs and leaves less than half its
 // tokens empty (4096 x 10240 x 2560: 119 us with 256 rows x 128 tokens, 146 with
 // 256 x 64, 251 with 128 x 32; 512 x 4096 x 4096, 64, 128 and 512 tiles: 36, 24
 // and 22).  Where even the smallest leaves CUs idle, waves share k (32 x 4096 x
 // 4096 18.4 and 8.1 us, 128 x 4096 x 4096 18.6 and 12.7; with 224 tiles the
 // smallest is the better one, 23.5 and 33.8 for 32 x 28672 x 4096).
-Plan plan_of(int64_t n, int64_t B, bool head) {
+Plan plan_of(int64_t n, int64_t k, int64_t B) {
   constexpr int kFull = 180;  // workgroups that about fill the 256 CUs
   if (B <= 16) {
-    const int64_t tiles = (n + 15) / 16;
-    if (tiles < 512) return Plan{kFew16Rows8, 16, 16};
-    if (tiles < 2048 || (B <= 4 && !head)) return Plan{kFew16Rows4, 16, 16};
-    return Plan{kFew32Rows2, 64, 16};
+    const int64_t tiles = (n + 15) / 16, steps = w_steps(k);
+    if (tiles < 512 || (B <= 4 && steps >= 44)) return Plan{kFew16Rows8, 16, 16};
+    if (tiles < 2048 || (B <= 4 && steps >= 24)) return Plan{kFew16Rows4, 16, 16};
+    return B <= 4 ? Plan{kFew16Rows2, 32, 16} : Plan{k16, 128, 16};
   }
   for (const Plan& p : {Plan{k128, 256, 128}, Plan{k64, 256, 64}, Plan{k32, 128, 32}})
     if (2 * B > p.tokens && p.tiles(n, B) >= kFull) return p;
   return B <= 32 ? Plan{kTokens32Rows8, 16, 32} : Plan{kTokens32Rows4, 32, 32};
 }
 
-template <int FT, int FN, int KW, int G, bool BF16, bool HEAD>
+// Whether W passes the caches by: its rows are read by one workgroup alone, and
+// too many to be there still at the next call, at least once other work has run.
+// Waves sharing k gain from 64 MB (1 x 128256 x 1024, 131 MB, three weights in
+// turn: 21.7 -> 19.8 us, one weight again and again 19.8 -> 19.0; below it 1 x
+// 4096 x 4096 5.3 -> 5.5 and 4.4 -> 4.6).  Tiles gain where W is larger than the
+// Infinity Cache (64 x 151936 x 2560, 389 MB: 87.5 -> 83.8; 128 x 128256 x 2048,
+// 263 MB: 67.7 -> 71.0, again and again 67.0 -> 69.7).
+bool past_caches(const Plan& p, int64_t n, int64_t k, int64_t B) {
+  return p.token_tiles(B) == 1 && w8a8_packed_bytes(n, k) > (p.kind < k16 ? int64_t(64) << 20 : int64_t(256) << 20);
+}
+
+template <int FT, int FN, int KW, int G, bool PAST, bool BF16, bool HEAD>
 void launch_few(const W8A8Args& a, hipStream_t st) {
   constexpr int kRows = 16 * FN * G, kTokens = 16 * FT;
   const dim3 grid((unsigned)((a.n + kRows - 1) / kRows), (unsigned)((a.B + kTokens - 1) / kTokens));
-  hipLaunchKernelGGL((k_w8a8_few<FT, FN, KW, G, BF16, HEAD>), grid, dim3(64 * KW * G), 0, st, a);
+  hipLaunchKernelGGL((k_w8a8_few<FT, FN, KW, G, PAST, BF16, HEAD>), grid, dim3(64 * KW * G), 0, st, a);
 }
 
-template <int FT, int FN, int WN, bool BF16, bool HEAD>
+template <int FT, int FN, int WN, bool PAST, bool BF16, bool HEAD>
 void launch_tile(const W8A8Args& a, hipStream_t st) {
   constexpr int kRows = 16 * FN * WN, kTokens = 16 * FT;
   const int nt = (int)((a.n + kRows - 1) / kRows), qt = (a.B + kTokens - 1) / kTokens;
-  const dim3 grid((unsigned)(((int64_t)nt * qt + 7) / 8 * 8)), block(64 * WN);
-  if (qt == 1)
-    hipLaunchKernelGGL((k_w8a8_tile<FT, FN, WN, true, BF16, HEAD>), grid, block, 0, st, a, nt, qt);
-  else
-    hipLaunchKernelGGL((k_w8a8_tile<FT, FN, WN, false, BF16, HEAD>), grid, block, 0, st, a, nt, qt);
+  const dim3 grid((unsigned)(((int64_t)nt * qt + 7) / 8 * 8));
+  hipLaunchKernelGGL((k_w8a8_tile<FT, FN, WN, PAST, BF16, HEAD>), grid, dim3(64 * WN), 0, st, a, nt, qt);
+}
+
+template <bool PAST, bool BF16, bool HEAD>
+void launch_kind(const W8A8Args& a, Kind kind, hipStream_t st) {
+  switch (kind) {
+    case kFew16Rows8: return launch_few<1, 1, 8, 1, PAST, BF16, HEAD>(a, st);
+    case kFew16Rows4: return launch_few<1, 1, 4, 1, PAST, BF16, HEAD>(a, st);
+    case kFew16Rows2: return launch_few<1, 1, 2, 2, PAST, BF16, HEAD>(a, st);
+    case kTokens32Rows8: return launch_few<2, 1, 8, 1, PAST, BF16, HEAD>(a, st);
+    // more than 32 tokens: two tiles of them or more share W
+    case kTokens32Rows4: return launch_few<2, 2, 4, 1, false, BF16, HEAD>(a, st);
+    case k16: return launch_tile<1, 2, 4, PAST, BF16, HEAD>(a, st);
+    case k32: return launch_tile<2, 2, 4, PAST, BF16, HEAD>(a, st);
+    case k64: return launch_tile<4, 2, 8, PAST, BF16, HEAD>(a, st);
+    case k128: return launch_tile<8, 2, 8, PAST, BF16, HEAD>(a, st);
+  }
 }
 
 template <bool BF16, bool HEAD>
-void launch_kind(const W8A8Args& a, hipStream_t st) {
-  switch (plan_of(a.n, a.B, HEAD).kind) {
-    case kFew16Rows8: return launch_few<1, 1, 8, 1, BF16, HEAD>(a, st);
-    case kFew16Rows4: return launch_few<1, 1, 4, 1, BF16, HEAD>(a, st);
-    case kFew32Rows2: return launch_few<1, 2, 2, 2, BF16, HEAD>(a, st);
-    case kTokens32Rows8: return launch_few<2, 1, 8, 1, BF16, HEAD>(a, st);
-    case kTokens32Rows4: return launch_few<2, 2, 4, 1, BF16, HEAD>(a, st);
-    case k32: return launch_tile<2, 2, 4, BF16, HEAD>(a, st);
-    case k64: return launch_tile<4, 2, 8, BF16, HEAD>(a, st);
-    case k128: return launch_tile<8, 2, 8, BF16, HEAD>(a, st);
-  }
+void launch_product(const W8A8Args& a, hipStream_t st) {
+  const Plan p = plan_of(a.n, a.k, a.B);
+  if (past_caches(p, a.n, a.k, a.B))
+    launch_kind<true, BF16, HEAD>(a, p.kind, st);
+  else
+    launch_kind<false, BF16, HEAD>(a, p.kind, st);
 }
 
 }  // namespace
 
 int64_t w8a8_packed_bytes(int64_t n, int64_t k) { return (n + 15) / 16 * w_steps(k) * 1024; }
 
-int64_t w8a8_parts(int64_t n, int64_t B) { return plan_of(n, B, true).row_tiles(n); }
+int64_t w8a8_parts(int64_t n, int64_t k, int64_t B) { return plan_of(n, k, B).row_tiles(n); }
 
-bool w8a8_fits(int64_t n, int64_t B) {
+bool w8a8_fits(int64_t n, int64_t k, int64_t B) {
   // tiles of 512 threads; the few-token kernels' grids have the tokens in y
-  const Plan p = plan_of(n, B, false);
-  return p.kind < k32 || p.tiles(n, B) < (int64_t(1) << 23);
+  const Plan p = plan_of(n, k, B);
+  return p.kind < k16 || p.tiles(n, B) < (int64_t(1) << 23);
 }
 
 hipError_t launch_w8a8(const W8A8Args& a, bool out_bf16, bool head, hipStream_t st) {
   if (head)
-    launch_kind<false, true>(a, st);
+    launch_product<false, true>(a, st);
   else if (out_bf16)
-    launch_kind<true, false>(a, st);
+    launch_product<true, false>(a, st);
   else
-    launch_kind<false, false>(a, st);
+    launch_product<false, false>(a, st);
   return hipGetLastError();
 }
 

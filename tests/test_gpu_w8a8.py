@@ -43,7 +43,8 @@ SIZES = [(1, 1, 1), (1, 16, 64), (3, 17, 65), (5, 130, 16), (16, 128, 128), (17,
          # each way of cutting a call up, and odd and even numbers of blocks of k
          (3, 9001, 70), (16, 8200, 448), (7, 32785, 48), (16, 33000, 320), (20, 25001, 320), (32, 24600, 448),
          (40, 32801, 320), (64, 33000, 448), (100, 65601, 320), (128, 65600, 192), (300, 32801, 320),
-         (257, 33001, 448), (200, 4000, 320), (129, 70001, 130)]
+         (257, 33001, 448), (200, 4000, 320), (129, 70001, 130), (2, 33001, 320), (3, 33000, 1600),
+         (1, 9001, 2900), (9, 32770, 130)]
 
 
 @pytest.mark.parametrize("B,n,k", SIZES)
@@ -193,3 +194,31 @@ def test_more_than_one_launch_holds_is_refused():
         head.forward(q, qs)
     got = head.forward(q[:3], qs[:3])
     assert got["token"].tolist() == [0, 0, 0] and got["token_logit"].tolist() == [1.0] * 3
+
+
+# weights that pass the caches by: of more than 64 MB (up to 16 or 32 tokens) and
+# of more than 256 MB, each way of cutting them up
+@pytest.mark.parametrize("n,k,Bs", [(70001, 1000, (1, 4)), (45001, 1600, (2,)), (24001, 2900, (3,)), (5001, 14000, (16,)),
+                                    (20001, 3500, (5,)), (16001, 4400, (20,)), (240001, 1152, (1, 16, 17, 40, 100, 130))])
+def test_large_weights_are_as_their_slices(n, k, Bs):
+    """Exact sums and one formula: rows 0 .. 999 and the last 1000 as a weight of
+    their own, cut up another way, give the same bits."""
+    from lm_output_head_amd import W8A8Head
+    g = torch.Generator(device="cuda").manual_seed(n)
+    w = torch.randint(-128, 128, (n, k), dtype=torch.int8, device="cuda", generator=g)
+    ws = torch.rand(n, device="cuda", generator=g) / 4000
+    head = W8A8Head(codes=w, scales=ws)
+    cuts = [(lo, W8A8Head(codes=w[lo:lo + 1000].contiguous(), scales=ws[lo:lo + 1000])) for lo in (0, n // 2, n - 1000)]
+    for B in Bs:
+        say("large weight", B, n, k)
+        q = torch.randint(-128, 128, (B, k), dtype=torch.int8, device="cuda", generator=g)
+        qs = torch.rand(B, device="cuda", generator=g)
+        for dt in (torch.float32, torch.bfloat16):
+            z = head.matmul(q, qs, dtype=dt)
+            for lo, part in cuts:
+                assert torch.equal(z[:, lo:lo + 1000], part.matmul(q, qs, dtype=dt)), (B, dt, lo)
+        out, z = head.forward(q, qs, want_logits=True), head.matmul(q, qs)
+        assert torch.equal(out["logits"], z)
+        top = z.amax(1)
+        first = torch.where(z == top[:, None], torch.arange(n, device="cuda"), n).amin(1)  # ties: the smaller token
+        assert torch.equal(out["token"].long(), first) and torch.equal(out["token_logit"], top)
