@@ -383,25 +383,52 @@ __global__ __launch_bounds__(64 * WN) __attribute__((amdgpu_waves_per_eu(WN == 8
   }
 }
 
-// scale[j] = max |W[j]| / 127; *bad is set where a row is not finite.
+// N consecutive elements of W from i on as floats, in 16-byte loads at any
+// alignment of the element (one by one the layout of 128256 x 2048 bfloat16 took
+// 525 us and its scales 273, with them 147 and 108).
+template <typename T, int N>
+__device__ __forceinline__ void w_run(const void* W, int64_t i, float (&v)[N]) {
+  constexpr int kPer = 16 / (int)sizeof(T);
+  typedef T V __attribute__((ext_vector_type(kPer), aligned(sizeof(T))));
+#pragma unroll
+  for (int e = 0; e < N; e += kPer) {
+    const V x = *reinterpret_cast<const V*>(static_cast<const T*>(W) + i + e);
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      if constexpr (sizeof(T) == 2)
+        v[e + u] = __uint_as_float((uint32_t)x[u] << 16);
+      else
+        v[e + u] = x[u];
+    }
+  }
+}
 template <typename T>
-__device__ __forceinline__ float w_elem(const void* W, int64_t i);
-template <>
-__device__ __forceinline__ float w_elem<float>(const void* W, int64_t i) { return static_cast<const float*>(W)[i]; }
-template <>
-__device__ __forceinline__ float w_elem<uint16_t>(const void* W, int64_t i) {
-  return __uint_as_float((uint32_t)static_cast<const uint16_t*>(W)[i] << 16);
+__device__ __forceinline__ float w_elem(const void* W, int64_t i) {
+  if constexpr (sizeof(T) == 2)
+    return __uint_as_float((uint32_t)static_cast<const T*>(W)[i] << 16);
+  else
+    return static_cast<const T*>(W)[i];
 }
 
+// scale[j] = max |W[j]| / 127; *bad is set where a row is not finite.
 template <typename T>
 __global__ __launch_bounds__(256) void k_w8a8_scales(const void* W, int64_t n, int64_t k, float* scales, int* bad) {
+  constexpr int N = 16 / (int)sizeof(T);
+  const int lane = threadIdx.x & 63;
   for (int64_t j = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); j < n; j += (int64_t)gridDim.x * 4) {
     uint32_t top = 0u;  // |W| as bits: NaN's and infinity's are above every finite value's
-    for (int64_t i = threadIdx.x & 63; i < k; i += 64)
-      top = max(top, __float_as_uint(w_elem<T>(W, j * k + i)) & 0x7FFFFFFFu);
+    auto take = [&](float v) { top = max(top, __float_as_uint(v) & 0x7FFFFFFFu); };
+    const int64_t whole = k / N * N;
+    for (int64_t i = (int64_t)N * lane; i < whole; i += 64 * N) {
+      float v[N];
+      w_run<T, N>(W, j * k + i, v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) take(v[e]);
+    }
+    if (whole + lane < k) take(w_elem<T>(W, j * k + whole + lane));
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
-    if ((threadIdx.x & 63) == 0) {
+    if (lane == 0) {
       scales[j] = __uint_as_float(top) / 127.f;
       if (top >= 0x7F800000u) atomicOr(bad, 1);
     }
@@ -418,22 +445,30 @@ __global__ __launch_bounds__(256) void k_w8a8_pack(const int8_t* codes, const vo
     const int64_t s = (c >> 6) % steps, j = (c >> 6) / steps * 16 + (lane & 15), i0 = s * 64 + (lane >> 4) * 16;
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     if (j < n) {
-      const float sc = codes ? 0.f : scales[j];
-      if (codes && i0 + 16 <= k) {  // 16 codes as they are, at any alignment
+      const bool whole = i0 + 16 <= k;
+      if (codes && whole) {  // 16 codes as they are, at any alignment
         typedef uint32_t V __attribute__((ext_vector_type(4), aligned(1)));
         const V x = *reinterpret_cast<const V*>(codes + j * k + i0);
         out[c] = uint4{x[0], x[1], x[2], x[3]};
         continue;
       }
+      const float sc = codes ? 0.f : scales[j];
+      float v[16];
+      if (!codes && whole) {
+        w_run<T, 16>(W, j * k + i0, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          v[e] = i0 + e < k ? codes ? (float)codes[j * k + i0 + e] : w_elem<T>(W, j * k + i0 + e) : 0.f;
+      }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        if (i0 + e >= k) break;
-        int v = 0;
+        int q = 0;
         if (codes)
-          v = codes[j * k + i0 + e];
+          q = (int)v[e];
         else if (sc > 0.f)
-          v = (int)fminf(fmaxf(rintf(w_elem<T>(W, j * k + i0 + e) / sc), -127.f), 127.f);
-        w[e >> 2] |= ((uint32_t)v & 0xFFu) << (8 * (e & 3));
+          q = (int)fminf(fmaxf(rintf(v[e] / sc), -127.f), 127.f);
+        w[e >> 2] |= ((uint32_t)q & 0xFFu) << (8 * (e & 3));
       }
     }
     out[c] = uint4{w[0], w[1], w[2], w[3]};
@@ -459,22 +494,23 @@ __global__ __launch_bounds__(256) void k_w8a8_align(const int8_t* q, int64_t ld_
 
 // The choice over a row's parts, 8 per thread at a time: their loads together,
 // the largest m first, then every part's sum relative to it.
-constexpr int kChoice = 256, kChoiceN = 8;
-__global__ __launch_bounds__(kChoice) void k_choice(const Part* parts, int64_t nparts, int32_t* out_token,
+constexpr int kChoiceN = 8;
+template <int TH>
+__global__ __launch_bounds__(TH) void k_choice(const Part* parts, int64_t nparts, int32_t* out_token,
                                                     float* out_logit, float* out_lse) {
-  __shared__ Part sh[kChoice / 64];
+  __shared__ Part sh[TH / 64];
   const int64_t q = blockIdx.x;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const Part* row = parts + q * nparts;
   Part p = part_empty();
-  for (int64_t i0 = threadIdx.x; i0 < nparts; i0 += kChoice * kChoiceN) {
+  for (int64_t i0 = threadIdx.x; i0 < nparts; i0 += TH * kChoiceN) {
     Part v[kChoiceN];
 #pragma unroll
-    for (int i = 0; i < kChoiceN; ++i) v[i] = row[min(i0 + i * kChoice, nparts - 1)];
+    for (int i = 0; i < kChoiceN; ++i) v[i] = row[min(i0 + i * TH, nparts - 1)];
     float m = p.m, s = 0.f;
 #pragma unroll
     for (int i = 0; i < kChoiceN; ++i) {
-      if (i0 + i * kChoice >= nparts) v[i] = part_empty();
+      if (i0 + i * TH >= nparts) v[i] = part_empty();
       choice_key(p, v[i].key, v[i].z, v[i].id);
       m = fmaxf(m, v[i].m);
     }
@@ -486,10 +522,9 @@ __global__ __launch_bounds__(kChoice) void k_choice(const Part* parts, int64_t n
   p = wave_choice(p);
   if (lane == 0) sh[wave] = p;
   __syncthreads();
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int w = 1; w < kChoice / 64; ++w) p = choice_merge(p, sh[w]);
-    write_choice(p, q, out_token, out_logit, out_lse);
+  if (wave == 0) {
+    p = wave_choice(lane < TH / 64 ? sh[lane] : part_empty());
+    if (lane == 0) write_choice(p, q, out_token, out_logit, out_lse);
   }
 }
 
@@ -533,13 +568,17 @@ Plan plan_of(int64_t n, int64_t k, int64_t B) {
 
 // Whether W passes the caches by: its rows are read by one workgroup alone, and
 // too many to be there still at the next call, at least once other work has run.
-// Waves sharing k gain from 64 MB (1 x 128256 x 1024, 131 MB, three weights in
-// turn: 21.7 -> 19.8 us, one weight again and again 19.8 -> 19.0; below it 1 x
-// 4096 x 4096 5.3 -> 5.5 and 4.4 -> 4.6).  Tiles gain where W is larger than the
-// Infinity Cache (64 x 151936 x 2560, 389 MB: 87.5 -> 83.8; 128 x 128256 x 2048,
-// 263 MB: 67.7 -> 71.0, again and again 67.0 -> 69.7).
+// The more tokens, the more of the time is other than W's, and the larger the W
+// that gains.  us with several weights in turn, then (one weight again and again):
+//   waves sharing k: 1 x 4096 x 4096 5.3 -> 5.5 (4.4 -> 4.6), 1 x 128256 x 1024,
+//     131 MB, 21.7 -> 19.8 (19.8 -> 19.0);
+//   up to 32 tokens: 32 x 65536 x 1024, 67 MB, 16.1 -> 16.0 (13.7 -> 14.9), 32 x
+//     128256 x 2048, 263 MB, 51.8 -> 50.3 (45.5 -> 49.2);
+//   more: 64 x 65536 x 2048, 134 MB, 29.1 -> 29.9 (24.8 -> 28.5), 128 x 128256 x
+//     2048 67.7 -> 71.0 (67.0 -> 69.7), 64 x 151936 x 2560, 389 MB, 87.5 -> 83.8.
 bool past_caches(const Plan& p, int64_t n, int64_t k, int64_t B) {
-  return p.token_tiles(B) == 1 && w8a8_packed_bytes(n, k) > (p.kind < k16 ? int64_t(64) << 20 : int64_t(256) << 20);
+  const int64_t from = (int64_t)(p.kind < k16 ? 64 : p.kind < k64 ? 128 : 256) << 20;
+  return p.token_tiles(B) == 1 && w8a8_packed_bytes(n, k) > from;
 }
 
 template <int FT, int FN, int KW, int G, bool PAST, bool BF16, bool HEAD>
@@ -639,7 +678,10 @@ hipError_t launch_w8a8_align(const int8_t* q, int64_t ld_q, int64_t B, int64_t k
 
 hipError_t launch_choice(const Part* parts, int64_t B, int64_t nparts, int32_t* out_token, float* out_logit,
                          float* out_lse, hipStream_t st) {
-  hipLaunchKernelGGL(k_choice, dim3((unsigned)B), dim3(kChoice), 0, st, parts, nparts, out_token, out_logit, out_lse);
+  if (nparts > 256 * kChoiceN)  // the head of 1 x 128256 x 2048, 8016 parts: 44.9 us with 1024 threads, 46.9 with 256
+    hipLaunchKernelGGL(k_choice<1024>, dim3((unsigned)B), dim3(1024), 0, st, parts, nparts, out_token, out_logit, out_lse);
+  else
+    hipLaunchKernelGGL(k_choice<256>, dim3((unsigned)B), dim3(256), 0, st, parts, nparts, out_token, out_logit, out_lse);
   return hipGetLastError();
 }
 

@@ -119,6 +119,25 @@ def test_quantised_weight(dt):
     assert torch.equal(c2, codes) and torch.equal(s2, scales)
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("k", [1, 5, 77, 135, 600])
+def test_quantised_weight_of_any_width(dt, k):
+    """Rows that are no whole loads, a large element in the last place."""
+    from lm_output_head_amd import W8A8Head
+    W = torch.randn(37, k, device="cuda").to(dt)
+    W[:, -1] = -5
+    say("quantised weight", dt, k)
+    codes, scales = W8A8Head(W).codes()
+    w, c, s = W.double().cpu().numpy(), codes.cpu().numpy().astype(np.float64), scales.double().cpu().numpy()
+    want = np.abs(w).max(1) / 127
+    assert np.all(np.abs(s - want) <= U * want)
+    assert np.all(c[np.abs(w).max(1) == 5, -1] == -127)  # a draw of more than 5 makes another element the largest
+    assert np.all(np.abs(c - w / s[:, None]) <= 0.5 + 128 * U)
+    W[36, -1] = float("nan")
+    with pytest.raises(Exception, match="infinity or NaN"):
+        W8A8Head(W)
+
+
 def test_non_finite_weights_are_refused():
     from lm_output_head_amd import FlashHeadError, W8A8Head
     for bad in (float("inf"), float("nan")):
