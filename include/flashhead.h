@@ -451,8 +451,7 @@ fh_status fh_cluster(const void* E, fh_dtype dtype, int64_t v, int64_t d, int64_
  *                 out_residual and the pair (out_q, out_scale) may be NULL,
  *                 not all.  out or out_residual may be x or residual itself
  *                 (same address and stride); no other overlap.
- * 1 <= B < 2^31, 1 <= d < 2^31.  Any alignment of the elements' own size;
- * rows aligned to 16 bytes are read and written 16 bytes at a time.
+ * 1 <= B < 2^31, 1 <= d < 2^31.  Any alignment of the elements' own size.
  */
 fh_status fh_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
                      const void* weight, fh_dtype dtype, int64_t B, int64_t d, float eps,
@@ -539,7 +538,7 @@ typedef struct {
   const int32_t* n_prompt;    /* [B] ids at the row's start that are its prompt; NULL: 0 */
   const int32_t* n_history;   /* [B] ids of the row that count, clamped to
                                  [0, history_len]; NULL: history_len */
-  const float* repetition;    /* [B] > 0: ids in prompt or output, z > 0 ? z / r : z r */
+  const float* repetition;    /* [B] > 0: ids in prompt or output, z > 0 ? z (1 / r) : z r */
   const float* frequency;     /* [B]: z -= f times its count in the output */
   const float* presence;      /* [B]: z -= p if it is in the output */
   const int32_t* bias_ids;    /* [B x bias_len] ids, row stride ld_bias */

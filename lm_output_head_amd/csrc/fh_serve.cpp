@@ -189,7 +189,7 @@ fh_status fh_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t 
     if (d < 1 || d > kMaxRows) return fail(FH_EINVAL, "d outside [1, 2^31 - 1]");
     if (!(eps >= 0.f && std::isfinite(eps))) return fail(FH_EINVAL, "eps must be finite and >= 0");
     if (!std::isfinite(weight_offset)) return fail(FH_EINVAL, "weight_offset must be finite");
-    const struct { const char* name; const void* p; int64_t ld; bool elems; } rows[] = {
+    const struct Rows { const char* name; const void* p; int64_t ld; bool elems; } rows[] = {
         {"ld_x", x, ld_x, true}, {"ld_residual", residual, ld_residual, true}, {"ld_out", out, ld_out, true},
         {"ld_out_residual", out_residual, ld_out_residual, true}, {"ld_q", out_q, ld_q, false}};
     const size_t elem = dtype == FH_BF16 ? 2 : 4;
@@ -201,6 +201,11 @@ fh_status fh_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t 
     }
     if ((weight && !aligned_to(weight, elem)) || (out_scale && !aligned_to(out_scale, 4)))
       return fail(FH_EINVAL, "weight and out_scale must be aligned to their elements");
+    if (out && out == out_residual) return fail(FH_EINVAL, "out and out_residual are the same storage");
+    for (const auto& o : {rows[2], rows[3]})
+      for (const auto& i : {rows[0], rows[1]})
+        if (B > 1 && o.p && o.p == i.p && o.ld != i.ld)
+          return fail(FH_EINVAL, std::string(o.name) + " and " + i.name + " differ on the same storage");
     fh::NormArgs a{};
     a.x = x;
     a.residual = residual;
@@ -352,6 +357,8 @@ fh_status fh_logits_apply(const float* logits, int64_t ld_logits, const int32_t*
     if (s == FH_OK && ids) s = check_ld("ld_ids", ld_ids, n, B);
     if (s == FH_OK && out_logits) s = check_ld("ld_out", ld_out, n, B);
     if (s != FH_OK) return s;
+    if (out_logits == logits && ld_out != ld_logits && B > 1)
+      return fail(FH_EINVAL, "ld_out and ld_logits differ on the same storage");
     fh::RulesArgs a{};
     const fh_logit_rules none{};
     const fh_logit_rules& l = rules ? *rules : none;

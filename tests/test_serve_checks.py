@@ -55,6 +55,9 @@ NORM = dict(x=A, ld_x=64, residual=A, ld_residual=64, weight=A, dtype=1, B=4, d=
     ({"weight": P((1 << 20) + 1)}, "aligned"),
     ({"dtype": 0, "out": P((1 << 20) + 2)}, "aligned"),
     ({"scale": P((1 << 20) + 2)}, "aligned"),
+    ({}, "out and out_residual are the same storage"),
+    ({"out_residual": None, "ld_out": 65}, "ld_out and ld_x differ"),
+    ({"out": None, "x": P(1 << 21), "ld_residual": 70}, "ld_out_residual and ld_residual differ"),
 ])
 def test_norm_refusals(lib, kw, needle):
     _refused(lib, lib.fh_rmsnorm(*dict(NORM, **kw).values()), needle)
@@ -106,6 +109,7 @@ CALL = dict(z=A, ld=100, ids=None, ld_ids=0, B=3, n=100, v=100, rules=None, mode
     ({"n": 0, "v": 0}, "n and v"),
     ({"v": 101}, "n = v"),
     ({"out": None, "token": None}, "no output"),
+    ({"ld_out": 104}, "differ on the same storage"),
     ({"mode": 1}, "mode"),
     ({"mode": 4}, "mode"),
     ({"mode": 2, "T": 0.0}, "temperature"),
