@@ -557,9 +557,9 @@ typedef struct {
 } fh_logit_rules;
 
 /*
- * fh_logits_workspace — bytes of workspace of a fh_logits_apply call over
- * [B x n] logits that asks for tokens or LSEs (0 is enough for one that does
- * not), or FH_EINVAL.
+ * fh_logits_workspace — bytes of workspace that are enough for a
+ * fh_logits_apply call over [B x n] logits that asks for tokens or LSEs (0 for
+ * short rows, and for a call that does not), or FH_EINVAL.
  */
 int64_t fh_logits_workspace(int64_t B, int64_t n);
 

@@ -57,9 +57,8 @@ __device__ __forceinline__ void load_run(const T* p, int i, int n, T other, T (&
 template <bool DENSE, int TILE, int TH>
 struct Tables {
   static constexpr int kSize = DENSE ? TILE : 2 * TILE;
-  static constexpr int kBits = 32768;
-  alignas(16) uint32_t count[kSize];
-  alignas(16) float bias[DENSE ? 4 : kSize];
+  static constexpr int kBits = TILE > 4096 ? 65536 : 32768;
+  alignas(16) uint32_t count[kSize];  // then the sums of the biases, or the logits of dense rows
   alignas(16) int32_t key[DENSE ? 4 : kSize];
   alignas(16) uint32_t maybe[DENSE ? 4 : kBits / 32];
   // a list's entries that fall into the tile, by wave, in order
@@ -72,10 +71,7 @@ struct Tables {
     const i32x4a zero{0, 0, 0, 0};
     for (int i = 4 * tid; i < kSize; i += 4 * TH) {
       *reinterpret_cast<i32x4a*>(&count[i]) = zero;
-      if constexpr (!DENSE) {
-        *reinterpret_cast<i32x4a*>(&bias[i]) = zero;
-        *reinterpret_cast<i32x4a*>(&key[i]) = i32x4a{kFree, kFree, kFree, kFree};
-      }
+      if constexpr (!DENSE) *reinterpret_cast<i32x4a*>(&key[i]) = i32x4a{kFree, kFree, kFree, kFree};
     }
     if constexpr (!DENSE)
       for (int i = 4 * tid; i < kBits / 32; i += 4 * TH) *reinterpret_cast<i32x4a*>(&maybe[i]) = zero;
@@ -113,9 +109,9 @@ struct Tables {
 
 // G runs of W consecutive logits per thread: a tile is TH W G.  Held to the
 // registers of six waves per SIMD (64 x 151936 sampled, the whole call: 30.8 us at
-// five, 30.5 at six, 31.6 at seven).
+// five, 30.5 at six, 31.6 at seven); workgroups of sixteen waves to four.
 template <bool DENSE, int TH, int W, int G>
-__global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(6))) void k_rules(RulesArgs a) {
+__global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(TH == 1024 ? 4 : 6))) void k_rules(RulesArgs a) {
   constexpr int kTile = TH * W * G, N = W * G, kBatch = 4 * TH * kAhead;  // ids of the history at once
   typedef Tables<DENSE, kTile, TH> Table;
   static_assert(DENSE || ((Table::kSize & (Table::kSize - 1)) == 0 && Table::kSize <= 65536), "the hash masks 16 bits");
@@ -271,11 +267,16 @@ __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(6))) void k_
   }
   if (a.bias_ids) {
     // dense rows: the logits themselves in the table, each to its own thread's
-    // words, which only that thread has read above
-    float* sums = DENSE ? reinterpret_cast<float*>(sh.count) : sh.bias;
+    // words, which only that thread has read above; else the counts make room
+    float* sums = reinterpret_cast<float*>(sh.count);
     if constexpr (DENSE) {
 #pragma unroll
       for (int i = 0; i < N; ++i) sums[place[i]] = z[i];
+    } else if (a.history) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (open[i]) sums[place[i]] = 0.f;
     }
     for (int i0 = 0; i0 < nb; i0 += TH) {
       if (i0 > 0) load_bias(i0 + tid);
@@ -329,7 +330,7 @@ __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(6))) void k_
           if (at + e < width) out[at + e] = z[W * j + e];
     }
   }
-  if (a.parts) {
+  if (a.choice) {
     uint32_t word[N] = {};
     if (a.token_sample) {
 #pragma unroll
@@ -348,43 +349,70 @@ __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(6))) void k_
     __syncthreads();
     if (wave == 0) {
       part = wave_choice(lane < TH / 64 ? sh.parts[lane] : part_empty());
-      if (lane == 0) a.parts[b * gridDim.x + blockIdx.x] = part;
+      if (lane == 0) {
+        if (gridDim.x == 1)
+          write_choice(part, b, a.out_token, a.out_token_logit, a.out_lse);
+        else
+          a.parts[b * gridDim.x + blockIdx.x] = part;
+      }
     }
   }
 }
 
-// Tiles of a call: large ones walk the history less often, small ones spread few
-// rows over the CUs; the large one where it leaves two workgroups per CU (64 x
-// 151936 with 8192 of history, sampled, the whole call: 30.5 us with tiles of
-// 4096, 32.9 with 2048, 38.4 with 8192; 1 x 128256: the kernel 6.5 us with 1024,
-// 12.9 with 4096).  Candidates' tiles have a thread per candidate or two, so that the
-// history, which each of them searches for, is short per thread (8 x 8192 with
-// 32768 of history: 36 us with 512 threads for 512 candidates, 69 with 256 for
-// 256; 64 x 8192 with 8192: 27 us with 512 threads for 1024, 37 with 256).
-int tile_of(int64_t B, int64_t n, bool dense) {
-  const int large = dense ? 4096 : 1024, small = dense ? 1024 : 512;
-  return B * ((n + large - 1) / large) >= 512 ? large : small;
+// The tile of a call.  A row of one tile writes its choice itself: no second
+// launch, 3 us of the host's time and as much of the GPU's.
+struct Shape {
+  int tile, threads;
+  void (*kernel)(RulesArgs);
+};
+
+// Dense rows (us of the GPU's time, sampled, 1000 or 2000 tokens of history).
+// One tile up to 8192 tokens (64 x 4000: 8.9 with one of 1024 threads, 9.7 with
+// four of 256; 1024 threads hold few rows of a CU, so many rows take 256; 256 x
+// 6000: 12.5 with 8192 to a tile, 14.2 with 1024, 1 x 6000 10.9 and 8.7, but 12.2
+// and 15.4 with the host's).  Beyond, small tiles spread few rows over the CUs,
+// large ones walk the history less often; the large one where it leaves two
+// workgroups per CU (64 x 151936: 26.3 with tiles of 4096, 32.4 with 1024, 27.1
+// with 8192, 37.8 with 16384; 1 x 151936: 11.2, 8.5, 12.1 and 14.8).
+Shape dense_shape(int64_t B, int64_t n) {
+  const Shape small{1024, 256, k_rules<true, 256, 4, 1>}, large{4096, 256, k_rules<true, 256, 4, 4>};
+  if (n <= 1024) return small;
+  if (n <= 4096 && B < 512) return Shape{4096, 1024, k_rules<true, 1024, 4, 1>};
+  if (n > 4096 && n <= 8192) return Shape{8192, 512, k_rules<true, 512, 4, 4>};
+  return B * ((n + large.tile - 1) / large.tile) >= 512 ? large : small;
 }
+
+// Listed tokens: each tile searches for the whole history, so a tile has a thread
+// per token or few, and a CU at most one tile where that can be (1000 of history:
+// 8 x 8192 12.1 with tiles of 512, 15.0 with 4096; 64 x 8192 20.1 with 512, 17.4
+// with 2048, 23.7 with 8192; 256 x 8192 47.0 with 512, 47.9 with 2048, 27.3 with
+// 8192).  Up to 4096 tokens one tile (64 x 1000 9.7, 12.0 in two; 64 x 3000 14.0,
+// as in six; 1 x 4096 14.6, 11.1 in eight, but 14.5 and 16.3 with the host's).
+Shape list_shape(int64_t B, int64_t n) {
+  const Shape shapes[] = {{512, 512, k_rules<false, 512, 1, 1>},
+                          {1024, 512, k_rules<false, 512, 1, 2>},
+                          {2048, 1024, k_rules<false, 1024, 1, 2>},
+                          {4096, 1024, k_rules<false, 1024, 1, 4>},
+                          {8192, 1024, k_rules<false, 1024, 1, 8>}};
+  if (n <= 512) return shapes[0];
+  if (n <= 4096) return shapes[n <= 1024 ? 2 : 3];
+  for (const Shape& s : shapes)
+    if (B * ((n + s.tile - 1) / s.tile) <= 256) return s;
+  return shapes[4];
+}
+
+Shape shape_of(int64_t B, int64_t n, bool dense) { return dense ? dense_shape(B, n) : list_shape(B, n); }
 
 }  // namespace
 
 int64_t rules_parts(int64_t B, int64_t n, bool dense) {
-  const int tile = tile_of(B, n, dense);
+  const int tile = shape_of(B, n, dense).tile;
   return (n + tile - 1) / tile;
 }
 
 hipError_t launch_rules(const RulesArgs& a, int64_t B, hipStream_t st) {
-  const dim3 grid((unsigned)rules_parts(B, a.n, !a.ids), (unsigned)B);
-  switch (tile_of(B, a.n, !a.ids)) {
-    case 4096: hipLaunchKernelGGL((k_rules<true, 256, 4, 4>), grid, dim3(256), 0, st, a); break;
-    case 1024:
-      if (a.ids)
-        hipLaunchKernelGGL((k_rules<false, 512, 1, 2>), grid, dim3(512), 0, st, a);
-      else
-        hipLaunchKernelGGL((k_rules<true, 256, 4, 1>), grid, dim3(256), 0, st, a);
-      break;
-    default: hipLaunchKernelGGL((k_rules<false, 512, 1, 1>), grid, dim3(512), 0, st, a);
-  }
+  const Shape s = shape_of(B, a.n, !a.ids);
+  hipLaunchKernelGGL(s.kernel, dim3((unsigned)((a.n + s.tile - 1) / s.tile), (unsigned)B), dim3(s.threads), 0, st, a);
   return hipGetLastError();
 }
 

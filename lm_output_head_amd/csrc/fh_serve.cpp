@@ -156,6 +156,12 @@ fh_status check_product(const fh_w8a8* w, const int8_t* q, int64_t ld_q, const f
   return s;
 }
 
+// The rules' partials; a row of one part needs none.
+int64_t rules_bytes(int64_t B, int64_t n, bool dense) {
+  const int64_t parts = fh::rules_parts(B, n, dense);
+  return parts > 1 ? (int64_t)sizeof(fh::Part) * B * parts : 0;
+}
+
 // q's rows where the kernel can read them, in fields q and ld_q of a.
 hipError_t take_rows(const fh_w8a8* w, const int8_t* q, int64_t ld_q, int64_t B, void* workspace, hipStream_t st,
                      fh::W8A8Args* a) {
@@ -336,7 +342,7 @@ int64_t fh_logits_workspace(int64_t B, int64_t n) {
   return guarded<int64_t>(FH_ENOMEM, [&]() -> int64_t {
     if (B < 1 || B > 65535) return fail(FH_EINVAL, "B outside [1, 65535]");
     if (n < 1 || n > kMaxWidth) return fail(FH_EINVAL, "n outside [1, 2^30]");
-    return (int64_t)sizeof(fh::Part) * B * std::max(fh::rules_parts(B, n, true), fh::rules_parts(B, n, false));
+    return std::max(rules_bytes(B, n, true), rules_bytes(B, n, false));
   });
 }
 
@@ -390,7 +396,7 @@ fh_status fh_logits_apply(const float* logits, int64_t ld_logits, const int32_t*
     } else if (l.mask_row) {
       return fail(FH_EINVAL, "mask_row needs a mask");
     }
-    if (s == FH_OK && choice) s = check_workspace(workspace, workspace_bytes, fh_logits_workspace(B, n));
+    if (s == FH_OK && choice) s = check_workspace(workspace, workspace_bytes, rules_bytes(B, n, !ids));
     if (s != FH_OK) return s;
     a.z = logits;
     a.ld_z = ld_logits;
@@ -420,11 +426,16 @@ fh_status fh_logits_apply(const float* logits, int64_t ld_logits, const int32_t*
     a.seed = seed;
     a.out = out_logits;
     a.ld_out = ld_out;
-    a.parts = choice ? static_cast<fh::Part*>(workspace) : nullptr;
+    a.choice = choice;
+    a.out_token = out_token;
+    a.out_token_logit = out_token_logit;
+    a.out_lse = out_lse;
+    a.parts = static_cast<fh::Part*>(workspace);
     hipStream_t st = static_cast<hipStream_t>(stream);
     hipError_t r = fh::launch_rules(a, B, st);
-    if (r == hipSuccess && choice)
-      r = fh::launch_choice(a.parts, B, fh::rules_parts(B, n, !ids), out_token, out_token_logit, out_lse, st);
+    const int64_t parts = fh::rules_parts(B, n, !ids);
+    if (r == hipSuccess && choice && parts > 1)
+      r = fh::launch_choice(a.parts, B, parts, out_token, out_token_logit, out_lse, st);
     return r == hipSuccess ? FH_OK : hip_fail(r, "logit rules launch");
   });
 }

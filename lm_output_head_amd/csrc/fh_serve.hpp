@@ -88,9 +88,13 @@ struct RulesArgs {
   uint64_t seed;
   float* out;            // or null
   int64_t ld_out;
-  Part* parts;           // [B x rules_parts], or null: no choice
+  int choice;            // whether a token is chosen:
+  int32_t* out_token;    // a row of one part writes it here (or null),
+  float* out_token_logit;
+  float* out_lse;
+  Part* parts;           // others their partials [B x rules_parts]
 };
-int64_t rules_parts(int64_t B, int64_t n, bool dense);  // partials per row
+int64_t rules_parts(int64_t B, int64_t n, bool dense);  // partials per row; one is its choice
 hipError_t launch_rules(const RulesArgs& a, int64_t B, hipStream_t st);
 // the choice over each row's parts (w8a8 head, rules)
 hipError_t launch_choice(const Part* parts, int64_t B, int64_t nparts, int32_t* out_token,

@@ -55,10 +55,13 @@ def apply_rules(z, ids, v, *, history=None, n_prompt=None, n_history=None, repet
             with np.errstate(invalid="ignore"):
                 z[b] = np.where(hit, np.where(z[b] > 0, z[b] / rep, z[b] * rep), z[b])
             c = np.where(known, count[tt], 0)
-            drop = c * (0.0 if frequency is None else float(frequency[b]))
-            drop = drop + (c > 0) * (0.0 if presence is None else float(presence[b]))
-            size[b] = np.abs(z[b]) + np.abs(drop)
-            z[b] -= drop
+            often = c * (0.0 if frequency is None else float(frequency[b]))
+            once = (c > 0) * (0.0 if presence is None else float(presence[b]))
+            # each step's own magnitude: z - often is rounded at up to |z| + |often|, also
+            # where presence then takes it back (f = 0.1807, p = -0.1743, z = -0.0055:
+            # 2^-24 * 0.186 = 1.1e-8, where 8 * 2^-24 (|z| + |often + once|) is 5.6e-9)
+            size[b] = np.abs(z[b]) + np.abs(often) + np.abs(once)
+            z[b] -= often + once
         if bias_ids is not None:
             N = bias_ids.shape[1]
             nb = int(np.clip(N if n_bias is None else n_bias[b], 0, N))

@@ -71,7 +71,9 @@ def run_and_check(z, ids, v, r, mode, T, seed=9):
 
 CASES = [(1, 1, 1, 1, 0.9), (1, 33, 0, 0, 0.5), (2, 1000, 50, 0, 0.0), (3, 4096, 300, 7, 0.25), (2, 4097, 0, 300, 0.25),
          (4, 5001, 1000, 20, 0.01), (2, 12293, 700, 600, 0.0), (5, 20000, 9000, 64, 0.3), (64, 300, 40, 3, 0.5), (64, 33000, 5000, 20, 0.5),
-         (1, 128256, 1000, 16, 0.25), (3, 40057, 5000, 1, 0.9)]
+         (1, 128256, 1000, 16, 0.25), (3, 40057, 5000, 1, 0.9),
+         # each way of cutting a call up
+         (520, 3001, 200, 5, 0.5), (3, 1025, 100, 4, 0.5), (200, 8192, 3000, 20, 0.5)]
 
 
 @pytest.mark.parametrize("B,v,L,nb,density", CASES)
@@ -85,7 +87,9 @@ def test_dense(B, v, L, nb, density, mode, T):
 @pytest.mark.parametrize("B,v,n,L,nb,density", [(1, 10, 1, 3, 2, 0.5), (3, 1000, 64, 100, 10, 0.5), (2, 5000, 1024, 0, 30, 0.3),
                                                 (2, 5000, 1025, 600, 0, 0.0), (4, 128256, 8192, 2000, 32, 0.25),
                                                 (3, 3000, 3000, 500, 8, 0.9), (2, 2000, 5001, 500, 8, 0.9),
-                                                (64, 20000, 8200, 5000, 20, 0.5)])
+                                                (64, 20000, 8200, 5000, 20, 0.5), (5, 700, 2500, 400, 8, 0.9),
+                                                (16, 20000, 12000, 3000, 20, 0.5), (64, 9000, 8000, 500, 30, 0.5),
+                                                (130, 9000, 8192, 2000, 1100, 0.5), (130, 20000, 9000, 9000, 30, 0.5)])
 @pytest.mark.parametrize("mode,T", [(0, 1.0), (2, 0.8)])
 def test_candidates(B, v, n, L, nb, density, mode, T):
     """Listed tokens in any order, some twice, some no tokens (-1, v)."""

@@ -118,9 +118,9 @@ CALL = dict(z=A, ld=100, ids=None, ld_ids=0, B=3, n=100, v=100, rules=None, mode
     ({"ids": A, "ld_ids": 99}, "ld_ids"),
     ({"ld_out": 99}, "ld_out"),
     ({"z": P((1 << 20) + 2)}, "aligned"),
-    ({"ws": None}, "workspace"),
-    ({"ws_bytes": 8}, "workspace"),
-    ({"ws": P((1 << 20) + 4)}, "16-byte aligned"),
+    ({"ws": None, "n": 20000, "v": 20000, "ld": 20000, "ld_out": 20000}, "workspace"),
+    ({"ws_bytes": 8, "n": 20000, "v": 20000, "ld": 20000, "ld_out": 20000}, "workspace"),
+    ({"ws": P((1 << 20) + 4), "n": 20000, "v": 20000, "ld": 20000, "ld_out": 20000}, "16-byte aligned"),
     ({"rules": {"ld_history": 9}}, "ld_history"),
     ({"rules": {"history_len": -1}}, "history_len"),
     ({"rules": {"history_len": (1 << 30) + 1, "ld_history": 1 << 31}}, "history_len"),
@@ -143,7 +143,8 @@ def test_rules_refusals(lib, kw, needle):
 
 
 def test_workspace_sizes(lib):
-    assert lib.fh_logits_workspace(3, 100) > 0
+    assert lib.fh_logits_workspace(3, 20000) > 0
+    assert lib.fh_logits_workspace(3, 100) == 0
     for B, n in [(0, 10), (65536, 10), (1, 0), (1, (1 << 30) + 1)]:
         _refused(lib, lib.fh_logits_workspace(B, n), "outside")
 
