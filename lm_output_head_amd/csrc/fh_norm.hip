@@ -2,9 +2,9 @@
 // with a scale per row: s = x + residual, y = s / sqrt(mean(s^2) + eps) *
 // (offset + weight), q = rint(y / (max |y| / 127)), all in float32 with one
 // rounding per output.  Bound by the bytes of its rows: 16384 x 2560 bfloat16
-// with a residual and all outputs in 79.7 us, 4.74 TB/s (a copy reaches 4.80; 266
-// us when each pass read the row again).  One row of 2048 takes 2.9 us: a load,
-// two reductions and a store on end.
+// with a residual, the sum and the codes in 70.5 us, 5.36 TB/s (a copy reaches 4.80;
+// 266 us when each pass read the row again).  One row of 2048 takes 2.9 us: a
+// load, two reductions and a store on end.
 
 #include <hip/hip_runtime.h>
 
@@ -109,9 +109,18 @@ __device__ __forceinline__ void store_codes(int8_t* p, int64_t at, int64_t d, co
   }
 }
 
-__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+// Sum and maximum over the L lanes that share a row.
+template <int L>
+__device__ __forceinline__ float lane_sum(float v) {
+  if constexpr (L == 64) return wave_sum(v);
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
+  for (int m = 1; m < L; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t lane_umax(uint32_t v) {
+#pragma unroll
+  for (int m = 1; m < L; m <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
   return v;
 }
 
@@ -129,28 +138,30 @@ __device__ __forceinline__ V across(V v, V* sh, Op op) {
 
 __device__ __forceinline__ float scale_of(uint32_t top) { return __uint_as_float(top) / 127.f; }
 
-// W waves per row, C chunks per lane: the row stays in registers between its
-// one read and the writes.  A workgroup is max(4, W) waves.
-template <typename T, int W, int C>
+// W waves (or, W = 1, L of a wave's lanes) per row, C chunks per lane: the row
+// stays in registers between its one read and the writes.  A workgroup is
+// max(4, W) waves.
+template <typename T, int L, int W, int C>
 __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void k_rmsnorm(NormArgs a, int64_t B) {
-  constexpr int N = Elems<T>::N, kRows = W <= 4 ? 4 / W : 1;
+  static_assert(W == 1 || L == 64, "waves that share a row do so with all lanes");
+  constexpr int N = Elems<T>::N, kRows = W == 1 ? 256 / L : 1, kLanes = L * W;
   static_assert(kRows == 1 || W == 1, "waves that share a row make up the workgroup");
   __shared__ float sum_sh[W];
   __shared__ uint32_t top_sh[W];
-  const int64_t b = (int64_t)blockIdx.x * kRows + (kRows > 1 ? threadIdx.x >> 6 : 0), d = a.d;
+  const int64_t b = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes, d = a.d;
   if (b >= B) return;
-  const int lane = kRows > 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int lane = threadIdx.x % kLanes;
   const T* x = static_cast<const T*>(a.x) + b * a.ld_x;
   const T* r = a.residual ? static_cast<const T*>(a.residual) + b * a.ld_residual : nullptr;
   const T* w = static_cast<const T*>(a.weight);
   float y[C][N];
 #pragma unroll
-  for (int c = 0; c < C; ++c) load_chunk<T>(x, (int64_t)N * (lane + 64 * W * c), d, y[c]);
+  for (int c = 0; c < C; ++c) load_chunk<T>(x, (int64_t)N * (lane + kLanes * c), d, y[c]);
   if (r) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float v[N];
-      load_chunk<T>(r, (int64_t)N * (lane + 64 * W * c), d, v);
+      load_chunk<T>(r, (int64_t)N * (lane + kLanes * c), d, v);
 #pragma unroll
       for (int i = 0; i < N; ++i) y[c][i] += v[i];
     }
@@ -160,7 +171,7 @@ __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void k_rmsnorm(NormArgs a, i
   if (a.out_residual) {
     T* o = static_cast<T*>(a.out_residual) + b * a.ld_out_residual;
 #pragma unroll
-    for (int c = 0; c < C; ++c) store_chunk<T>(o, (int64_t)N * (lane + 64 * W * c), d, y[c]);
+    for (int c = 0; c < C; ++c) store_chunk<T>(o, (int64_t)N * (lane + kLanes * c), d, y[c]);
     if (!a.out && !a.out_q) return;
   }
   float ss = 0.f;
@@ -168,12 +179,12 @@ __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void k_rmsnorm(NormArgs a, i
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int i = 0; i < N; ++i) ss = fmaf(y[c][i], y[c][i], ss);
-  ss = across<W>(wave_sum(ss), sum_sh, [](float p, float q) { return p + q; });
+  ss = across<W>(lane_sum<L>(ss), sum_sh, [](float p, float q) { return p + q; });
   const float inv = 1.f / sqrtf(ss / (float)d + a.eps);
   uint32_t top = 0u;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int64_t at = (int64_t)N * (lane + 64 * W * c);
+    const int64_t at = (int64_t)N * (lane + kLanes * c);
     float v[N];
     if (w) load_chunk<T>(w, at, d, v);
 #pragma unroll
@@ -185,78 +196,119 @@ __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void k_rmsnorm(NormArgs a, i
     if (a.out) store_chunk<T>(static_cast<T*>(a.out) + b * a.ld_out, at, d, y[c]);
   }
   if (!a.out_q) return;
-  top = across<W>(wave_umax(top), top_sh, [](uint32_t p, uint32_t q) { return max(p, q); });
+  top = across<W>(lane_umax<L>(top), top_sh, [](uint32_t p, uint32_t q) { return max(p, q); });
   if (lane == 0) a.out_scale[b] = scale_of(top);
   const CodeScale cs(top);
 #pragma unroll
   for (int c = 0; c < C; ++c)
-    store_codes<N>(a.out_q + b * a.ld_q, (int64_t)N * (lane + 64 * W * c), d, y[c], cs);
+    store_codes<N>(a.out_q + b * a.ld_q, (int64_t)N * (lane + kLanes * c), d, y[c], cs);
 }
 
 // Rows too long for the registers: three passes over the row, the later two from
 // the caches.
 template <typename T>
 __global__ __launch_bounds__(1024) void k_rmsnorm_long(NormArgs a, int64_t B) {
-  constexpr int W = 16;
+  constexpr int W = 16, N = Elems<T>::N;
   __shared__ float sum_sh[W];
   __shared__ uint32_t top_sh[W];
-  const int tid = threadIdx.x;
-  const int64_t d = a.d;
+  const int64_t d = a.d, first = (int64_t)N * threadIdx.x, step = (int64_t)N * 64 * W;
   const T* w = static_cast<const T*>(a.weight);
   for (int64_t b = blockIdx.x; b < B; b += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + b * a.ld_x;
     const T* r = a.residual ? static_cast<const T*>(a.residual) + b * a.ld_residual : nullptr;
-    auto sum_at = [&](int64_t i) { return Elems<T>::get(x[i]) + (r ? Elems<T>::get(r[i]) : 0.f); };
+    auto load_sum = [&](int64_t at, float (&s)[N]) {
+      load_chunk<T>(x, at, d, s);
+      if (r) {
+        float v[N];
+        load_chunk<T>(r, at, d, v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] += v[i];
+      }
+    };
     float ss = 0.f;
-    for (int64_t i = tid; i < d; i += 64 * W) {
-      const float s = sum_at(i);
-      ss = fmaf(s, s, ss);
+    for (int64_t at = first; at < d; at += step) {
+      float s[N];
+      load_sum(at, s);
+#pragma unroll
+      for (int i = 0; i < N; ++i) ss = fmaf(s[i], s[i], ss);
     }
     ss = across<W>(wave_sum(ss), sum_sh, [](float p, float q) { return p + q; });
     const float inv = 1.f / sqrtf(ss / (float)d + a.eps);
-    auto norm_at = [&](int64_t i, float s) { return w ? s * inv * (a.offset + Elems<T>::get(w[i])) : s * inv; };
+    auto norm = [&](int64_t at, const float (&s)[N], float (&y)[N]) {
+      float v[N];
+      if (w) load_chunk<T>(w, at, d, v);
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] = w ? s[i] * inv * (a.offset + v[i]) : s[i] * inv;
+    };
     uint32_t top = 0u;
     if (a.out_q) {
-      for (int64_t i = tid; i < d; i += 64 * W) top = max(top, abs_bits(norm_at(i, sum_at(i))));
-      top = across<W>(wave_umax(top), top_sh, [](uint32_t p, uint32_t q) { return max(p, q); });
-      if (tid == 0) a.out_scale[b] = scale_of(top);
+      for (int64_t at = first; at < d; at += step) {
+        float s[N], y[N];
+        load_sum(at, s);
+        norm(at, s, y);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (at + i < d) top = max(top, abs_bits(y[i]));
+      }
+      top = across<W>(lane_umax<64>(top), top_sh, [](uint32_t p, uint32_t q) { return max(p, q); });
+      if (threadIdx.x == 0) a.out_scale[b] = scale_of(top);
     }
     const CodeScale cs(top);
-    // an element is read and written by one thread, x and residual before the
+    // a chunk is read and written by one thread, x and residual before the
     // outputs that may be their own storage
-    for (int64_t i = tid; i < d; i += 64 * W) {
-      const float s = sum_at(i), y = norm_at(i, s);
-      if (a.out) static_cast<T*>(a.out)[b * a.ld_out + i] = Elems<T>::put(y);
-      if (a.out_residual) static_cast<T*>(a.out_residual)[b * a.ld_out_residual + i] = Elems<T>::put(s);
-      if (a.out_q) a.out_q[b * a.ld_q + i] = (int8_t)byte_of(cs.of(y));
+    for (int64_t at = first; at < d; at += step) {
+      float s[N], y[N];
+      load_sum(at, s);
+      norm(at, s, y);
+      if (a.out) store_chunk<T>(static_cast<T*>(a.out) + b * a.ld_out, at, d, y);
+      if (a.out_residual) store_chunk<T>(static_cast<T*>(a.out_residual) + b * a.ld_out_residual, at, d, s);
+      if (a.out_q) store_codes<N>(a.out_q + b * a.ld_q, at, d, y, cs);
     }
     __syncthreads();  // sum_sh and top_sh are free for the next row
   }
 }
 
-template <typename T, int W>
+// Chunks per lane that rows of these lanes and waves come to.
+template <int L, int W>
+constexpr int kMost = L < 64 ? 1 : W == 1 ? 3 : W == 16 ? 6 : 2;
+
+template <typename T, int L, int W>
 bool launch_w(const NormArgs& a, int64_t B, hipStream_t st) {
-  const int64_t chunks = (a.d + Elems<T>::N - 1) / Elems<T>::N, c = (chunks + 64 * W - 1) / (64 * W);
-  const int64_t rows = W == 1 ? 4 : 1;
-  const dim3 grid((unsigned)((B + rows - 1) / rows)), block(W <= 4 ? 256 : 64 * W);
-  if ((int64_t)grid.x * block.x >= int64_t(1) << 32) return false;  // more threads than a launch holds
+  const int64_t chunks = (a.d + Elems<T>::N - 1) / Elems<T>::N, c = (chunks + L * W - 1) / (L * W);
+  const int64_t rows = W == 1 ? 256 / L : 1, groups = (B + rows - 1) / rows;
+  const dim3 grid((unsigned)groups), block(W <= 4 ? 256 : 64 * W);
+  if (groups * block.x >= int64_t(1) << 32) return false;  // more threads than a launch holds
   switch (c) {
-#define FH_CASE(CC) \
-  case CC: hipLaunchKernelGGL((k_rmsnorm<T, W, CC>), grid, block, 0, st, a, B); return true;
-    FH_CASE(1) FH_CASE(2) FH_CASE(3) FH_CASE(4) FH_CASE(5) FH_CASE(6) FH_CASE(7) FH_CASE(8)
+#define FH_CASE(CC)                                                                                     \
+  case CC:                                                                                              \
+    if constexpr (CC <= kMost<L, W>) {                                                                  \
+      hipLaunchKernelGGL((k_rmsnorm<T, L, W, CC>), grid, block, 0, st, a, B);                           \
+      return true;                                                                                      \
+    }                                                                                                   \
+    return false;
+    FH_CASE(1) FH_CASE(2) FH_CASE(3) FH_CASE(4) FH_CASE(5) FH_CASE(6)
 #undef FH_CASE
     default: return false;
   }
 }
 
+// Lanes and waves per row, by its chunks of 16 bytes (us, bfloat16 with a residual
+// and all outputs): the fewest that keep a lane's chunks to one or two, more where
+// rows are few (64 x 2560: 4.9 with 8 waves, 5.6 with 4, 7.4 with 1; 16384 x 2560:
+// 81.7, 75.1 and 83.2; 16384 x 4096 106, 112 and 143; 4096 x 16384 115 with 16
+// waves, 123 with 8, 167 with 4; 16384 x 1152 35 with one wave, 43 with 4).
 template <typename T>
 void launch(const NormArgs& a, int64_t B, hipStream_t st) {
-  // a wave per row while rows are many and fit its lanes' 8 chunks; else the
-  // row's waves share it
   const int64_t chunks = (a.d + Elems<T>::N - 1) / Elems<T>::N;
-  if ((chunks <= 64 || (B > 2048 && chunks <= 64 * 8)) && launch_w<T, 1>(a, B, st)) return;
-  if (launch_w<T, 4>(a, B, st) || launch_w<T, 16>(a, B, st)) return;
-  hipLaunchKernelGGL((k_rmsnorm_long<T>), dim3((unsigned)std::min<int64_t>(B, 1 << 20)), dim3(1024), 0, st, a, B);
+  const bool done = chunks <= 8                      ? launch_w<T, 8, 1>(a, B, st)
+                    : chunks <= 16                   ? launch_w<T, 16, 1>(a, B, st)
+                    : chunks <= 32                   ? launch_w<T, 32, 1>(a, B, st)
+                    : chunks <= (B < 2048 ? 64 : 192) ? launch_w<T, 64, 1>(a, B, st)
+                    : chunks <= (B < 1024 ? 256 : 384) ? launch_w<T, 64, 4>(a, B, st)
+                    : chunks <= (B < 512 ? 512 : 1024) ? launch_w<T, 64, 8>(a, B, st)
+                                                     : launch_w<T, 64, 16>(a, B, st);
+  if (!done)
+    hipLaunchKernelGGL((k_rmsnorm_long<T>), dim3((unsigned)std::min<int64_t>(B, 1 << 20)), dim3(1024), 0, st, a, B);
 }
 
 }  // namespace

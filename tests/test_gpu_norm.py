@@ -63,7 +63,10 @@ def make(B, d, dt, seed, res):
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("B,d", [(1, 1), (1, 2048), (3, 7), (2, 64), (5, 1152), (17, 1000), (4, 2560), (2, 8192),
-                                 (300, 96), (3, 4104), (2, 16385), (1, 70001)])
+                                 (300, 96), (3, 4104), (2, 16385), (1, 70001),
+                                 # lanes, waves and chunks of each kind
+                                 (70, 16), (33, 61), (65, 127), (9, 130), (31, 256), (5, 513), (2050, 700), (2051, 1153),
+                                 (1030, 2570), (600, 7001), (3, 24000), (2, 49153)])
 def test_sizes(dt, B, d):
     from lm_output_head_amd import rmsnorm
     x, r, w = make(B, d, dt, B * d, True)
