@@ -219,18 +219,21 @@ __device__ __forceinline__ void lds_barrier() {
 // results overlap the other's products (head of 128 x 128256 sampled 102 -> 88
 // us; with the 250 registers of a 256 x 256 tile, one per CU, 4096 x 10240 x 2560
 // took 137 us, not 119).
-template <int FT, int FN, int WN, bool PAST, bool BF16, bool HEAD>
-__global__ __launch_bounds__(64 * WN) __attribute__((amdgpu_waves_per_eu(WN == 8 ? 4 : 1))) void k_w8a8_tile(W8A8Args a, int n_tiles, int q_tiles) {
+//
+// KW groups of WN waves share the tile: each takes a run of the blocks of k, with
+// buffers of its own, and the first adds up the sums.
+template <int FT, int FN, int WN, int KW, bool PAST, bool BF16, bool HEAD>
+__global__ __launch_bounds__(64 * WN * KW) __attribute__((amdgpu_waves_per_eu(WN * KW == 8 ? 4 : 1))) void k_w8a8_tile(W8A8Args a, int n_tiles, int q_tiles) {
   constexpr int kStage = kStepPad, kFrags = FT * kStage;  // fragments of a token block
   constexpr int kOwn = (kFrags + WN - 1) / WN;       // of them, this wave's to stage
   constexpr int kBlock = kFrags * 64;
   typedef typename Out<BF16>::T T;
   // results of 16 tokens on their way out, two buffers
   constexpr int kRow = 16 * FN * WN + 16 / (int)sizeof(T), kTurn = 16 * kRow;
-  constexpr int kShared = 2 * kBlock * 16, kStaged = 2 * kTurn * (int)sizeof(T);
-  __shared__ __attribute__((aligned(16))) char smem[kShared > kStaged ? kShared : kStaged];
+  constexpr int kShared = 2 * kBlock * 16 * KW, kStaged = 2 * kTurn * (int)sizeof(T);
+  constexpr int kSums = (KW - 1) * WN * FN * FT * 64 * 16;
+  __shared__ __attribute__((aligned(16))) char smem[std::max(kShared, std::max(kStaged, kSums))];
   __shared__ Part sP[HEAD ? WN : 1][HEAD ? 16 * FT : 1];
-  i32x4* sQ = reinterpret_cast<i32x4*>(smem);
 
   // workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles, token
   // tiles fastest, so that its L2 keeps the rows of W that they share
@@ -239,12 +242,14 @@ __global__ __launch_bounds__(64 * WN) __attribute__((amdgpu_waves_per_eu(WN == 8
   if ((int)(blockIdx.x >> 3) >= per || tile >= total) return;
   const int nt = tile / q_tiles, qt = tile % q_tiles;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = KW == 1 ? tid >> 6 : (tid >> 6) % WN, group = KW == 1 ? 0 : (tid >> 6) / WN;
   const int g = lane >> 4, col = lane & 15;
+  i32x4* sQ = reinterpret_cast<i32x4*>(smem) + group * 2 * kBlock;
   const int64_t rows = (a.n + 15) / 16;
   const int64_t t0 = ((int64_t)nt * WN + wave) * FN;
   const int q0 = qt * 16 * FT;
-  const int steps = w_steps(a.k), chunks = (a.k + 15) / 16, blocks = steps / kStage;
+  const int steps = w_steps(a.k), chunks = (a.k + 15) / 16;
+  const int blocks = (steps / kStage + KW - 1) / KW, first = group * blocks;  // the last group's may end past the row
 
   const i32x4* wp[FN];
 #pragma unroll
@@ -264,7 +269,7 @@ __global__ __launch_bounds__(64 * WN) __attribute__((amdgpu_waves_per_eu(WN == 8
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
       // a 16-byte chunk past the row stands in as its first: W is zero there
-      const int c = 4 * (kStage * blk + qs[i]) + g;
+      const int c = 4 * (kStage * (first + blk) + qs[i]) + g;
       qr[i] = *reinterpret_cast<const i32x4*>(qp[i] + 16 * (c < chunks ? c : 0));
     }
   };
@@ -279,7 +284,7 @@ __global__ __launch_bounds__(64 * WN) __attribute__((amdgpu_waves_per_eu(WN == 8
     for (int s = 0; s < kStage; ++s)
 #pragma unroll
       for (int m = 0; m < FN; ++m) {
-        const i32x4* p = wp[m] + (int64_t)min(kStage * blk + s, steps - 1) * 64;
+        const i32x4* p = wp[m] + (int64_t)min(kStage * (first + blk) + s, steps - 1) * 64;
         dst[s][m] = PAST ? __builtin_nontemporal_load(p) : *p;
       }
   };
@@ -288,7 +293,8 @@ __global__ __launch_bounds__(64 * WN) __attribute__((amdgpu_waves_per_eu(WN == 8
   for (int m = 0; m < FN; ++m)
 #pragma unroll
     for (int t = 0; t < FT; ++t) acc[m][t] = i32x4{0, 0, 0, 0};
-  auto multiply = [&](int buf, const i32x4 (&w)[kStage][FN]) {
+  auto multiply = [&](int blk, int buf, const i32x4 (&w)[kStage][FN]) {
+    if (KW > 1 && kStage * (first + blk) >= steps) return;
 #pragma unroll
     for (int s = 0; s < kStage; ++s) {
       i32x4 qf[FT];
@@ -314,7 +320,7 @@ __global__ __launch_bounds__(64 * WN) __attribute__((amdgpu_waves_per_eu(WN == 8
   for (int blk = 0; blk < blocks; blk += 2) {
     load_q(blk + 1);
     stay();
-    multiply(0, wf[0]);
+    multiply(blk, 0, wf[0]);
     stay();
     load_w(blk + 2, wf[0]);
     stay();
@@ -323,7 +329,7 @@ __global__ __launch_bounds__(64 * WN) __attribute__((amdgpu_waves_per_eu(WN == 8
     if (blk + 1 < blocks) {
       load_q(blk + 2);
       stay();
-      multiply(1, wf[1]);
+      multiply(blk + 1, 1, wf[1]);
       stay();
       load_w(blk + 3, wf[1]);
       stay();
@@ -336,34 +342,55 @@ __global__ __launch_bounds__(64 * WN) __attribute__((amdgpu_waves_per_eu(WN == 8
   // results go through LDS, so that a wave writes runs of whole rows (64 bytes
   // per token straight from the accumulators cost 22 us of 96 at 64 x 151936 and
   // 49 us of 187 at 4096 x 10240).
+  if constexpr (KW > 1) {
+    i32x4* sums = reinterpret_cast<i32x4*>(smem);
+    if (group > 0) {
+#pragma unroll
+      for (int m = 0; m < FN; ++m)
+#pragma unroll
+        for (int t = 0; t < FT; ++t) sums[((((group - 1) * WN + wave) * FN + m) * FT + t) * 64 + lane] = acc[m][t];
+    }
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int w = 0; w < KW - 1; ++w)
+#pragma unroll
+        for (int m = 0; m < FN; ++m)
+#pragma unroll
+          for (int t = 0; t < FT; ++t) acc[m][t] += sums[(((w * WN + wave) * FN + m) * FT + t) * 64 + lane];
+    }
+    __syncthreads();
+  }
   float ws[FN][4];
   load_scales<FN>(a, t0, g, ws);
   T* turn = reinterpret_cast<T*>(smem);
 #pragma unroll
   for (int t = 0; t < FT; ++t) {
-    const int64_t q = q0 + 16 * t + col;
-    const float qsc = q < a.B ? a.qs[q] : 0.f;
-    T* row = turn + (t & 1) * kTurn + col * kRow + 16 * FN * wave + 4 * g;
-    float z[FN][4];
+    if (group == 0) {
+      const int64_t q = q0 + 16 * t + col;
+      const float qsc = q < a.B ? a.qs[q] : 0.f;
+      T* row = turn + (t & 1) * kTurn + col * kRow + 16 * FN * wave + 4 * g;
+      float z[FN][4];
 #pragma unroll
-    for (int m = 0; m < FN; ++m) {
+      for (int m = 0; m < FN; ++m) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) z[m][i] = (float)acc[m][t][i] * (qsc * ws[m][i]);
-      typedef T V __attribute__((ext_vector_type(4)));
-      V o;
+        for (int i = 0; i < 4; ++i) z[m][i] = (float)acc[m][t][i] * (qsc * ws[m][i]);
+        typedef T V __attribute__((ext_vector_type(4)));
+        V o;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = Out<BF16>::of(z[m][i]);
-      if (a.out) *reinterpret_cast<V*>(row + 16 * m) = o;
-    }
-    if (HEAD) {
-      const Part p = column_choice(choose_tile<FN>(a, z, q, t0, g));
-      if (g == 0) sP[wave][16 * t + col] = p;
+        for (int i = 0; i < 4; ++i) o[i] = Out<BF16>::of(z[m][i]);
+        if (a.out) *reinterpret_cast<V*>(row + 16 * m) = o;
+      }
+      if (HEAD) {
+        const Part p = column_choice(choose_tile<FN>(a, z, q, t0, g));
+        if (g == 0) sP[wave][16 * t + col] = p;
+      }
     }
     if (a.out) {
       lds_barrier();  // the other buffer is read until the barrier after this one
       constexpr int kPer = 16 / (int)sizeof(T), kRuns = 16 * FN * WN / kPer;  // 16-byte runs of a token
 #pragma unroll
-      for (int c = tid; c < 16 * kRuns; c += 64 * WN) {
+      for (int c = tid; c < 16 * kRuns; c += 64 * WN * KW) {
         const int tok = c / kRuns, at = c % kRuns * kPer;
         const int64_t b = q0 + 16 * t + tok;
         if (b < a.B)
@@ -374,7 +401,7 @@ __global__ __launch_bounds__(64 * WN) __attribute__((amdgpu_waves_per_eu(WN == 8
   }
   if (HEAD) {
     __syncthreads();
-    for (int i = tid; i < 16 * FT && q0 + i < a.B; i += 64 * WN) {
+    for (int i = tid; i < 16 * FT && q0 + i < a.B; i += 64 * WN * KW) {
       Part p = sP[0][i];
 #pragma unroll
       for (int w = 1; w < WN; ++w) p = choice_merge(p, sP[w][i]);
@@ -531,8 +558,8 @@ __global__ __launch_bounds__(TH) void k_choice(const Part* parts, int64_t nparts
 unsigned grid_of(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20); }
 
 // How a call is cut up: a tile of k_w8a8_tile (named by its tokens), or a shape
-// of k_w8a8_few.
-enum Kind { kFew16Rows8, kFew16Rows4, kFew16Rows2, kTokens32Rows8, kTokens32Rows4, k16, k32, k64, k128 };
+// of k_w8a8_few.  x2, x4: groups that share a tile's k.
+enum Kind { kFew16Rows8, kFew16Rows4, kFew16Rows2, kTokens32Rows8, kTokens32Rows4, k16, k32, k32x2, k32x4, k64, k64x2, k128 };
 struct Plan {
   Kind kind;
   int rows, tokens;  // of a workgroup
@@ -549,21 +576,33 @@ struct Plan {
 // 81; 128256 x 2048 47 and 48; 30001 x 6144 34 and 36).
 // More: the largest tile that about fills the CUs and leaves less than half its
 // tokens empty (4096 x 10240 x 2560: 119 us with 256 rows x 128 tokens, 146 with
-// 256 x 64, 251 with 128 x 32; 512 x 4096 x 4096, 64, 128 and 512 tiles: 36, 24
-// and 22).  Where even the smallest leaves CUs idle, waves share k (32 x 4096 x
-// 4096 18.4 and 8.1 us, 128 x 4096 x 4096 18.6 and 12.7; with 224 tiles the
-// smallest is the better one, 23.5 and 33.8 for 32 x 28672 x 4096).
+// 256 x 64, 251 with 128 x 32).  Where that is none, tiles of 128 x 32 while k is
+// short, else groups that share a tile's k, so that larger tiles still keep a CU's
+// eight waves (tiles of 128 x 32, the same in two groups, 128 x 64 in two, 64 x 32
+// in four; 512 x 4096 x 8192 43.6, 42.6, 36.3 and 52 us; 512 x 4096 x 2048 12.4,
+// 13.1, 12.6 and 18; 256 x 4096 x 8192 39.6, 27.4, 35.1 and 30.8; 128 x 4096 x 8192
+// 38, 26.5, 34.8 and 20.0).  Fewer tiles still: waves sharing k on 32 rows (128 x
+// 4096 x 2048 8.0, 64 x 32 in four groups 8.0; 64 x 4096 x 4096 9.2 and 11.1) or on
+// 16 (64 x 1000 x 8192 11.3, on 32 14.5; 32 x 6000 x 4096 12.9 and 10.9; 17 x 8192
+// x 8192, little of whose second 16 tokens is read, 20.1 and 24.1).
 Plan plan_of(int64_t n, int64_t k, int64_t B) {
   constexpr int kFull = 180;  // workgroups that about fill the 256 CUs
+  const int64_t tiles = (n + 15) / 16, steps = w_steps(k);
   if (B <= 16) {
-    const int64_t tiles = (n + 15) / 16, steps = w_steps(k);
     if (tiles < 512 || (B <= 4 && steps >= 44)) return Plan{kFew16Rows8, 16, 16};
     if (tiles < 2048 || (B <= 4 && steps >= 24)) return Plan{kFew16Rows4, 16, 16};
     return B <= 4 ? Plan{kFew16Rows2, 32, 16} : Plan{k16, 128, 16};
   }
-  for (const Plan& p : {Plan{k128, 256, 128}, Plan{k64, 256, 64}, Plan{k32, 128, 32}})
+  for (const Plan& p : {Plan{k128, 256, 128}, Plan{k64, 256, 64}})
     if (2 * B > p.tokens && p.tiles(n, B) >= kFull) return p;
-  return B <= 32 ? Plan{kTokens32Rows8, 16, 32} : Plan{kTokens32Rows4, 32, 32};
+  const Plan p{k32, 128, 32};
+  const int64_t t = p.tiles(n, B);
+  if (t >= 2 * kFull) return steps >= 48 && B > 32 ? Plan{k64x2, 128, 64} : p;
+  if (t >= 150 && t <= 256 && steps >= 24) return Plan{k32x2, 128, 32};
+  if (t >= kFull) return p;
+  if (t >= 100 && steps >= 64) return Plan{k32x4, 64, 32};
+  const bool narrow = B <= 24 || (t < 40 && (B <= 32 || steps >= 64));
+  return narrow ? Plan{kTokens32Rows8, 16, 32} : Plan{kTokens32Rows4, 32, 32};
 }
 
 // Whether W passes the caches by: its rows are read by one workgroup alone, and
@@ -588,12 +627,12 @@ void launch_few(const W8A8Args& a, hipStream_t st) {
   hipLaunchKernelGGL((k_w8a8_few<FT, FN, KW, G, PAST, BF16, HEAD>), grid, dim3(64 * KW * G), 0, st, a);
 }
 
-template <int FT, int FN, int WN, bool PAST, bool BF16, bool HEAD>
+template <int FT, int FN, int WN, int KW, bool PAST, bool BF16, bool HEAD>
 void launch_tile(const W8A8Args& a, hipStream_t st) {
   constexpr int kRows = 16 * FN * WN, kTokens = 16 * FT;
   const int nt = (int)((a.n + kRows - 1) / kRows), qt = (a.B + kTokens - 1) / kTokens;
   const dim3 grid((unsigned)(((int64_t)nt * qt + 7) / 8 * 8));
-  hipLaunchKernelGGL((k_w8a8_tile<FT, FN, WN, PAST, BF16, HEAD>), grid, dim3(64 * WN), 0, st, a, nt, qt);
+  hipLaunchKernelGGL((k_w8a8_tile<FT, FN, WN, KW, PAST, BF16, HEAD>), grid, dim3(64 * WN * KW), 0, st, a, nt, qt);
 }
 
 template <bool PAST, bool BF16, bool HEAD>
@@ -603,12 +642,14 @@ void launch_kind(const W8A8Args& a, Kind kind, hipStream_t st) {
     case kFew16Rows4: return launch_few<1, 1, 4, 1, PAST, BF16, HEAD>(a, st);
     case kFew16Rows2: return launch_few<1, 1, 2, 2, PAST, BF16, HEAD>(a, st);
     case kTokens32Rows8: return launch_few<2, 1, 8, 1, PAST, BF16, HEAD>(a, st);
-    // more than 32 tokens: two tiles of them or more share W
-    case kTokens32Rows4: return launch_few<2, 2, 4, 1, false, BF16, HEAD>(a, st);
-    case k16: return launch_tile<1, 2, 4, PAST, BF16, HEAD>(a, st);
-    case k32: return launch_tile<2, 2, 4, PAST, BF16, HEAD>(a, st);
-    case k64: return launch_tile<4, 2, 8, PAST, BF16, HEAD>(a, st);
-    case k128: return launch_tile<8, 2, 8, PAST, BF16, HEAD>(a, st);
+    case kTokens32Rows4: return launch_few<2, 2, 4, 1, PAST, BF16, HEAD>(a, st);
+    case k16: return launch_tile<1, 2, 4, 1, PAST, BF16, HEAD>(a, st);
+    case k32: return launch_tile<2, 2, 4, 1, PAST, BF16, HEAD>(a, st);
+    case k32x2: return launch_tile<2, 2, 4, 2, PAST, BF16, HEAD>(a, st);
+    case k32x4: return launch_tile<2, 2, 2, 4, PAST, BF16, HEAD>(a, st);
+    case k64: return launch_tile<4, 2, 8, 1, PAST, BF16, HEAD>(a, st);
+    case k64x2: return launch_tile<4, 2, 4, 2, PAST, BF16, HEAD>(a, st);
+    case k128: return launch_tile<8, 2, 8, 1, PAST, BF16, HEAD>(a, st);
   }
 }
 

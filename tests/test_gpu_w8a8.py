@@ -44,7 +44,7 @@ SIZES = [(1, 1, 1), (1, 16, 64), (3, 17, 65), (5, 130, 16), (16, 128, 128), (17,
          (3, 9001, 70), (16, 8200, 448), (7, 32785, 48), (16, 33000, 320), (20, 25001, 320), (32, 24600, 448),
          (40, 32801, 320), (64, 33000, 448), (100, 65601, 320), (128, 65600, 192), (300, 32801, 320),
          (257, 33001, 448), (200, 4000, 320), (129, 70001, 130), (2, 33001, 320), (3, 33000, 1600),
-         (1, 9001, 2900), (9, 32770, 130)]
+         (1, 9001, 2900), (9, 32770, 130), (100, 6000, 1600), (128, 3200, 4200), (200, 7000, 3100), (30, 6001, 100)]
 
 
 @pytest.mark.parametrize("B,n,k", SIZES)
@@ -150,7 +150,8 @@ def test_non_finite_weights_are_refused():
 @pytest.mark.parametrize("B,n,k", [(1, 1, 16), (1, 5000, 2048), (3, 1000, 100), (16, 4099, 128), (33, 700, 1152),
                                    (64, 3000, 256), (130, 1111, 192), (300, 640, 64),
                                    (3, 9001, 70), (7, 32785, 48), (20, 25001, 80), (40, 32801, 64), (100, 65601, 64),
-                                   (300, 33001, 64), (200, 4000, 320)])
+                                   (300, 33001, 64), (200, 4000, 320), (9, 32770, 130), (100, 6000, 1600),
+                                   (128, 3200, 4200), (200, 7000, 3100)])
 @pytest.mark.parametrize("mode,T", [(0, 1.0), (2, 0.7)])
 def test_head(B, n, k, mode, T):
     from lm_output_head_amd import W8A8Head
@@ -215,10 +216,11 @@ def test_more_than_one_launch_holds_is_refused():
     assert got["token"].tolist() == [0, 0, 0] and got["token_logit"].tolist() == [1.0] * 3
 
 
-# weights that pass the caches by: of more than 64 MB (up to 16 or 32 tokens) and
-# of more than 256 MB, each way of cutting them up
+# weights that pass the caches by, of more than 64, 128 or 256 MB, each way of
+# cutting them up
 @pytest.mark.parametrize("n,k,Bs", [(70001, 1000, (1, 4)), (45001, 1600, (2,)), (24001, 2900, (3,)), (5001, 14000, (16,)),
-                                    (20001, 3500, (5,)), (16001, 4400, (20,)), (240001, 1152, (1, 16, 17, 40, 100, 130))])
+                                    (20001, 3500, (5,)), (12001, 5700, (20, 30)), (19300, 7100, (32,)),
+                                    (16001, 8500, (20,)), (25001, 10800, (50,)), (240001, 1152, (1, 16, 17, 40, 100, 130))])
 def test_large_weights_are_as_their_slices(n, k, Bs):
     """Exact sums and one formula: rows 0 .. 999 and the last 1000 as a weight of
     their own, cut up another way, give the same bits."""
