@@ -171,3 +171,41 @@ def test_millions_of_rows(dt, d):
         b = rmsnorm(x[lo:lo + 700], want_q=True)
         for k in b:
             assert torch.all((a[k][lo:lo + 700].double() - b[k].double()).abs() <= (1 if k == "q" else 2.0 ** -7) * b[k].double().abs().clamp(min=1))
+
+
+def quotients(y, scale):
+    """rint(y / scale) within [-127, 127] in float32, 0 where the scale is 0:
+    numpy's float32 division is correctly rounded, subnormal values included."""
+    y, scale = y.cpu().numpy(), scale.cpu().numpy()[:, None]
+    with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
+        return np.where(scale > 0, np.clip(np.rint(y / scale), -127, 127), 0).astype(np.int8)
+
+
+@pytest.mark.parametrize("B,d", [(60000, 96), (4096, 1153), (3000, 2560), (900, 9000), (150, 40000)])
+def test_codes_are_the_rounded_quotients(B, d):
+    """out_q = rint(y / out_scale), one division in float32, for every code: a
+    float32 `out` is y itself.  A product with 127 / max |y| differs from it next
+    to halves, in about one of a million codes."""
+    from lm_output_head_amd import rmsnorm
+    g = torch.Generator(device="cuda").manual_seed(d)
+    x = torch.randn(B, d, generator=g, device="cuda") * 3
+    w = torch.randn(d, generator=g, device="cuda")
+    say("norm codes", B, d)
+    got = rmsnorm(x, w, want_q=True)
+    assert np.array_equal(got["q"].cpu().numpy(), quotients(got["out"], got["q_scale"]))
+
+
+@pytest.mark.parametrize("d", [96, 2560, 40000])
+@pytest.mark.parametrize("m", [1, 9, 30, 64, 200, 5000, 3 << 20])
+def test_codes_of_rows_near_zero(d, m):
+    """max |y| down to the smallest subnormal: a scale of 0 has codes 0, a
+    subnormal scale (one significant bit and up) those of its own quotients."""
+    from lm_output_head_amd import rmsnorm
+    g = torch.Generator().manual_seed(d + m)
+    x = torch.randn(5, d, generator=g).cuda()
+    w = torch.full((d,), m * 2.0 ** -149, dtype=torch.float64).float().cuda()
+    say("norm codes near zero", d, m)
+    got = rmsnorm(x, w, want_q=True)
+    top = got["out"].abs().amax(1).cpu().numpy()
+    assert np.array_equal(got["q_scale"].cpu().numpy(), top / np.float32(127))
+    assert np.array_equal(got["q"].cpu().numpy(), quotients(got["out"], got["q_scale"]))
