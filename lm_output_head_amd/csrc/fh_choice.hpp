@@ -2,9 +2,9 @@
 // with nothing left: Part folds and merges that keep their meaning there.
 //
 // A Part holds the best (key, id) with its logit z, and (m, s) with m = max x,
-// s = sum exp(x - m), x = z / T'.  exp_from(x, m) is 1 where x = m, so m = +inf
-// counts its own terms (s >= 1, LSE +inf) and a row of -inf alone has
-// m = -inf (LSE -inf, whatever s); a NaN x leaves m and makes s NaN (LSE NaN).
+// s = sum exp(x - m), x = z / T'.  A row of -inf alone has m = -inf (LSE -inf,
+// whatever s), one with +inf m = s = +inf (LSE +inf); exp_from(x, m) is 1 where
+// x = m, so merges keep both.  A NaN x leaves m and makes s NaN (LSE NaN).
 // A NaN key compares false and is never taken; a best key of -inf means that
 // nothing is left.
 #pragma once
@@ -78,6 +78,10 @@ __device__ __forceinline__ float exponential_from_word(uint32_t w) {
 // one logarithm more per logit and no division (e l' > e' l); the key itself is
 // formed for the winner alone, to be compared between lanes.  ORDERED: the ids
 // ascend, so a tie stays with the earlier one; else the ids are compared.
+//
+// The exponent's shift is m within the finite values: beside x = +inf every finite
+// e is then at most 1 and the infinite e wins the race (a shift of 0 would let any
+// x above 88 overflow to the same +inf); m = -inf leaves e = 0.
 template <int N, bool ORDERED>
 __device__ __forceinline__ Part choose(const float (&z)[N], const int32_t (&id)[N], bool sample, float inverse,
                                        const uint32_t (&word)[N]) {
@@ -89,7 +93,7 @@ __device__ __forceinline__ Part choose(const float (&z)[N], const int32_t (&id)[
       x[i] = scaled_logit(z[i], inverse);
       p.m = fmaxf(p.m, x[i]);
     }
-    const float shift = fabsf(p.m) < INFINITY ? p.m : 0.f;  // exp of +-inf is what it has to be
+    const float shift = __builtin_amdgcn_fmed3f(p.m, -FLT_MAX, FLT_MAX);
     float be = 0.f, bl = 1.f;
     uint32_t bw = 0u;
 #pragma unroll
@@ -116,7 +120,7 @@ __device__ __forceinline__ Part choose(const float (&z)[N], const int32_t (&id)[
     }
     p.z = p.key;
     p.m = p.key;  // -inf or the largest; a NaN is neither
-    const float shift = fabsf(p.m) < INFINITY ? p.m : 0.f;
+    const float shift = __builtin_amdgcn_fmed3f(p.m, -FLT_MAX, FLT_MAX);
 #pragma unroll
     for (int i = 0; i < N; ++i) p.s += __expf(z[i] - shift);
   }

@@ -231,3 +231,53 @@ def test_same_choice_as_the_dense_head():
         assert torch.equal(a["token"], d["token"]) and torch.equal(a["token_logit"], d["token_logit"])
         assert torch.allclose(a["lse"], d["lse"], rtol=1e-5, atol=1e-6)
     head.close()
+
+
+def smallest_infinite(z, ids):
+    t = np.broadcast_to(np.arange(z.shape[1]), z.shape) if ids is None else ids
+    return np.where(np.isposinf(z), t, np.iinfo(np.int32).max).min(1)
+
+
+@pytest.mark.parametrize("B,n,listed", [(40, 300, False), (40, 3001, False), (40, 6000, False), (40, 20000, False),
+                                        (520, 3001, False), (130, 33000, False), (40, 300, True), (40, 900, True),
+                                        (40, 3000, True), (40, 9000, True), (130, 9000, True)])
+def test_infinite_logits_are_drawn_before_large_ones(B, n, listed):
+    """Every finite z / T is past exp's range (100 and more): +inf, one or
+    several, is drawn all the same, the smallest token of them."""
+    from lm_output_head_amd import logits_apply
+    rng = np.random.default_rng(n + B)
+    v = n + 1000 if listed else n
+    ids = np.stack([rng.permutation(v)[:n] for _ in range(B)]).astype(np.int32) if listed else None
+    z = rng.uniform(5, 30, (B, n)).astype(np.float32)
+    for b in range(B):
+        z[b, rng.integers(0, n, 1 + b % 3)] = np.inf
+        if b % 4 == 1:  # neighbours of one thread's run
+            i = int(rng.integers(0, n - 1))
+            z[b, i:i + 2] = np.inf
+    z[5, np.flatnonzero(np.isfinite(z[5]))[::7]] = np.nan
+    z[6, np.flatnonzero(np.isfinite(z[6]))[::2]] = np.finfo(np.float32).max
+    say("infinite logits", B, n, listed)
+    gpu = None if ids is None else torch.from_numpy(ids).cuda()
+    for mode, T in ((0, 1.0), (2, 0.05), (2, 0.001), (2, 1.0)):
+        out = host(logits_apply(torch.from_numpy(z).cuda(), ids=gpu, v=v, mode=mode, temperature=T, seed=8))
+        assert np.array_equal(out["token"], smallest_infinite(z, ids)), (mode, T)
+        assert np.all(np.isposinf(out["token_logit"]))
+        lse = np.full(B, np.inf)
+        lse[5] = np.nan
+        assert np.array_equal(out["lse"], lse, equal_nan=True)
+
+
+@pytest.mark.parametrize("listed", [False, True])
+def test_a_bias_of_infinity_forces_its_token(listed):
+    from lm_output_head_amd import logits_apply
+    rng = np.random.default_rng(4)
+    B, n = 64, 5000
+    z = rng.uniform(2, 30, (B, n)).astype(np.float32)
+    ids = np.stack([rng.permutation(n) for _ in range(B)]).astype(np.int32) if listed else None
+    r = {"bias_ids": rng.integers(0, n, (B, 9)).astype(np.int32), "bias": np.ones((B, 9), np.float32)}
+    r["bias"][:, 4] = np.inf
+    say("bias of infinity", listed)
+    for T in (0.02, 0.25):
+        out = host(logits_apply(torch.from_numpy(z).cuda(), on_gpu(n, r), v=n, mode=2, temperature=T, seed=1,
+                                ids=None if ids is None else torch.from_numpy(ids).cuda()))
+        assert np.array_equal(out["token"], r["bias_ids"][:, 4])

@@ -243,3 +243,23 @@ def test_large_weights_are_as_their_slices(n, k, Bs):
         top = z.amax(1)
         first = torch.where(z == top[:, None], torch.arange(n, device="cuda"), n).amin(1)  # ties: the smaller token
         assert torch.equal(out["token"].long(), first) and torch.equal(out["token_logit"], top)
+
+
+def test_infinite_logits_are_drawn_before_large_ones():
+    """A channel whose scale overflows the product: its +inf is drawn though
+    every other z / T is past exp's range, the smallest token of several."""
+    from lm_output_head_amd import W8A8Head
+    n, k = 3000, 64
+    w = torch.ones(n, k, dtype=torch.int8, device="cuda")
+    for first, more in ((9, (11, 40, 2000)), (1502, ()), (2999, ()), (130, (131,))):
+        scales = torch.ones(n, device="cuda")
+        scales[[first, *more]] = 3e38
+        head = W8A8Head(codes=w, scales=scales)
+        for B in (1, 5, 40, 130):
+            q, qs = torch.ones(B, k, dtype=torch.int8, device="cuda"), torch.full((B,), 2.0, device="cuda")
+            say("int8 head, infinite logits", first, B)
+            for mode, T in ((0, 1.0), (2, 0.5)):
+                out = head.forward(q, qs, mode=mode, temperature=T, seed=6)
+                assert out["token"].tolist() == [first] * B and torch.all(out["token_logit"] == float("inf"))
+                assert torch.all(out["lse"] == float("inf"))
+        head.close()
