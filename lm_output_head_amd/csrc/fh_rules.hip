@@ -5,7 +5,7 @@
 // A workgroup owns one tile of one row and keeps a table of its tokens in LDS: a
 // word with the token's count in the output and, in bit 31, whether it is in the
 // prompt.  The tile's logits travel to registers while the workgroup walks the
-// row's whole history and adds what falls into its tile; biases are added in a
+// row's whole history and adds what falls into its tile; biases are added up in a
 // second turn of the table.  Dense rows index the table by token; rows of listed
 // candidates through a hash of their ids.  Counts are integer sums, and one
 // thread adds all biases of a token in the list's order, so results do not
@@ -50,7 +50,7 @@ __device__ __forceinline__ void load_run(const T* p, int i, int n, T other, T (&
   for (int e = 0; e < W; ++e) v[e] = ALL || i + e < n ? p[i + e] : other;
 }
 
-// DENSE: a word per token of the tile, its count and later its logit.  Else a
+// DENSE: a word per token of the tile, its count and later its bias.  Else a
 // hash of twice the tile's size, so that at most half of its slots are taken and
 // every search ends, behind a bitmap of the ids' low bits that turns most of the
 // history away at its first read.
@@ -58,7 +58,7 @@ template <bool DENSE, int TILE, int TH>
 struct Tables {
   static constexpr int kSize = DENSE ? TILE : 2 * TILE;
   static constexpr int kBits = TILE > 4096 ? 65536 : 32768;
-  alignas(16) uint32_t count[kSize];  // then the sums of the biases, or the logits of dense rows
+  alignas(16) uint32_t count[kSize];  // then the sums of the biases
   alignas(16) int32_t key[DENSE ? 4 : kSize];
   alignas(16) uint32_t maybe[DENSE ? 4 : kBits / 32];
   // a list's entries that fall into the tile, by wave, in order
@@ -266,21 +266,16 @@ __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(TH == 1024 ?
     }
   }
   if (a.bias_ids) {
-    // dense rows: the logits themselves in the table, each to its own thread's
-    // words, which only that thread has read above; else the counts make room
+    // the counts make room for the sums, -0 at first, which adds nothing to any
+    // logit; a dense row's words have been read by their own thread alone
     float* sums = reinterpret_cast<float*>(sh.count);
-    if constexpr (DENSE) {
+    if (!DENSE && a.history) __syncthreads();
 #pragma unroll
-      for (int i = 0; i < N; ++i) sums[place[i]] = z[i];
-    } else if (a.history) {
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (open[i]) sums[place[i]] = 0.f;
-    }
+    for (int i = 0; i < N; ++i)
+      if (DENSE || open[i]) sums[place[i]] = -0.f;
     for (int i0 = 0; i0 < nb; i0 += TH) {
       if (i0 > 0) load_bias(i0 + tid);
-      __syncthreads();  // the logits are there, the list before is done with
+      __syncthreads();  // the sums are there, the list before is done with
       const int mine = i0 + tid < nb && sh.may_hold(bias_id, base, width, v) ? sh.find(bias_id, base) : -1;
       const uint64_t in = __ballot(mine >= 0);
       const int at = 64 * wave + __popcll(in & ((1ull << lane) - 1));
@@ -291,8 +286,9 @@ __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(TH == 1024 ?
       if (lane == 0) sh.listed[wave] = __popcll(in);
       __syncthreads();
       if (mine >= 0) {
-        // the first entry of a place adds up the place's entries, in order
-        float sum = 0.f;
+        // the first entry of a place goes on with the place's sum, in order; what
+        // the others read is not used
+        float sum = sums[mine];
         int first = at;
         for (int w = 0; w < TH / 64; ++w) {
           const int m = sh.listed[w];
@@ -302,13 +298,13 @@ __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(TH == 1024 ?
               sum += sh.list_add[e];
             }
         }
-        if (first == at) sums[mine] += sum;
+        if (first == at) sums[mine] = sum;
       }
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (DENSE || open[i]) z[i] = DENSE ? sums[place[i]] : z[i] + sums[place[i]];
+      if (DENSE || open[i]) z[i] += sums[place[i]];
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {

@@ -281,3 +281,33 @@ def test_a_bias_of_infinity_forces_its_token(listed):
         out = host(logits_apply(torch.from_numpy(z).cuda(), on_gpu(n, r), v=n, mode=2, temperature=T, seed=1,
                                 ids=None if ids is None else torch.from_numpy(ids).cuda()))
         assert np.array_equal(out["token"], r["bias_ids"][:, 4])
+
+
+@pytest.mark.parametrize("B,n,listed", [(3, 900, False), (3, 3000, False), (3, 7000, False), (3, 12000, False),
+                                        (300, 12000, False), (600, 2500, False), (3, 400, True), (3, 900, True),
+                                        (3, 3000, True), (2, 9000, True), (130, 9000, True)])
+def test_long_bias_lists_are_summed_in_order(B, n, listed):
+    """The listed biases of a token are added up in float32 in the list's order
+    and their sum to the logit, in one rounding, however long the list and
+    whatever the size of the call."""
+    from lm_output_head_amd import logits_apply
+    rng = np.random.default_rng(n)
+    v, nb = n, 2600
+    z = rng.normal(0, 3, (1, n)).astype(np.float32)
+    ids = rng.permutation(v)[None].astype(np.int32) if listed else None
+    bias_ids = rng.integers(0, v, (1, nb)).astype(np.int32)
+    bias = rng.normal(0, 3, (1, nb)).astype(np.float32)
+    for t, places, adds in ((7, (0, 301, 2599), (1e8, -1e8, 0.5)),
+                            (11, (255, 256, 511, 512, 1023, 1024, 2048), (1e8, 3, -1e8, 1e7, 5, -1e7, 0.25)),
+                            (12, (1, 2, 3), (-3e7, 3e7, 1.5))):
+        bias_ids[0, list(places)] = t
+        bias[0, list(places)] = adds
+    total = np.zeros(v, np.float32)
+    for t, add in zip(bias_ids[0], bias[0]):
+        total[t] = total[t] + add
+    want = z + (total if ids is None else total[ids[0]])
+    say("long bias lists", B, n, listed)
+    r = {"bias_ids": np.repeat(bias_ids, B, 0), "bias": np.repeat(bias, B, 0)}
+    gpu = None if ids is None else torch.from_numpy(np.repeat(ids, B, 0)).cuda()
+    out = host(logits_apply(torch.from_numpy(np.repeat(z, B, 0)).cuda(), on_gpu(v, r), ids=gpu, v=v))
+    assert np.array_equal(out["logits"], np.repeat(want, B, 0))
