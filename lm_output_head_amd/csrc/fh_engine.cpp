@@ -35,6 +35,7 @@ fh_status fail(fh_status st, const std::string& msg) {
 }
 
 fh_status hip_fail(hipError_t e, const char* what) {
+  (void)hipGetLastError();  // reported here: a later launch must not find it
   g_err = std::string(what) + ": " + hipGetErrorString(e);
   return e == hipErrorOutOfMemory ? FH_ENOMEM : FH_EHIP;
 }

@@ -15,7 +15,8 @@ extern thread_local std::string g_err;
 
 // Set the thread's error text; return st.
 fh_status fail(fh_status st, const std::string& msg);
-// The same for a failed HIP call: FH_ENOMEM or FH_EHIP.
+// The same for a failed HIP call, whose error the runtime also keeps until it is
+// read: that one is consumed.  FH_ENOMEM or FH_EHIP.
 fh_status hip_fail(hipError_t e, const char* what);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -24,8 +25,8 @@ struct DeviceGuard {
   int prev = -1;
   bool ok = true;
   explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) != hipSuccess) { ok = false; return; }
-    if (prev != dev && hipSetDevice(dev) != hipSuccess) ok = false;
+    ok = hipGetDevice(&prev) == hipSuccess && (prev == dev || hipSetDevice(dev) == hipSuccess);
+    if (!ok) (void)hipGetLastError();  // the call reports it
   }
   ~DeviceGuard() {
     int cur = -1;

@@ -263,3 +263,30 @@ def test_infinite_logits_are_drawn_before_large_ones():
                 assert out["token"].tolist() == [first] * B and torch.all(out["token_logit"] == float("inf"))
                 assert torch.all(out["lse"] == float("inf"))
         head.close()
+
+
+def test_a_refused_allocation_leaves_no_error_behind():
+    """A weight larger than the card is refused before anything is read; the
+    calls after it do not find its error."""
+    import ctypes
+    from lm_output_head_amd import FlashHeadError, W8A8Head, load_library, logits_apply, rmsnorm
+    from lm_output_head_amd._abi import check
+    lib = load_library()
+    n, k = 1 << 27, 131071  # 1.8e13 bytes
+    assert n * k > 16 * torch.cuda.get_device_properties(0).total_memory
+    codes, scales = torch.ones(4, 64, dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda")
+    x = torch.randn(3, 64, device="cuda")
+    torch.cuda.synchronize()
+    for create, args in ((lib.fh_w8a8_create_codes, (codes.data_ptr(), scales.data_ptr())),
+                         (lib.fh_w8a8_create, (x.data_ptr(), 0))):
+        w = ctypes.c_void_p()
+        say("a weight larger than the card")
+        with pytest.raises(FlashHeadError) as e:
+            check(create(*args, n, k, None, ctypes.byref(w)))
+        assert e.value.status == -2 and not w.value
+        assert lib.hipPeekAtLastError() == 0
+        rmsnorm(x)
+        logits_apply(x)
+        head = W8A8Head(codes=codes, scales=scales)
+        assert head.matmul(codes, scales).shape == (4, 4)
+        head.close()
