@@ -490,10 +490,13 @@ def fh_logits_apply(logits, ids, v, rules, mode, temperature, seed, out_logits=N
 
 def logits_apply(logits, rules=None, *, ids=None, v=None, mode: int = 0, temperature: float = 1.0, seed: int = 0,
                  want_token: bool = True, out=None, stream=None) -> dict:
-    """The rules on logits [B x n] of all tokens, or of the tokens ids [B x n]
+    """The rules on logits [B x n] of all v tokens, or of the tokens ids [B x n]
     (a forward's "logits" and "ids"): "logits" (in `out`, which may be logits
-    itself) and with want_token "token", "token_logit" and "lse"."""
+    itself) and with want_token "token", "token_logit" and "lse".  v is the
+    rules' or, of logits of all tokens, n; ids without rules need it."""
     if v is None:
+        if rules is None and ids is not None:
+            raise ValueError("ids without rules need v, the number of tokens")
         v = rules.v if rules is not None else logits.shape[-1]
     ld_z, ld_ids, struct = _apply_inputs(logits, ids, v, rules)
     dev = _device(logits, ids, out)

@@ -249,6 +249,17 @@ def test_binding_apply_refusals():
             serve.fh_logits_apply(**args)
 
 
+def test_binding_ids_without_rules_need_the_number_of_tokens():
+    """The candidates' number says nothing about the vocabulary: taken for it,
+    every id at or above it would be no token."""
+    z, ids = torch.zeros(2, 8), torch.full((2, 8), 5000, dtype=torch.int32)
+    with pytest.raises(ValueError, match="ids without rules need v"):
+        serve.logits_apply(z, ids=ids)
+    for kw in ({"v": 10000}, {"rules": serve.LogitRules(10000)}):
+        with pytest.raises(ValueError, match="one GPU"):
+            serve.logits_apply(z, ids=ids, **kw)
+
+
 # ------------------------------------------------------------ definitions' pins
 
 def test_oracle_rules_by_hand():
