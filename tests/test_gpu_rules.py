@@ -311,3 +311,15 @@ def test_long_bias_lists_are_summed_in_order(B, n, listed):
     gpu = None if ids is None else torch.from_numpy(np.repeat(ids, B, 0)).cuda()
     out = host(logits_apply(torch.from_numpy(np.repeat(z, B, 0)).cuda(), on_gpu(v, r), ids=gpu, v=v))
     assert np.array_equal(out["logits"], np.repeat(want, B, 0))
+
+
+def test_lists_of_one_row_at_any_stride():
+    """One row's stride says nothing: lists cut from wider ones of different widths."""
+    from lm_output_head_amd import LogitRules, logits_apply
+    z = torch.zeros(1, 50, device="cuda")
+    ids = torch.arange(40, dtype=torch.int32, device="cuda").view(1, 40)
+    r = LogitRules(50, bias_ids=ids[:, 3:6], bias=torch.ones(1, 3, device="cuda"))
+    out = logits_apply(z, r)["logits"]
+    want = torch.zeros(1, 50, device="cuda")
+    want[0, 3:6] = 1
+    assert torch.equal(out, want)

@@ -235,6 +235,14 @@ def test_binding_rules_refusals(kw, needle):
         serve.LogitRules(100, **kw)
 
 
+def test_binding_lists_of_one_row_have_any_stride():
+    """One row's stride says nothing (refused here for its place alone)."""
+    ids = torch.zeros(1, 40, dtype=torch.int32)[:, 3:6]
+    for bias in (torch.ones(1, 3), torch.ones(1, 60)[:, :3]):
+        with pytest.raises(ValueError, match="one GPU"):
+            serve.LogitRules(50, bias_ids=ids, bias=bias)
+
+
 def test_binding_apply_refusals():
     z = torch.zeros(2, 100)
     none = serve.LogitRules(100)
