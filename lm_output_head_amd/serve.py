@@ -193,7 +193,11 @@ def fh_w8a8_create_codes(codes: torch.Tensor, scales: torch.Tensor, stream=None)
 
 
 def fh_w8a8_destroy(w) -> None:
-    _WEIGHTS.pop(_key(w), None)
+    """Release the weight (None is a no-op); a second time is refused."""
+    if _key(w) is None:
+        return
+    if _WEIGHTS.pop(_key(w), None) is None:
+        raise ValueError("unknown int8 weight (not created by fh_w8a8_create, or destroyed)")
     _abi.load().fh_w8a8_destroy(w)
 
 
@@ -306,9 +310,8 @@ class W8A8Head:
         self.n, self.k, self.device = _weight(self.w)
 
     def close(self):
-        if self.w is not None:
-            fh_w8a8_destroy(self.w)
-            self.w = None
+        w, self.w = self.w, None
+        fh_w8a8_destroy(w)
 
     def __del__(self):
         # not while the interpreter shuts down (see FlashHead)

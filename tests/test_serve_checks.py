@@ -215,6 +215,30 @@ def test_binding_product_refusals(weight):
         serve.W8A8Head(codes=q, scales=s)
 
 
+def test_binding_destroys_a_weight_once(monkeypatch):
+    """A handle is freed memory after its release: another one is refused
+    before the library sees it, through the function or a head that holds it."""
+    freed = []
+
+    class Library:
+        def fh_w8a8_destroy(self, w):
+            freed.append(w)
+
+    monkeypatch.setattr(_abi, "load", Library)
+    serve._WEIGHTS[0x5EED] = (12, 16, torch.device("cpu"))
+    head = object.__new__(serve.W8A8Head)
+    head.w = 0x5EED
+    serve.fh_w8a8_destroy(0x5EED)
+    with pytest.raises(ValueError, match="unknown int8 weight"):
+        serve.fh_w8a8_destroy(0x5EED)
+    with pytest.raises(ValueError, match="unknown int8 weight"):
+        head.close()
+    head.close()  # holds nothing any more
+    serve.fh_w8a8_destroy(None)
+    serve.fh_w8a8_destroy(ctypes.c_void_p())
+    assert freed == [0x5EED]
+
+
 @pytest.mark.parametrize("kw,needle", [
     ({"history": torch.zeros(2, 5)}, "history: expected"),
     ({"history": torch.zeros(5, dtype=torch.int32)}, "history must be"),
