@@ -204,7 +204,7 @@ def stream_bandwidth(sizes, nbuf=16, steps=100):
 CLUSTER_SOURCES = ("fh_cluster.hip",)  # the offline clustering, its own translation unit
 # the operators around the dense head: no code of theirs runs in a head call
 SERVE_SOURCES = ("fh_norm.hip", "fh_w8a8.hip", "fh_rules.hip", "fh_serve.cpp", "fh_serve.hpp",
-                 "fh_choice.hpp", "fh_host.hpp")
+                 "fh_choice.hpp")
 
 
 def kernel_source_hash(cluster: bool = False) -> str:
