@@ -209,3 +209,40 @@ def test_codes_of_rows_near_zero(d, m):
     top = got["out"].abs().amax(1).cpu().numpy()
     assert np.array_equal(got["q_scale"].cpu().numpy(), top / np.float32(127))
     assert np.array_equal(got["q"].cpu().numpy(), quotients(got["out"], got["q_scale"]))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [5, 600])
+def test_each_of_millions_of_rows(dt, d):
+    """Every row of a large call is what the same lanes give it in a call of
+    4096 rows, bit for bit."""
+    from lm_output_head_amd import rmsnorm
+    B, part = (1 << 22) + 3, 4096
+    g = torch.Generator(device="cuda").manual_seed(d)
+    x = torch.randn(part, d, generator=g, device="cuda").to(dt)
+    say("each of millions of rows", dt, d)
+    a = rmsnorm(x.repeat(B // part + 1, 1)[:B], want_q=True)
+    b = rmsnorm(x, want_q=True)
+    check(x, None, None, 1e-6, 0.0, b)
+    for k in b:
+        whole = B // part * part
+        assert torch.all(a[k][:whole].reshape(B // part, *b[k].shape) == b[k]), k
+        assert torch.equal(a[k][whole:], b[k][:B - whole]), k
+
+
+def test_rows_past_one_launch_of_the_long_kernel():
+    """2^29 + 5 rows of 3: eight lanes a row would be 2^32 threads, so
+    workgroups walk over rows, some 512 each.  A row this short is one lane's
+    sum either way, so slices through the eight-lane kernel give the same bits."""
+    from lm_output_head_amd import rmsnorm
+    B, d, part = (1 << 29) + 5, 3, 1 << 26
+    g = torch.Generator(device="cuda").manual_seed(29)
+    x = torch.randn(B, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.tensor([0.5, -1.25, 2.0], device="cuda").bfloat16()
+    say("norm of 2^29 + 5 rows")
+    a = rmsnorm(x, w, want_q=True)
+    for lo in range(0, B, part):
+        b = rmsnorm(x[lo:lo + part], w, want_q=True)
+        for k in b:
+            assert torch.equal(a[k][lo:lo + part], b[k]), (k, lo)
+    check(x[-2000:], None, w, 1e-6, 0.0, {k: t[-2000:] for k, t in a.items()})
