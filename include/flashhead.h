@@ -440,7 +440,8 @@ fh_status fh_cluster(const void* E, fh_dtype dtype, int64_t v, int64_t d, int64_
  * The norm and the codes are taken from the unrounded s and y.  A row that
  * holds an infinity or NaN, or whose sum of squares exceeds float32, has an
  * out_scale or out that says so (NaN, or 0 from the infinite norm) and codes
- * that mean nothing; so does a row of zeros with eps = 0.
+ * that mean nothing; so does a row of zeros with eps = 0, and without eps a row
+ * whose mean square is below float32's normal range (2^-126) loses precision.
  *   x             device [B x d] of dtype, row stride ld_x >= d.
  *   residual      the same, row stride ld_residual; NULL: s = x.
  *   weight        device [d] of dtype; NULL: the factor is 1.

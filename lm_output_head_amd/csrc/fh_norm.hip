@@ -2,9 +2,9 @@
 // with a scale per row: s = x + residual, y = s / sqrt(mean(s^2) + eps) *
 // (offset + weight), q = rint(y / (max |y| / 127)), all in float32 with one
 // rounding per output.  Bound by the bytes of its rows: 16384 x 2560 bfloat16
-// with a residual, the sum and the codes in 70.5 us, 5.36 TB/s (a copy reaches 4.80;
-// 266 us when each pass read the row again).  One row of 2048 takes 2.9 us: a
-// load, two reductions and a store on end.
+// with a residual and every output (378 MB) in 74.5 us, 5.07 TB/s (a copy reaches
+// 4.8 to 4.9; 266 us when each pass read the row again).  One row of 2048 takes
+// 3.2 us: a load, two reductions and a store on end.
 
 #include <hip/hip_runtime.h>
 
@@ -310,11 +310,13 @@ bool launch_w(const NormArgs& a, int64_t B, hipStream_t st) {
   }
 }
 
-// Lanes and waves per row, by its chunks of 16 bytes (us, bfloat16 with a residual
-// and all outputs): the fewest that keep a lane's chunks to one or two, more where
-// rows are few (64 x 2560: 4.9 with 8 waves, 5.6 with 4, 7.4 with 1; 16384 x 2560:
-// 81.7, 75.1 and 83.2; 16384 x 4096 106, 112 and 143; 4096 x 16384 115 with 16
-// waves, 123 with 8, 167 with 4; 16384 x 1152 35 with one wave, 43 with 4).
+// Lanes and waves per row, by its chunks of 16 bytes (us a launch, bfloat16 with a
+// residual and all outputs, three sets of buffers in turn): the fewest that keep a
+// lane's chunks to one or two, more where rows are few (64 x 2560: 4.5 with 8
+// waves, 5.5 with 4 or 16; 16384 x 2560: 85.7 with 4, 88.8 with 8; 16384 x 4096 110
+// with 8, 111 with 4; 4096 x 16384 116 with 16, and 7 and 45% longer with the four
+// or eight chunks that 8 or 4 waves would hold; 16384 x 1152 41 with one wave, 48
+// with 4).
 template <typename T>
 void launch(const NormArgs& a, int64_t B, hipStream_t st) {
   const int64_t chunks = (a.d + Elems<T>::N - 1) / Elems<T>::N;

@@ -11,10 +11,13 @@
 // thread adds all biases of a token in the list's order, so results do not
 // depend on the order of execution.
 //
-// Many rows are bound by the logits' bytes: 64 rows of 151936 take 30 us (with
-// the choice's second launch), 128 rows 47, so 64 more cost 16.5 us, 4.7 TB/s,
-// a copy's rate.  Few rows are bound by latency: the chain of history, table and
-// reductions, 6 us at 1 x 128256 with 1000 of history.
+// us of the GPU's time, sampled, 8192 of history unless said: 64 rows of 151936 with
+// masks and 64 biases take 27.1 us and 3.4 more with the choice's launch.  Without
+// masks and biases it is 26.6 in all, and 42.4 for 128 rows: 64 rows more cost 15.8
+// us, 4.9 TB/s, a copy's rate, but the first 64 go through load, history, choice
+// and draw together, so that their stream and their arithmetic overlap little.
+// Few rows are bound by latency: the chain of history, table and reductions, 7 us
+// in two launches at 1 x 128256, greedy, with 1000 of history.
 
 #include <hip/hip_runtime.h>
 
@@ -362,14 +365,14 @@ struct Shape {
   void (*kernel)(RulesArgs);
 };
 
-// Dense rows (us of the GPU's time, sampled, 1000 or 2000 tokens of history).
-// One tile up to 8192 tokens (64 x 4000: 8.9 with one of 1024 threads, 9.7 with
-// four of 256; 1024 threads hold few rows of a CU, so many rows take 256; 256 x
-// 6000: 12.5 with 8192 to a tile, 14.2 with 1024, 1 x 6000 10.9 and 8.7, but 12.2
-// and 15.4 with the host's).  Beyond, small tiles spread few rows over the CUs,
-// large ones walk the history less often; the large one where it leaves two
-// workgroups per CU (64 x 151936: 26.3 with tiles of 4096, 32.4 with 1024, 27.1
-// with 8192, 37.8 with 16384; 1 x 151936: 11.2, 8.5, 12.1 and 14.8).
+// Dense rows (us of the GPU's time with the choice's launch, sampled, a mask, 1000
+// tokens of history, 2000 at 151936).  One tile up to 8192 tokens (64 x 4000: 6.7
+// with one of 1024 threads, 8.7 with four of 256; 1024 threads hold few rows of a
+// CU, so many rows take 256; 256 x 6000: 9.6 with 8192 to a tile, 11.6 with 1024, 1
+// x 6000 8.7 and 7.8, but a launch less for the host).  Beyond, small tiles spread
+// few rows over the CUs, large ones walk the history less often; the large one
+// where it leaves two workgroups per CU (64 x 151936: 26.6 with tiles of 4096, 32.8
+// with 1024, 26.6 with 8192, 35.0 with 16384; 1 x 151936: 10.4, 7.9, 11.5 and 13.4).
 Shape dense_shape(int64_t B, int64_t n) {
   const Shape small{1024, 256, k_rules<true, 256, 4, 1>}, large{4096, 256, k_rules<true, 256, 4, 4>};
   if (n <= 1024) return small;
@@ -379,11 +382,12 @@ Shape dense_shape(int64_t B, int64_t n) {
 }
 
 // Listed tokens: each tile searches for the whole history, so a tile has a thread
-// per token or few, and a CU at most one tile where that can be (1000 of history:
-// 8 x 8192 12.1 with tiles of 512, 15.0 with 4096; 64 x 8192 20.1 with 512, 17.4
-// with 2048, 23.7 with 8192; 256 x 8192 47.0 with 512, 47.9 with 2048, 27.3 with
-// 8192).  Up to 4096 tokens one tile (64 x 1000 9.7, 12.0 in two; 64 x 3000 14.0,
-// as in six; 1 x 4096 14.6, 11.1 in eight, but 14.5 and 16.3 with the host's).
+// per token or few, and a CU at most one tile where that can be (as above, 1000 of
+// history: 8 x 8192 11.8 with tiles of 512, 17.4 with 4096; 64 x 8192 18.2 with
+// 512, 15.8 with 2048, 19.4 with 8192; 256 x 8192 45.5 with 512, 42.5 with 2048,
+// 21.0 with 8192).  Up to 4096 tokens one tile (64 x 1000 8.2, 11.9 in two; 64 x
+// 3000 11.9, 13.1 in six; 1 x 4096 12.0, 10.5 in eight, but a launch less for the
+// host).
 Shape list_shape(int64_t B, int64_t n) {
   const Shape shapes[] = {{512, 512, k_rules<false, 512, 1, 1>},
                           {1024, 512, k_rules<false, 512, 1, 2>},

@@ -9,8 +9,9 @@
 //
 // Few tokens are bound by the bytes of W: 1 x 128256 x 2048 in 37.8 us, 6.97 TB/s
 // (a read through the caches reaches 6.3); 64 x 151936 x 2560 with float results in 84 us,
-// 5.1 TB/s.  Many by the matrix cores: 4096 x 10240 x 2560 in 114 to 119 us, 1.8
-// to 1.9 POP/s, where the library's product reaches 2.1 at 8192^3.
+// 5.1 TB/s.  Many by how well the matrix cores are fed: 4096 x 10240 x 2560 in 114
+// to 120 us, 1.8 to 1.9 POP/s (the library's product reaches 2.06 at 8192^3), where
+// they are busy 47% of the cycles, at a clock that falls to 1.8 to 1.9 GHz.
 
 #include <hip/hip_runtime.h>
 
@@ -216,9 +217,9 @@ __device__ __forceinline__ void lds_barrier() {
 // the caches by (64 x 151936 x 2560: 87.5 -> 83.8 us).
 //
 // Tiles of eight waves are held to 128 registers, two workgroups per CU: one's
-// results overlap the other's products (head of 128 x 128256 sampled 102 -> 88
-// us; with the 250 registers of a 256 x 256 tile, one per CU, 4096 x 10240 x 2560
-// took 137 us, not 119).
+// results overlap the other's products (a head of 128 x 128256 sampled went from
+// 102 to 88 us by it, and later changes took it to 75; with the 250 registers of a
+// 256 x 256 tile, one per CU, 4096 x 10240 x 2560 took 137 us, not 119).
 //
 // KW groups of WN waves share the tile: each takes a run of the blocks of k, with
 // buffers of its own, and the first adds up the sums.
@@ -567,24 +568,32 @@ struct Plan {
   int64_t token_tiles(int64_t B) const { return (B + tokens - 1) / tokens; }
   int64_t tiles(int64_t n, int64_t B) const { return row_tiles(n) * token_tiles(B); }
 };
-// Up to 4 tokens: waves of some 8 steps of k each (1 token: 128256 x 2048 in 37.8,
-// 40.9 and 40.8 us with 4, 2 and 8 waves, 262144 x 1152 in 46.9, 44.7 and 51, 40000
-// x 4096 in 27.0, 27.9 and 25.9); the fewer rows, the more waves (1000 x 8192 with
-// 8 waves 5.2 us, with 4 7.5).
+// What decides is how many waves have loads in flight: the larger a tile, the
+// seldomer W and the tokens are read again, but a CU wants some eight waves of it,
+// so a call takes the largest shape whose workgroups still reach most CUs (180 of
+// 256 count as most), and where tiles are few the waves come from sharing k, which
+// pays once each has about eight steps of it to cover its start and the joining.
+//
+// us a launch, weights of 400 MB together in turn, so that none is still cached
+// (256 x 4096 x 8192 below takes 24.0 where three are):
+// Up to 4 tokens: waves of some 8 steps of k each (1 token: 128256 x 2048 in 38.2,
+// 41.6 and 41.2 us with 4, 2 and 8 waves, 262144 x 1152 in 43.9, 44.2 and 57.8,
+// 40000 x 4096 in 26.9, 27.6 and 25.6); the fewer rows, the more waves (1000 x 8192
+// with 8 waves 5.3 us, with 4 7.6).
 // Up to 16: a wave reads its tokens once per KB of W, so they are staged in LDS
-// where rows are many (16 tokens, 151936 x 2560: 70 us, with two waves on 32 rows
-// 81; 128256 x 2048 47 and 48; 30001 x 6144 34 and 36).
+// where rows are many (16 tokens, 151936 x 2560: 69.5 us, with two waves on 32 rows
+// 81.1; 128256 x 2048 46.4 and 52.3; 30001 x 6144 32.7 and 39.0).
 // More: the largest tile that about fills the CUs and leaves less than half its
-// tokens empty (4096 x 10240 x 2560: 119 us with 256 rows x 128 tokens, 146 with
-// 256 x 64, 251 with 128 x 32).  Where that is none, tiles of 128 x 32 while k is
+// tokens empty (4096 x 10240 x 2560: 114 us with 256 rows x 128 tokens, 143 with
+// 256 x 64, 245 with 128 x 32).  Where that is none, tiles of 128 x 32 while k is
 // short, else groups that share a tile's k, so that larger tiles still keep a CU's
 // eight waves (tiles of 128 x 32, the same in two groups, 128 x 64 in two, 64 x 32
-// in four; 512 x 4096 x 8192 43.6, 42.6, 36.3 and 52 us; 512 x 4096 x 2048 12.4,
-// 13.1, 12.6 and 18; 256 x 4096 x 8192 39.6, 27.4, 35.1 and 30.8; 128 x 4096 x 8192
-// 38, 26.5, 34.8 and 20.0).  Fewer tiles still: waves sharing k on 32 rows (128 x
-// 4096 x 2048 8.0, 64 x 32 in four groups 8.0; 64 x 4096 x 4096 9.2 and 11.1) or on
-// 16 (64 x 1000 x 8192 11.3, on 32 14.5; 32 x 6000 x 4096 12.9 and 10.9; 17 x 8192
-// x 8192, little of whose second 16 tokens is read, 20.1 and 24.1).
+// in four; 512 x 4096 x 8192 42.8, 42.1, 36.5 and 56.7 us; 512 x 4096 x 2048 12.1,
+// 13.0, 12.5 and 19.2; 256 x 4096 x 8192 38.7, 26.9, 35.4 and 30.8; 128 x 4096 x
+// 8192 37.7, 26.1, 34.8 and 19.8).  Fewer tiles still: waves sharing k on 32 rows
+// (128 x 4096 x 2048 7.9, 64 x 32 in four groups 8.0; 64 x 4096 x 4096 9.1 and
+// 11.1) or on 16 (64 x 1000 x 8192 11.4, on 32 14.4; 32 x 6000 x 4096 12.6 and
+// 10.7; 17 x 8192 x 8192, little of whose second 16 tokens is read, 17.5 and 20.8).
 Plan plan_of(int64_t n, int64_t k, int64_t B) {
   constexpr int kFull = 180;  // workgroups that about fill the 256 CUs
   const int64_t tiles = (n + 15) / 16, steps = w_steps(k);
