@@ -481,8 +481,8 @@ fh_status fh_w8a8_create_codes(const int8_t* codes, const float* scales, int64_t
                                void* stream, fh_w8a8** out);
 
 /* fh_w8a8_destroy — release the handle (NULL is a no-op), after waiting for
- * the device to finish work that may still read it.  Captured graphs that use
- * it end with it. */
+ * the device to finish work that may still read it (so not while a stream is
+ * being captured).  Captured graphs that use it end with it. */
 void fh_w8a8_destroy(fh_w8a8* w);
 
 /* fh_w8a8_get — copy the codes [n x k] and scales [n] out (device). */
@@ -513,7 +513,9 @@ fh_status fh_w8a8_matmul(const fh_w8a8* w, const int8_t* q, int64_t ld_q, const 
 /*
  * fh_w8a8_forward — the dense head on that product: fh_dense_forward's
  * choice over the n logits of each row (argmax or one draw from softmax(z / T)
- * with the same Philox stream, LSE over all n).
+ * with the same Philox stream, LSE over all n; z / T is z times 1 / T rounded, so
+ * a draw between keys that differ by a float32 rounding may fall otherwise).
+ * +inf is drawn before any finite logit, the smallest token of several.
  *   mode, temperature, seed   as for fh_dense_forward.
  *   out_token  [B] int32: the token, -1 where no logit of the row is above
  *              -inf (NaN is never chosen).
@@ -568,8 +570,9 @@ int64_t fh_logits_workspace(int64_t B, int64_t n);
  * fh_logits_apply — the rules, then the choice of the token.  Per row b and
  * token t with logit z, in float32 and in this order: the repetition, the
  * frequency and the presence penalty, the bias, and -inf where the mask does
- * not allow t (whatever z was, NaN too).  Then fh_dense_forward's choice over
- * the row: argmax or a draw from softmax(z / T), the same Philox stream, LSE.
+ * not allow t (whatever z was, NaN too).  Then the choice over the row as
+ * fh_w8a8_forward's: argmax or a draw from softmax(z / T), the same Philox
+ * stream, LSE.
  *   logits   device [B x n] float, row stride ld_logits: of all tokens (ids
  *            NULL, n = v), e.g. fh_dense_forward's or fh_w8a8_matmul's, or of
  *            the tokens in ids, e.g. fh_forward's out_logits and out_ids.
