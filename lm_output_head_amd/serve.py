@@ -419,9 +419,9 @@ class LogitRules:
         self.v = v
         self.B = sized[0].shape[0] if sized else (mask.shape[0] if mask is not None else None)
         s = _abi.FhLogitRules()
-        # an empty list has no address: the rows that count in it go with it
-        empty = {name for name, t in (("n_prompt", history), ("n_history", history), ("n_bias", bias))
-                 if t is not None and t.shape[1] == 0}
+        # an empty list or table has no address: what counts or picks its rows goes with it
+        empty = {name for name, t, axis in (("n_prompt", history, 1), ("n_history", history, 1), ("n_bias", bias, 1),
+                                            ("mask_row", mask, 0)) if t is not None and t.shape[axis] == 0}
         for name, (t, dt) in vectors.items():
             if t is not None:
                 _vector(t, dt, self.B, name)
@@ -440,7 +440,8 @@ class LogitRules:
             if mask.dim() != 2:
                 raise ValueError(f"mask must be [R x words], got shape {tuple(mask.shape)}")
             s.ld_mask = _rows(mask, torch.int32, (mask.shape[0], (v + 31) // 32), "mask")
-            s.mask, s.mask_rows = mask.data_ptr(), mask.shape[0]
+            if mask.shape[0]:
+                s.mask, s.mask_rows = mask.data_ptr(), mask.shape[0]
             if mask_row is None and mask.shape[0] < (self.B or 0):
                 raise ValueError("the mask has fewer rows than the batch; give mask_row")
         kept = [t for t in sized + [mask] if t is not None]

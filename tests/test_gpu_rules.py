@@ -323,3 +323,15 @@ def test_lists_of_one_row_at_any_stride():
     want = torch.zeros(1, 50, device="cuda")
     want[0, 3:6] = 1
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("cut", [False, True])
+def test_a_mask_of_no_rows_allows_everything(cut):
+    """No grammar at present: every mask_row is outside [0, 0)."""
+    from lm_output_head_amd import LogitRules, logits_apply
+    z = torch.randn(3, 4000, device="cuda")
+    words = torch.zeros(2, 125, dtype=torch.int32, device="cuda")[:0] if cut else torch.zeros(
+        0, 125, dtype=torch.int32, device="cuda")
+    rows = torch.tensor([-1, 0, 5], dtype=torch.int32, device="cuda")
+    out = logits_apply(z, LogitRules(4000, mask=words, mask_row=rows))
+    assert torch.equal(out["logits"], z) and torch.equal(out["token"].long(), z.argmax(1))
