@@ -433,7 +433,7 @@ class LogitRules:
         if bias is not None:
             shape = (self.B, bias.shape[1])
             s.ld_bias = _rows(bias, torch.float32, shape, "bias")
-            if _rows(bias_ids, torch.int32, shape, "bias_ids") != s.ld_bias and self.B != 1:
+            if _rows(bias_ids, torch.int32, shape, "bias_ids") != s.ld_bias and self.B != 1 and shape[1]:
                 raise ValueError("bias_ids and bias must have the same row stride")
             s.bias_ids, s.bias, s.bias_len = bias_ids.data_ptr(), bias.data_ptr(), bias.shape[1]
         if mask is not None:

@@ -267,6 +267,13 @@ def test_binding_lists_of_one_row_have_any_stride():
             serve.LogitRules(50, bias_ids=ids, bias=bias)
 
 
+def test_binding_empty_lists_have_any_stride():
+    ids = torch.zeros(3, 40, dtype=torch.int32)[:, :0]
+    for bias in (torch.ones(3, 0), torch.ones(3, 60)[:, :0]):
+        with pytest.raises(ValueError, match="one GPU"):
+            serve.LogitRules(50, bias_ids=ids, bias=bias)
+
+
 def test_binding_apply_refusals():
     z = torch.zeros(2, 100)
     none = serve.LogitRules(100)
