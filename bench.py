@@ -204,7 +204,9 @@ def stream_bandwidth(sizes, nbuf=16, steps=100):
 CLUSTER_SOURCES = ("fh_cluster.hip",)  # the offline clustering, its own translation unit
 # the operators around the dense head: no code of theirs runs in a head call
 SERVE_SOURCES = ("fh_norm.hip", "fh_w8a8.hip", "fh_rules.hip", "fh_serve.cpp", "fh_serve.hpp",
-                 "fh_choice.hpp")
+                 "fh_choice.hpp", "fh_rows.hpp", "fh_product.hpp", "fh_serve_host.hpp",
+                 "fh_fp8.hip", "fh_fp8_quant.hip", "fh_fp8_api.cpp", "fh_fp8.hpp",
+                 "fh_beam.hip", "fh_beam_api.cpp", "fh_beam.hpp")
 
 
 def kernel_source_hash(cluster: bool = False) -> str:

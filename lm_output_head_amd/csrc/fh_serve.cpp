@@ -8,13 +8,11 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <exception>
-#include <limits>
 #include <new>
 #include <string>
 
-#include "fh_host.hpp"
 #include "fh_serve.hpp"
+#include "fh_serve_host.hpp"
 #include "flashhead.h"
 
 struct fh_w8a8 {
@@ -28,57 +26,20 @@ namespace {
 
 using fh::DeviceGuard;
 using fh::aligned16;
+using fh::aligned_to;
+using fh::check_choice;
+using fh::check_ld;
+using fh::check_workspace;
 using fh::fail;
+using fh::guarded;
 using fh::hip_fail;
-
-// No exception leaves a C entry (building an error text can throw).
-template <typename R, typename F>
-R guarded(R failed, F&& body) noexcept {
-  try {
-    fh::g_err.clear();
-    return body();
-  } catch (const std::exception&) {
-    return failed;
-  }
-}
-
-bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+using fh::inverse_of;
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxWidth = int64_t(1) << 30;    // n and v: grids stay below 2^32 threads,
 constexpr int64_t kMaxChannels = int64_t(1) << 27;  // and the product's, a wave or more per 16 channels
 constexpr int64_t kMaxList = int64_t(1) << 30;     // places of a history or list, in 32 bits with a batch past them
 constexpr int64_t kMaxK = (int64_t(1) << 17) - 1;  // 128^2 k < 2^31
-constexpr int64_t kMaxElems = int64_t(1) << 60;    // rows * stride stays far inside int64
-
-// The stride of `rows` rows of `width` elements, or an error text.
-fh_status check_ld(const char* name, int64_t ld, int64_t width, int64_t rows) {
-  if (ld < width)
-    return fail(FH_EINVAL, std::string(name) + "=" + std::to_string(ld) + " below the row's " +
-                               std::to_string(width) + " elements");
-  if (ld > kMaxElems / rows) return fail(FH_EINVAL, std::string(name) + " too large");
-  return FH_OK;
-}
-
-fh_status check_choice(int mode, float temperature) {
-  if (mode != FH_TOKEN_ARGMAX && mode != FH_TOKEN_SAMPLE)
-    return fail(FH_EINVAL, "mode must be FH_TOKEN_ARGMAX or FH_TOKEN_SAMPLE");
-  if (mode == FH_TOKEN_SAMPLE && !(temperature > 0.f && std::isfinite(temperature)))
-    return fail(FH_EINVAL, "sampling needs a finite temperature > 0");
-  return FH_OK;
-}
-
-float inverse_of(float temperature) {
-  return (float)std::min(1.0 / (double)temperature, (double)std::numeric_limits<float>::max());
-}
-
-fh_status check_workspace(const void* workspace, int64_t bytes, int64_t need) {
-  if (need == 0) return FH_OK;
-  if (!workspace || bytes < need)
-    return fail(FH_EINVAL, "this call needs " + std::to_string(need) + " bytes of workspace");
-  if (!aligned16(workspace)) return fail(FH_EINVAL, "workspace must be 16-byte aligned");
-  return FH_OK;
-}
 
 void free_w8a8(fh_w8a8* w) {
   if (!w) return;
