@@ -598,6 +598,156 @@ fh_status fh_logits_apply(const float* logits, int64_t ld_logits, const int32_t*
                           float* out_token_logit, float* out_lse, void* workspace,
                           int64_t workspace_bytes, void* stream);
 
+/*
+ * Around an fp8 head: hidden states in 8-bit floating point (OCP E4M3: bias 7,
+ * finite to 448, no infinities, NaN 0x7F and 0xFF) with a float scale per 128
+ * elements of a row (the last group of a row may be shorter), a weight with a
+ * scale per block of 128 x 128, their product and the dense head on it.
+ */
+
+/*
+ * fh_rmsnorm_fp8 — fh_rmsnorm with an fp8 output: s and y as there, and of every
+ * 128 elements of a row, in float32,
+ *   out_scale = max |y| / 448;  out_q = y / out_scale rounded to E4M3 (ties to
+ *   even, within [-448, 448]; 0 where out_scale is 0)
+ * A group that holds an infinity or NaN has an out_scale that says so (infinity
+ * or NaN) and codes that mean nothing.
+ *   out_q      device [B x d], row stride ld_q >= d.
+ *   out_scale  device [B x ceil(d / 128)] float, row stride ld_scale.
+ *   out, out_residual  as for fh_rmsnorm, either may be NULL.
+ * The other arguments as for fh_rmsnorm.
+ */
+fh_status fh_rmsnorm_fp8(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
+                         const void* weight, fh_dtype dtype, int64_t B, int64_t d, float eps,
+                         float weight_offset, void* out, int64_t ld_out, void* out_residual,
+                         int64_t ld_out_residual, uint8_t* out_q, int64_t ld_q, float* out_scale,
+                         int64_t ld_scale, void* stream);
+
+/* fh_fp8_quant — the same codes and scales of x [B x d] as it is (y = x). */
+fh_status fh_fp8_quant(const void* x, int64_t ld_x, fh_dtype dtype, int64_t B, int64_t d,
+                       uint8_t* out_q, int64_t ld_q, float* out_scale, int64_t ld_scale,
+                       void* stream);
+
+/* An fp8 weight matrix [n x k] with a float scale per block of 128 x 128. */
+typedef struct fh_fp8 fh_fp8; /* opaque */
+
+/*
+ * fh_fp8_create — quantise W, device [n x k] of dtype, dense: per block
+ * scale = max |W| / 448, codes as fh_fp8_quant's.  A block that holds an infinity
+ * or NaN gives FH_EINVAL.
+ * fh_fp8_create_codes — take codes [n x k] and scales [ceil(n / 128) x
+ * ceil(k / 128)] float as they are, both device and dense.
+ * Both copy into the handle's own layout (n k bytes, n rounded up to 16 and k to
+ * 128, plus the scales), wait for `stream`, and keep nothing of their arguments.
+ * 1 <= n <= 2^27, 1 <= k < 131072.  Not while `stream` is being captured.
+ */
+fh_status fh_fp8_create(const void* W, fh_dtype dtype, int64_t n, int64_t k, void* stream,
+                        fh_fp8** out);
+fh_status fh_fp8_create_codes(const uint8_t* codes, const float* scales, int64_t n, int64_t k,
+                              void* stream, fh_fp8** out);
+
+/* fh_fp8_destroy — as fh_w8a8_destroy. */
+void fh_fp8_destroy(fh_fp8* w);
+
+/* fh_fp8_get — copy the codes [n x k] and scales out (device). */
+fh_status fh_fp8_get(const fh_fp8* w, uint8_t* codes, float* scales, void* stream);
+
+/* fh_fp8_workspace — as fh_w8a8_workspace. */
+int64_t fh_fp8_workspace(const fh_fp8* w, const uint8_t* q, int64_t ld_q, int64_t B, int forward);
+
+/*
+ * fh_fp8_matmul — out[b, j] = sum over groups g of 128 of k of
+ *   (sum_{i in g} q[b, i] code[j, i]) (q_scale[b, g] scale[j / 128, g]),
+ * the products exact, the sums and the scales' product in float32, rounded to
+ * bf16 at the end for out_dtype FH_BF16.  How the sum over g is cut up depends on
+ * n, k and B, never on the values: equal calls give equal bits.
+ *   q        device [B x k] E4M3 codes, row stride ld_q >= k.
+ *   q_scale  device [B x ceil(k / 128)] float, row stride ld_scale.
+ *   out, workspace, B   as for fh_w8a8_matmul (fh_fp8_workspace).
+ */
+fh_status fh_fp8_matmul(const fh_fp8* w, const uint8_t* q, int64_t ld_q, const float* q_scale,
+                        int64_t ld_scale, int64_t B, void* out, int64_t ld_out,
+                        fh_dtype out_dtype, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+
+/* fh_fp8_forward — the dense head on that product; fh_w8a8_forward's arguments
+ * and choice. */
+fh_status fh_fp8_forward(const fh_fp8* w, const uint8_t* q, int64_t ld_q, const float* q_scale,
+                         int64_t ld_scale, int64_t B, int mode, float temperature, uint64_t seed,
+                         int32_t* out_token, float* out_token_logit, float* out_lse,
+                         float* out_logits, int64_t ld_logits, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/*
+ * Decoding by beams: `sequences` of `beams` rows each, row s * beams + w being
+ * beam w of sequence s.  As above these calls run on the current device, keep no
+ * state, and use the caller's workspace.
+ */
+
+/* fh_beam_workspace — bytes of workspace of a fh_beam_select call, or FH_EINVAL. */
+int64_t fh_beam_workspace(int64_t sequences, int64_t beams, int64_t n);
+
+/*
+ * fh_beam_select — of each sequence the `keep` continuations with the largest
+ * total t = score + (z - lse), best first, in float64 and rounded to float32 at
+ * the end; ties go to the smaller beam, then to the earlier place of its row.
+ *   logits   device [sequences beams x n] float, row stride ld_logits: after the
+ *            rules, of all tokens (ids NULL, n = v) or of the tokens in ids.
+ *            -inf and NaN are no continuation.
+ *   ids      device, the same shape, int32, row stride ld_ids, or NULL.  An id
+ *            outside [0, v) is no continuation; an id listed twice is two.
+ *   lse      device [sequences beams] float: the log-sum-exp to take (a head's
+ *            out_lse at T = 1, which knows more tokens than ids lists); NULL: that of
+ *            the row's logits (a row that holds NaN or +inf then has none, and
+ *            no continuation).
+ *   scores   device [sequences x beams] float: the beams' totals so far.  A beam
+ *            of -inf or NaN has no continuation (a first step gives all but
+ *            beam 0 -inf).
+ *   finished device [sequences x beams] int32 or NULL: a beam where it is not 0
+ *            has one continuation, eos with its score as it is, whatever its
+ *            logits.
+ *   eos      the token that finishes a beam, or -1 (finished is NULL then).
+ *   out_score, out_token, out_parent  device [sequences x keep], dense: the total,
+ *            the token and the beam that it continues; -inf, -1 and -1 where a
+ *            sequence has fewer continuations.
+ *   out_finished  the same, int32 or NULL: 1 where the token is eos.
+ * out_score may be scores itself and out_finished finished itself where
+ * keep = beams; no other overlap.
+ * 1 <= beams, keep <= 64, sequences beams <= 65535, 1 <= n, v <= 2^30.
+ */
+fh_status fh_beam_select(const float* logits, int64_t ld_logits, const int32_t* ids, int64_t ld_ids,
+                         int64_t sequences, int64_t beams, int64_t n, int64_t v, const float* lse,
+                         const float* scores, const int32_t* finished, int32_t eos, int64_t keep,
+                         float* out_score, int32_t* out_token, int32_t* out_parent,
+                         int32_t* out_finished, void* workspace, int64_t workspace_bytes,
+                         void* stream);
+
+/*
+ * How a state holds what belongs to the rows, in bytes: `outer` blocks (layers)
+ * of rows of `mid` parts (heads) of `positions` of `run` contiguous bytes, each
+ * level with its stride; a level of one has any.  No byte belongs to two places.
+ */
+typedef struct {
+  int64_t outer, mid, positions, run;
+  int64_t ld_outer, ld_row, ld_mid, ld_position;
+} fh_beam_layout;
+
+/*
+ * fh_beam_reorder — states[i][s, w] = states[i][s, parent[s, w]] for all w at
+ * once, in place; only rows that continue another are written.
+ *   states   host array of `count` device pointers to states of one layout, which
+ *            do not overlap; it is read before the call returns.
+ *   parent   device [sequences x beams] int32; outside [0, beams) leaves the row
+ *            as it is.
+ *   lengths  device [sequences x beams] int32 or NULL (all): positions of each
+ *            row that count, clamped to [0, positions].  A row takes its parent's;
+ *            what lies behind them is left as it is.
+ * parent and lengths must not lie in a state.  Any alignment.
+ */
+fh_status fh_beam_reorder(void* const* states, int64_t count, const fh_beam_layout* layout,
+                          int64_t sequences, int64_t beams, const int32_t* parent,
+                          const int32_t* lengths, void* stream);
+
 /* Thread-local description of the last error on this thread ("" if none). */
 const char* fh_last_error(void);
 

@@ -22,4 +22,12 @@ def __getattr__(name):
                 "fh_w8a8_matmul", "fh_w8a8_forward", "fh_logits_workspace", "fh_logits_apply"):
         from . import serve
         return getattr(serve, name)
+    if name in ("FP8Head", "rmsnorm_fp8", "fp8_quant", "fh_rmsnorm_fp8", "fh_fp8_quant", "fh_fp8_create",
+                "fh_fp8_create_codes", "fh_fp8_destroy", "fh_fp8_get", "fh_fp8_workspace", "fh_fp8_matmul",
+                "fh_fp8_forward"):
+        from . import fp8
+        return getattr(fp8, name)
+    if name in ("beam_select", "beam_reorder", "fh_beam_workspace", "fh_beam_select", "fh_beam_reorder"):
+        from . import beam
+        return getattr(beam, name)
     raise AttributeError(name)

@@ -27,7 +27,9 @@ EXPORTS = (
     "fh_set_path", "fh_sync_status",
     "fh_balanced_assign", "fh_cluster", "fh_rmsnorm", "fh_w8a8_create", "fh_w8a8_create_codes",
     "fh_w8a8_destroy", "fh_w8a8_get", "fh_w8a8_workspace", "fh_w8a8_matmul", "fh_w8a8_forward",
-    "fh_logits_workspace", "fh_logits_apply", "fh_last_error", "fh_version",
+    "fh_logits_workspace", "fh_logits_apply", "fh_rmsnorm_fp8", "fh_fp8_quant", "fh_fp8_create",
+    "fh_fp8_create_codes", "fh_fp8_destroy", "fh_fp8_get", "fh_fp8_workspace", "fh_fp8_matmul", "fh_fp8_forward",
+    "fh_beam_workspace", "fh_beam_select", "fh_beam_reorder", "fh_last_error", "fh_version",
 )
 
 
@@ -54,6 +56,11 @@ class FhLogitRules(ctypes.Structure):
                 ("mask_row", ctypes.c_void_p)]
 
 
+class FhBeamLayout(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int64) for name in ("outer", "mid", "positions", "run", "ld_outer",
+                                                    "ld_row", "ld_mid", "ld_position")]
+
+
 class FlashHeadError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"flashhead status {status}: {message}")
@@ -66,6 +73,7 @@ _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _u64 = ctypes.c_uint64
 _int = ctypes.c_int
+_i32 = ctypes.c_int32
 _f = ctypes.c_float
 
 _SIGS = {
@@ -102,6 +110,21 @@ _SIGS = {
     "fh_logits_workspace": ([_i64, _i64], _i64),
     "fh_logits_apply": ([_p, _i64, _p, _i64, _i64, _i64, _i64, ctypes.POINTER(FhLogitRules), _int,
                          _f, _u64, _p, _i64, _p, _p, _p, _p, _i64, _p], _int),
+    "fh_rmsnorm_fp8": ([_p, _i64, _p, _i64, _p, _int, _i64, _i64, _f, _f, _p, _i64, _p, _i64, _p,
+                        _i64, _p, _i64, _p], _int),
+    "fh_fp8_quant": ([_p, _i64, _int, _i64, _i64, _p, _i64, _p, _i64, _p], _int),
+    "fh_fp8_create": ([_p, _int, _i64, _i64, _p, ctypes.POINTER(_p)], _int),
+    "fh_fp8_create_codes": ([_p, _p, _i64, _i64, _p, ctypes.POINTER(_p)], _int),
+    "fh_fp8_destroy": ([_p], None),
+    "fh_fp8_get": ([_p, _p, _p, _p], _int),
+    "fh_fp8_workspace": ([_p, _p, _i64, _i64, _int], _i64),
+    "fh_fp8_matmul": ([_p, _p, _i64, _p, _i64, _i64, _p, _i64, _int, _p, _i64, _p], _int),
+    "fh_fp8_forward": ([_p, _p, _i64, _p, _i64, _i64, _int, _f, _u64, _p, _p, _p, _p, _i64, _p,
+                        _i64, _p], _int),
+    "fh_beam_workspace": ([_i64, _i64, _i64], _i64),
+    "fh_beam_select": ([_p, _i64, _p, _i64, _i64, _i64, _i64, _i64, _p, _p, _p, _i32, _i64, _p, _p,
+                        _p, _p, _p, _i64, _p], _int),
+    "fh_beam_reorder": ([_p, _i64, ctypes.POINTER(FhBeamLayout), _i64, _i64, _p, _p, _p], _int),
     "fh_last_error": ([], ctypes.c_char_p),
     "fh_version": ([], ctypes.c_char_p),
 }

@@ -294,7 +294,46 @@ def _choice_outputs(t, B, size):
     return token.view(torch.int32), logit, lse, ws if size else None
 
 
-class W8A8Head:
+class _Steps:
+    """What a decode step does on a dense head with quantised operands.  The head
+    has `device`, `matmul`, `forward`, and `_states`: the norm in the form that
+    both take."""
+
+    def step(self, x: torch.Tensor, weight=None, *, residual=None, eps=1e-6, weight_offset=0.0, rules=None,
+             mode: int = 0, temperature: float = 1.0, seed: int = 0, want_logits: bool = False,
+             stream=None) -> dict:
+        """One decode step after the last layer: rmsnorm(x + residual) in the
+        head's operands, the head, the rules (LogitRules, or None) and the choice
+        of the token."""
+        with _on(self.device, stream):
+            q, scale = self._states(x, weight, residual, eps, weight_offset)
+            if rules is None:
+                return self.forward(q, scale, mode, temperature, seed, want_logits)
+            z = self.matmul(q, scale)
+            out = logits_apply(z, rules, mode=mode, temperature=temperature, seed=seed, out=z)
+            if not want_logits:
+                del out["logits"]
+            return out
+
+    def beam_step(self, x: torch.Tensor, scores: torch.Tensor, weight=None, *, residual=None, eps=1e-6,
+                  weight_offset=0.0, rules=None, keep=None, finished=None, eos: int = -1, want_logits: bool = False,
+                  stream=None) -> dict:
+        """step for beams: x [S W x d], scores [S x W]; after the norm, the head and
+        the rules the best continuations over beams and tokens (beam_select),
+        whose "parent" beam_reorder takes."""
+        from .beam import beam_select
+        with _on(self.device, stream):
+            q, scale = self._states(x, weight, residual, eps, weight_offset)
+            z = self.matmul(q, scale)
+            if rules is not None:
+                logits_apply(z, rules, want_token=False, out=z)
+            out = beam_select(z, scores, keep=keep, finished=finished, eos=eos)
+            if want_logits:
+                out["logits"] = z
+            return out
+
+
+class W8A8Head(_Steps):
     """A dense head (or any linear layer) with int8 weights and activations:
     the rows of E quantised here, or int8 codes and scales as they are."""
 
@@ -328,6 +367,10 @@ class W8A8Head:
         if _device(q, q_scale) != dev:
             raise ValueError("tensors must be on the weight's GPU")
         return ld_q, _size(_abi.load().fh_w8a8_workspace(self.w, q.data_ptr(), ld_q, B, forward))
+
+    def _states(self, x, weight, residual, eps, weight_offset):
+        h = rmsnorm(x, weight, residual=residual, eps=eps, weight_offset=weight_offset, want_out=False, want_q=True)
+        return h["q"], h["q_scale"]
 
     def codes(self, stream=None):
         """The codes [n x k] and scales [n]."""
@@ -367,22 +410,6 @@ class W8A8Head:
                                               seed, token.data_ptr(), logit.data_ptr(), lse.data_ptr(), _ptr(logits),
                                               self.n, _ptr(ws), size, _stream(self.device)))
         return out
-
-    def step(self, x: torch.Tensor, weight=None, *, residual=None, eps=1e-6, weight_offset=0.0, rules=None,
-             mode: int = 0, temperature: float = 1.0, seed: int = 0, want_logits: bool = False,
-             stream=None) -> dict:
-        """One decode step after the last layer: rmsnorm(x + residual) in int8,
-        the head, the rules (LogitRules, or None) and the choice of the token."""
-        with _on(self.device, stream):
-            h = rmsnorm(x, weight, residual=residual, eps=eps, weight_offset=weight_offset, want_out=False,
-                        want_q=True)
-            if rules is None:
-                return self.forward(h["q"], h["q_scale"], mode, temperature, seed, want_logits)
-            z = self.matmul(h["q"], h["q_scale"])
-            out = logits_apply(z, rules, mode=mode, temperature=temperature, seed=seed, out=z)
-            if not want_logits:
-                del out["logits"]
-            return out
 
 
 # ------------------------------------------------------------ rules on logits
