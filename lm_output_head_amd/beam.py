@@ -10,6 +10,7 @@ s * W + w of a batch is beam w of sequence s, for S sequences of W beams.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -133,15 +134,20 @@ def _joined(shape, strides):
 
 def _layout(t, rows, dim, length_dim):
     """fh_beam_layout of a state, in bytes, as a tuple."""
-    if not -t.dim() <= dim < t.dim() or t.shape[dim] != rows:
-        raise ValueError(f"a state of shape {tuple(t.shape)} has no {rows} rows in dimension {dim}")
-    dim %= t.dim()
-    shape, strides, e = t.shape, t.stride(), t.element_size()
+    return _levels(t.shape, t.stride(), t.element_size(), rows, dim, length_dim)
+
+
+@functools.lru_cache(maxsize=1024)
+def _levels(shape, strides, e, rows, dim, length_dim):
+    n = len(shape)
+    if not -n <= dim < n or shape[dim] != rows:
+        raise ValueError(f"a state of shape {tuple(shape)} has no {rows} rows in dimension {dim}")
+    dim %= n
     outer = _joined(shape[:dim], strides[:dim])
-    if length_dim is not None and (not -t.dim() <= length_dim < t.dim() or length_dim % t.dim() <= dim):
+    if length_dim is not None and (not -n <= length_dim < n or length_dim % n <= dim):
         raise ValueError("length_dim must be one of the dimensions behind dim")
-    at = None if length_dim is None else length_dim % t.dim()
-    behind = [i for i in range(dim + 1, t.dim()) if i != at]
+    at = None if length_dim is None else length_dim % n
+    behind = [i for i in range(dim + 1, n) if i != at]
     rest = _joined([shape[i] for i in behind], [strides[i] for i in behind])
     run = rest.pop()[0] if rest and rest[-1][1] == 1 else 1
     if at is None:

@@ -13,6 +13,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fh_beam.hpp"
 #include "fh_choice.hpp"
@@ -27,9 +28,11 @@ typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef float f32x4a __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4), aligned(4)));
 
-// Four logits of a row from place i, -inf where there is no token.
-__device__ __forceinline__ void load_logits(const BeamArgs& a, const float* z, const int32_t* ids, int i, float (&v)[4]) {
-  if (i + 4 <= a.n) {
+// Four logits of a row from place i and their tokens, -inf where there is none.
+__device__ __forceinline__ void load_logits(const BeamArgs& a, const float* z, const int32_t* ids, int i, float (&v)[4],
+                                            int32_t (&id)[4]) {
+  const bool whole = i + 4 <= a.n;
+  if (whole) {
     const f32x4 x = *reinterpret_cast<const f32x4*>(z + i);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = x[e];
@@ -37,17 +40,20 @@ __device__ __forceinline__ void load_logits(const BeamArgs& a, const float* z, c
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = i + e < a.n ? z[i + e] : -INFINITY;
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) id[e] = i + e;
   if (ids) {
-    if (i + 4 <= a.n) {
+    if (whole) {
       const i32x4 t = *reinterpret_cast<const i32x4*>(ids + i);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if ((uint32_t)t[e] >= (uint32_t)a.v) v[e] = -INFINITY;
+      for (int e = 0; e < 4; ++e) id[e] = t[e];
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (i + e < a.n && (uint32_t)ids[i + e] >= (uint32_t)a.v) v[e] = -INFINITY;
+      for (int e = 0; e < 4; ++e) id[e] = i + e < a.n ? ids[i + e] : -1;
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if ((uint32_t)id[e] >= (uint32_t)a.v) v[e] = -INFINITY;
   }
 }
 
@@ -60,8 +66,9 @@ __global__ __launch_bounds__(256) void k_beam_scan(BeamArgs a, int chunks) {
   const float* z = a.z + row * a.ld_z;
   const int32_t* ids = a.ids ? a.ids + row * a.ld_ids : nullptr;
   float v[4][4], top[4];
+  int32_t id[4][4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) load_logits(a, z, ids, part * kPart + c * kChunk + 4 * lane, v[c]);
+  for (int c = 0; c < 4; ++c) load_logits(a, z, ids, part * kPart + c * kChunk + 4 * lane, v[c], id[c]);
 #pragma unroll
   for (int c = 0; c < 4; ++c) top[c] = wave_max(fmaxf(fmaxf(v[c][0], v[c][1]), fmaxf(v[c][2], v[c][3])));
   float sum = 0.f;
@@ -121,88 +128,197 @@ __device__ __forceinline__ int bin_of(double best, double t) {
   return min(max((int)(__float_as_uint(d) >> 20) - 967, 0), kBins - 1);
 }
 
-// A workgroup per sequence.
+// A workgroup per sequence, a wave per row of it.  ROWS: rows of a wave, each of at
+// most 256 QUADS chunks, whose largest logits stay in registers; 0: they are read
+// again wherever they are looked at.
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kMaxChunks = 512, kMaxCands = 1024, kAllChunks = 64;
+constexpr int kQuads = 4;
 static_assert(kMaxCands == kWaves * 64, "every wave's list has a place");
 
 struct BeamShared {
   double score[kMaxBeams], lse[kMaxBeams], best[kMaxBeams];
   int32_t done[kMaxBeams];
   Cand cand[kMaxCands];
+  int32_t token[kMaxCands];
   int rank[kMaxCands];
   int list[kMaxChunks];
   int hist[kBins];
   int border, chunks, cands;
 };
 
-__global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks) {
-  __shared__ BeamShared sh;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t s = blockIdx.x, row0 = s * a.beams;
-  const int W = a.beams, M = a.keep, all = W * chunks;
+__device__ __forceinline__ float most4(const f32x4a& x) { return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])); }
 
-  // the beams' log-sum-exps and best totals
-  for (int w = wave; w < W; w += kWaves) {
-    const float score = a.scores[row0 + w];
-    const bool done = (a.finished && a.finished[row0 + w]) || !(score > -INFINITY);
-    double lse = 0., best = score;
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double v) {
+  const int64_t x = __builtin_bit_cast(int64_t, v);
+  const uint32_t lo = (uint32_t)dpp_i<CTRL>((int)x), hi = (uint32_t)dpp_i<CTRL>((int)(x >> 32));
+  return __builtin_bit_cast(double, (int64_t)((uint64_t)hi << 32 | lo));
+}
+__device__ __forceinline__ int64_t readlane_l(int64_t x, int l) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)x, l);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), l);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double readlane_d(double v, int l) {
+  return __builtin_bit_cast(double, readlane_l(__builtin_bit_cast(int64_t, v), l));
+}
+// wave_sum's order in float64
+__device__ __forceinline__ double wave_sum_d(double x) {
+  x += dpp_d<0xB1>(x);
+  x += dpp_d<0x4E>(x);
+  x += dpp_d<0x141>(x);
+  x += dpp_d<0x140>(x);
+  return (readlane_d(x, 0) + readlane_d(x, 16)) + (readlane_d(x, 32) + readlane_d(x, 48));
+}
+
+template <int ROWS>
+__global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks) {
+  constexpr int kRows = ROWS > 0 ? ROWS : 1;
+  __shared__ BeamShared sh;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t s = blockIdx.x, row0 = s * a.beams;
+  const int W = a.beams, M = a.keep, all = W * chunks, quads = chunks / 4;
+
+  if (tid < kBins) sh.hist[tid] = 0;
+  if (tid == 0) sh.chunks = sh.cands = 0;
+  // four chunks from 4 i up of row w; a finished row has none written
+  auto load_top = [&](int w, int i) {
+    return *reinterpret_cast<const f32x4a*>(a.top + (row0 + w) * chunks + 4 * i);
+  };
+  const f32x4a none{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  // the beams' scores, and everything that the scan has left of them, on its way
+  // together
+  float score[kRows];
+  int32_t fin[kRows];
+  f32x4a top[kRows][kQuads];
+  float sum[kRows][kQuads];
+  if constexpr (ROWS > 0) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int w = wave + r * kWaves;
+      if (w >= W) break;
+      score[r] = a.scores[row0 + w];
+      fin[r] = a.finished ? a.finished[row0 + w] : 0;
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) {
+        const int i = lane + 64 * q;
+        top[r][q] = i < quads ? load_top(w, i) : none;
+        sum[r][q] = i < quads && !a.lse ? a.sum[(row0 + w) * quads + i] : 0.f;
+      }
+    }
+  }
+  // the rows' log-sum-exps and best totals
+  auto begin_row = [&](int w, float sc, int32_t f, auto most, auto adds) {
+    const bool done = f || !(sc > -INFINITY);
+    double lse = 0., best = sc;
     if (!done) {
-      const f32x4a* top = reinterpret_cast<const f32x4a*>(a.top + (row0 + w) * chunks);
-      const float* sum = a.sum + (row0 + w) * (chunks / 4);
-      float m = -INFINITY;
-      for (int i = lane; i < chunks / 4; i += 64) {
-        const f32x4a x = top[i];
-        m = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
-      }
-      m = wave_max(m);
-      if (a.lse) {
+      const float m = wave_max(most());
+      if (a.lse)
         lse = a.lse[row0 + w];
-      } else {
-        double acc = 0.;
-        for (int i = lane; i < chunks / 4; i += 64) {
-          const f32x4a x = top[i];
-          acc += (double)(sum[i] * exp_from(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), m));
-        }
-        for (int k = 1; k < 64; k <<= 1) acc += lane_xor(acc, k);
-        lse = m + log(acc);
-      }
-      best = score + ((double)m - lse);
+      else
+        lse = m + log(wave_sum_d(adds(m)));
+      best = sc + ((double)m - lse);
     }
     if (lane == 0) {
-      sh.score[w] = score;
+      sh.score[w] = sc;
       sh.lse[w] = lse;
       sh.best[w] = best;
       sh.done[w] = done;
     }
+  };
+  if constexpr (ROWS > 0) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int w = wave + r * kWaves;
+      if (w >= W) break;
+      begin_row(
+          w, score[r], fin[r],
+          [&]() {
+            float m = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < kQuads; ++q) m = fmaxf(m, most4(top[r][q]));
+            return m;
+          },
+          [&](float m) {
+            double acc = 0.;
+#pragma unroll
+            for (int q = 0; q < kQuads; ++q) acc += (double)(sum[r][q] * exp_from(most4(top[r][q]), m));
+            return acc;
+          });
+    }
+  } else {
+    for (int w = wave; w < W; w += kWaves)
+      begin_row(
+          w, a.scores[row0 + w], a.finished ? a.finished[row0 + w] : 0,
+          [&]() {
+            float m = -INFINITY;
+            for (int i = lane; i < quads; i += 64) m = fmaxf(m, most4(load_top(w, i)));
+            return m;
+          },
+          [&](float m) {
+            double acc = 0.;
+            for (int i = lane; i < quads; i += 64)
+              acc += (double)(a.sum[(row0 + w) * quads + i] * exp_from(most4(load_top(w, i)), m));
+            return acc;
+          });
   }
-  if (tid < kBins) sh.hist[tid] = 0;
-  if (tid == 0) sh.chunks = sh.cands = 0;
   __syncthreads();
   double best = -INFINITY;
   for (int w = 0; w < W; ++w) best = sh.best[w] > best ? sh.best[w] : best;  // NaN is no total
 
   auto total = [&](int w, float z) { return sh.score[w] + ((double)z - sh.lse[w]); };
-  // every chunk: f(beam, chunk, its largest total)
+  // every chunk: f(chunk, its largest total)
   auto each_chunk = [&](auto f) {
-    for (int i = tid; i < all; i += kThreads) {
-      const int w = i / chunks, c = i % chunks;
-      if (!sh.done[w]) f(w, c, total(w, a.top[(row0 + w) * chunks + c]));
+    auto four = [&](int w, double sc, double lse, int i, const f32x4a& x) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f(w * chunks + 4 * i + e, sc + ((double)x[e] - lse));
+    };
+    if constexpr (ROWS > 0) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const int w = wave + r * kWaves;
+        if (w >= W) break;
+        if (sh.done[w]) continue;
+        const double sc = sh.score[w], lse = sh.lse[w];
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q)
+          if (lane + 64 * q < quads) four(w, sc, lse, lane + 64 * q, top[r][q]);
+      }
+    } else {
+      for (int w = wave; w < W; w += kWaves) {
+        if (sh.done[w]) continue;
+        const double sc = sh.score[w], lse = sh.lse[w];
+        for (int i = lane; i < quads; i += 64) four(w, sc, lse, i, load_top(w, i));
+      }
     }
   };
-  // the listed chunks' places, a wave per chunk, and the finished beams:
-  // f(total, beam << 32 | place)
+  // the listed chunks' places, a wave per chunk and two at a time, and the finished
+  // beams: f(total, beam << 32 | place, token)
   auto each_place = [&](int listed, bool every, auto f) {
-    for (int i = wave; i < listed; i += kWaves) {
-      const int at = every ? i : sh.list[i], w = at / chunks, c = at % chunks;
-      if (sh.done[w]) continue;
-      float z[4];
-      const int place = c * kChunk + 4 * lane;
-      load_logits(a, a.z + (row0 + w) * a.ld_z, a.ids ? a.ids + (row0 + w) * a.ld_ids : nullptr, place, z);
+    for (int i0 = wave; i0 < listed; i0 += 2 * kWaves) {
+      float z[2][4];
+      int32_t id[2][4];
+      int w[2], place[2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f(total(w, z[e]), (int64_t)w << 32 | (place + e));
+      for (int u = 0; u < 2; ++u) {
+        const int i = i0 + u * kWaves, at = i < listed ? every ? i : sh.list[i] : 0;
+        w[u] = at / chunks;
+        place[u] = at % chunks * kChunk + 4 * lane;
+        if (i < listed && !sh.done[w[u]]) {
+          load_logits(a, a.z + (row0 + w[u]) * a.ld_z, a.ids ? a.ids + (row0 + w[u]) * a.ld_ids : nullptr, place[u], z[u],
+                      id[u]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[u][e] = -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f(total(w[u], z[u][e]), (int64_t)w[u] << 32 | (place[u] + e), id[u][e]);
     }
-    if (tid < W && sh.done[tid]) f(sh.score[tid], (int64_t)tid << 32);
+    if (tid < W && sh.done[tid]) f(sh.score[tid], (int64_t)tid << 32, a.eos);
   };
   auto count = [&](double t) {
     if (t > -INFINITY) atomicAdd(&sh.hist[bin_of(best, t)], 1);
@@ -230,16 +346,16 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
   const bool every = all <= kAllChunks;
   int border, listed = all;
   if (every) {
-    each_place(all, true, [&](double t, int64_t) { count(t); });
+    each_place(all, true, [&](double t, int64_t, int32_t) { count(t); });
     border = find_border();
   } else {
-    each_chunk([&](int, int, double t) { count(t); });
+    each_chunk([&](int, double t) { count(t); });
     if (tid < W && sh.done[tid]) count(sh.score[tid]);
     border = find_border();
-    each_chunk([&](int w, int c, double t) {
+    each_chunk([&](int at, double t) {
       if (t > -INFINITY && bin_of(best, t) <= border) {
         const int i = atomicAdd(&sh.chunks, 1);
-        if (i < kMaxChunks) sh.list[i] = w * chunks + c;
+        if (i < kMaxChunks) sh.list[i] = at;
       }
     });
     __syncthreads();
@@ -247,24 +363,24 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
   }
   int cands = kMaxCands + 1;
   if (every || listed <= kMaxChunks) {
-    each_place(listed, every, [&](double t, int64_t at) {
+    each_place(listed, every, [&](double t, int64_t at, int32_t token) {
       if (t > -INFINITY && bin_of(best, t) <= border) {
         const int i = atomicAdd(&sh.cands, 1);
-        if (i < kMaxCands) sh.cand[i] = Cand{t, at};
+        if (i < kMaxCands) {
+          sh.cand[i] = Cand{t, at};
+          sh.token[i] = token;
+        }
       }
     });
     __syncthreads();
     cands = sh.cands;
   }
 
-  auto write = [&](int r, const Cand& c) {
+  auto write = [&](int r, const Cand& c, int32_t token) {
     const bool live = c.t > -INFINITY;
-    const int w = (int)(c.at >> 32), place = (int)c.at;
-    int32_t token = -1;
-    if (live) token = sh.done[w] ? a.eos : a.ids ? a.ids[(row0 + w) * a.ld_ids + place] : place;
     a.out_score[s * M + r] = live ? (float)c.t : -INFINITY;
-    a.out_token[s * M + r] = token;
-    a.out_parent[s * M + r] = live ? w : -1;
+    a.out_token[s * M + r] = live ? token : -1;
+    a.out_parent[s * M + r] = live ? (int)(c.at >> 32) : -1;
     if (a.out_finished) a.out_finished[s * M + r] = live && token == a.eos;
   };
   if (cands <= kMaxCands) {
@@ -281,8 +397,8 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
       if (above) atomicAdd(&sh.rank[i], above);
     }
     __syncthreads();
-    if (tid < cands && sh.rank[tid] < M) write(sh.rank[tid], sh.cand[tid]);
-    if (tid >= cands && tid < M) write(tid, worst());
+    if (tid < cands && sh.rank[tid] < M) write(sh.rank[tid], sh.cand[tid], sh.token[tid]);
+    if (tid >= cands && tid < M) write(tid, worst(), -1);
     return;
   }
 
@@ -290,10 +406,7 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
   // 64 of its chunks in order, and the waves' lists are merged.
   Cand mine = worst();
   auto offer = [&](const Cand& c) {
-    const Cand last{__builtin_bit_cast(double, (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(__builtin_bit_cast(int64_t, mine.t) >> 32), M - 1) << 32 |
-                                                         (uint32_t)__builtin_amdgcn_readlane((int)__builtin_bit_cast(int64_t, mine.t), M - 1))),
-                    (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine.at >> 32), M - 1) << 32 |
-                              (uint32_t)__builtin_amdgcn_readlane((int)mine.at, M - 1))};
+    const Cand last{readlane_d(mine.t, M - 1), readlane_l(mine.at, M - 1)};
     if (!__ballot(beats(c, last))) return;
     Cand x = c;
     sort64(x, lane);
@@ -321,86 +434,153 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
     __syncthreads();
     if (wave < half) merge64(mine, sh.cand[(wave + half) * 64 + lane], lane);
   }
-  if (wave == 0 && lane < M) write(lane, mine);
+  if (wave == 0 && lane < M) {
+    int32_t token = -1;
+    if (mine.t > -INFINITY) {
+      const int w = (int)(mine.at >> 32), place = (int)mine.at;
+      token = sh.done[w] ? a.eos : a.ids ? a.ids[(row0 + w) * a.ld_ids + place] : place;
+    }
+    write(lane, mine, token);
+  }
 }
 
 // ------------------------------------------------------------- reordering
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// The first n < sizeof(V) bytes at p, and n of v to p.
+template <typename V>
+__device__ __forceinline__ V load_bytes(const char* p, int n) {
+  uint64_t lo = 0, hi = 0;
+  for (int i = 0; i < n; ++i) {
+    const uint64_t b = (uint8_t)p[i];
+    if (i < 8)
+      lo |= b << (8 * i);
+    else
+      hi |= b << (8 * i - 64);
+  }
+  if constexpr (sizeof(V) == 4)
+    return (uint32_t)lo;
+  else
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+__device__ __forceinline__ void store_bytes(char* p, const u32x4& v, int n) {
+  uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+  for (int i = 0; i < n; ++i) {
+    p[i] = (char)lo;
+    lo = lo >> 8 | hi << 56;
+    hi >>= 8;
+  }
+}
+__device__ __forceinline__ void store_bytes(char* p, uint32_t v, int n) {
+  for (int i = 0; i < n; ++i) p[i] = (char)(v >> (8 * i));
+}
+
 // Rows [sequences x beams] of states are permuted in place within each sequence: a
-// thread owns a column, the same bytes of all beams of a sequence, reads what the
-// beams continue and then writes those that continue another.  WMAX: registers for
-// that many beams, V bytes each.
-template <int WMAX, typename V>
-__global__ __launch_bounds__(256) void k_beam_reorder(BeamReorderArgs a, int64_t run, int64_t positions, int64_t slabs,
-                                                      int64_t items) {
+// thread owns columns, the same bytes of all beams of a sequence, reads what the
+// beams continue and then writes those that continue another.  A workgroup's
+// columns lie in one part of a row (state, layer, sequence, head), kSlab of them;
+// lane m of each wave looks up what beam m takes.  WMAX: registers for that many
+// beams, V bytes each.  DENSE: the positions of a part are one run.
+constexpr int kSlab = 256;
+
+template <int WMAX, typename V, bool DENSE, bool PAST>
+__global__ __launch_bounds__(256) void k_beam_reorder(BeamReorderArgs a, int64_t run, uint32_t slabs, uint32_t items) {
   constexpr int N = (int)sizeof(V);
-  const int W = a.beams;
-  const bool dense = positions == 1;  // all positions of a row are one run
-  const int64_t per = (run + N - 1) / N, columns = per * positions;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t slab = item % slabs, rest = item / slabs;
-    const int64_t s = rest % a.sequences, seg = rest / a.sequences;
-    const int64_t mid = seg % a.mid, outer = seg / a.mid % a.outer, st = seg / a.mid / a.outer;
-    const int64_t col = slab * 256 + threadIdx.x;
-    if (col >= columns) continue;
-    const int64_t p = dense ? 0 : col / per, o = (dense ? col : col % per) * N;
-    char* base = static_cast<char*>(a.state[st]) + outer * a.ld_outer + s * W * a.ld_row + mid * a.ld_mid +
-                 p * a.ld_position + o;
-    const int32_t* parent = a.parent + s * W;
-    // bytes of the column that beam m takes: N, fewer at a row's end, or none
-    auto wanted = [&](int m, int* src) -> int {
-      *src = m < W ? parent[m] : -1;
-      if ((uint32_t)*src >= (uint32_t)W || *src == m) return 0;
+  const int W = a.beams, lane = threadIdx.x & 63;
+  const uint32_t per = (uint32_t)((run + N - 1) / N);  // columns of a position, unless DENSE
+  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const uint32_t slab = item % slabs, rest = item / slabs;
+    const uint32_t s = rest % (uint32_t)a.sequences, seg = rest / (uint32_t)a.sequences;
+    const uint32_t mid = seg % (uint32_t)a.mid, layer = seg / (uint32_t)a.mid;
+    const uint32_t outer = layer % (uint32_t)a.outer, st = layer / (uint32_t)a.outer;
+    const int64_t col0 = (int64_t)slab * kSlab;
+    // what beam `lane` takes: its parent, and the bytes (positions) of it that this
+    // workgroup moves
+    int src = lane < W ? a.parent[(int64_t)s * W + lane] : -1, moves = 0;
+    if ((uint32_t)src < (uint32_t)W && src != lane) {
       int64_t count = a.positions;
-      if (a.lengths) count = min(max((int64_t)a.lengths[s * W + *src], (int64_t)0), a.positions);
-      if (!dense) return p < count ? (int)min(run - o, (int64_t)N) : 0;
-      return (int)min(max(count * a.run - o, (int64_t)0), (int64_t)N);
-    };
-    if (o + N <= run) {
-      V v[WMAX];
+      if (a.lengths) count = min(max((int64_t)a.lengths[(int64_t)s * W + src], (int64_t)0), a.positions);
+      moves = DENSE ? (int)min(max(count * a.run - col0 * N, (int64_t)0), (int64_t)kSlab * N) : (int)count;
+    }
+    if (!__ballot(moves > 0)) continue;
+    char* base = static_cast<char*>(a.state[st]) + outer * a.ld_outer + (int64_t)s * W * a.ld_row + mid * a.ld_mid +
+                 (DENSE ? col0 * N : 0);
+    const int64_t left = DENSE ? run - col0 * N : run;  // bytes of the run from `base` on
+    // the column's place from `base`, the run's bytes from it on, and its position
+    // or (DENSE) its byte of the slab
+    typename std::conditional<DENSE, uint32_t, int64_t>::type at;
+    int behind, p;
+    if (DENSE) {
+      p = ((int)threadIdx.x) * N;
+      at = p;
+      behind = (int)min(left - p, (int64_t)N);
+    } else {
+      const int64_t col = col0 + threadIdx.x;
+      const uint32_t q = (uint32_t)((uint64_t)col / per), o = (uint32_t)((uint64_t)col % per) * N;
+      p = (int)q;
+      at = q * a.ld_position + o;
+      behind = (int64_t)q < a.positions ? (int)min(left - o, (int64_t)N) : 0;
+    }
+    // bytes (of N) that beam m takes here, its count being `moves` of lane m
+    auto wanted = [&](int count) { return min(DENSE ? count - p : p < count ? N : 0, behind); };
+    typedef V U __attribute__((aligned(1)));
+    V v[WMAX];
 #pragma unroll
-      for (int m = 0; m < WMAX; ++m) {
-        int src;
-        if (wanted(m, &src)) __builtin_memcpy(&v[m], base + src * a.ld_row, N);
+    for (int m = 0; m < WMAX; ++m) {
+      const int count = __builtin_amdgcn_readlane(moves, m), from = __builtin_amdgcn_readlane(src, m);
+      const char* row = base + from * a.ld_row;
+      if (count > 0 && wanted(count) > 0) {
+        if (behind == N)
+          v[m] = PAST ? __builtin_nontemporal_load(reinterpret_cast<const U*>(row + at))
+                      : *reinterpret_cast<const U*>(row + at);
+        else  // a run's last bytes
+          v[m] = load_bytes<V>(row + at, behind);
       }
+    }
 #pragma unroll
-      for (int m = 0; m < WMAX; ++m) {
-        int src;
-        const int n = wanted(m, &src);
-        if (n == N) {
-          __builtin_memcpy(base + m * a.ld_row, &v[m], N);
-        } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (i < n) base[m * a.ld_row + i] = reinterpret_cast<const char*>(&v[m])[i];
-        }
-      }
-    } else {  // the row's last bytes, one by one
-      for (int i = 0; o + i < run; ++i) {
-        char v[WMAX];
-#pragma unroll
-        for (int m = 0; m < WMAX; ++m) {
-          int src;
-          if (wanted(m, &src) > i) v[m] = base[src * a.ld_row + i];
-        }
-#pragma unroll
-        for (int m = 0; m < WMAX; ++m) {
-          int src;
-          if (wanted(m, &src) > i) base[m * a.ld_row + i] = v[m];
-        }
+    for (int m = 0; m < WMAX; ++m) {
+      const int count = __builtin_amdgcn_readlane(moves, m);
+      char* row = base + m * a.ld_row;
+      if (count > 0) {
+        const int n = wanted(count);
+        if (n == N)
+          __builtin_nontemporal_store(v[m], reinterpret_cast<U*>(row + at));
+        else if (n > 0)
+          store_bytes(row + at, v[m], n);
       }
     }
   }
 }
 
+// How a call is cut up: bytes of a column, of a run, and workgroups' pieces.
+struct Cut {
+  bool dense, past;
+  int64_t run, slabs, items;
+  Cut(const BeamReorderArgs& a, int bytes) {
+    dense = a.ld_position == a.run || a.positions == 1;
+    run = dense ? a.run * a.positions : a.run;
+    slabs = ((run + bytes - 1) / bytes * (dense ? 1 : a.positions) + kSlab - 1) / kSlab;
+    items = slabs * a.sequences * a.mid * a.outer * a.count;
+    past = items * kSlab * bytes * a.beams > int64_t(256) << 20;
+  }
+};
+// Registers for 32 or 64 beams are four bytes each.
+int column_bytes(int beams) { return beams <= 16 ? 16 : 4; }
+
+template <int WMAX, typename V, bool DENSE>
+void launch_reorder(const BeamReorderArgs& a, const Cut& c, hipStream_t st) {
+  const dim3 grid((unsigned)std::min<int64_t>(c.items, 1 << 20));
+  hipLaunchKernelGGL(c.past ? (k_beam_reorder<WMAX, V, DENSE, true>) : (k_beam_reorder<WMAX, V, DENSE, false>), grid,
+                     dim3(256), 0, st, a, c.run, (uint32_t)c.slabs, (uint32_t)c.items);
+}
 template <int WMAX, typename V>
 void launch_reorder(const BeamReorderArgs& a, hipStream_t st) {
-  const bool dense = a.ld_position == a.run || a.positions == 1;
-  const int64_t run = dense ? a.run * a.positions : a.run, positions = dense ? 1 : a.positions;
-  const int64_t columns = (run + (int64_t)sizeof(V) - 1) / (int64_t)sizeof(V) * positions, slabs = (columns + 255) / 256;
-  const int64_t items = slabs * a.sequences * a.mid * a.outer * a.count;
-  hipLaunchKernelGGL((k_beam_reorder<WMAX, V>), dim3((unsigned)std::min<int64_t>(items, 1 << 22)), dim3(256), 0, st, a,
-                     run, positions, slabs, items);
+  const Cut c(a, (int)sizeof(V));
+  if (c.dense)
+    launch_reorder<WMAX, V, true>(a, c, st);
+  else
+    launch_reorder<WMAX, V, false>(a, c, st);
 }
 
 }  // namespace
@@ -411,17 +591,32 @@ hipError_t launch_beam_select(const BeamArgs& a, int64_t sequences, hipStream_t 
   const int chunks = (int)beam_chunks(a.n);
   hipLaunchKernelGGL(k_beam_scan, dim3((unsigned)((chunks + 15) / 16), (unsigned)(sequences * a.beams)), dim3(256), 0, st,
                      a, chunks);
-  hipLaunchKernelGGL(k_beam_choose, dim3((unsigned)sequences), dim3(kThreads), 0, st, a, chunks);
+  void (*choose)(BeamArgs, int) = chunks > 256 * kQuads || a.beams > 2 * kWaves ? k_beam_choose<0>
+                                  : a.beams > kWaves                              ? k_beam_choose<2>
+                                                                                  : k_beam_choose<1>;
+  hipLaunchKernelGGL(choose, dim3((unsigned)sequences), dim3(kThreads), 0, st, a, chunks);
   return hipGetLastError();
+}
+
+bool beam_reorder_fits(const BeamReorderArgs& a) {
+  const int64_t most = (int64_t(1) << 31) - 1;
+  const Cut c(a, column_bytes(a.beams));
+  int64_t items = c.slabs;
+  if (items > most || (!c.dense && a.positions > most)) return false;
+  for (int64_t n : {a.sequences, a.mid, a.outer, (int64_t)a.count}) {
+    if (n > most / items) return false;
+    items *= n;
+  }
+  return true;
 }
 
 hipError_t launch_beam_reorder(const BeamReorderArgs& a, hipStream_t st) {
   if (a.beams <= 4)
-    launch_reorder<4, uint4>(a, st);
+    launch_reorder<4, u32x4>(a, st);
   else if (a.beams <= 8)
-    launch_reorder<8, uint4>(a, st);
+    launch_reorder<8, u32x4>(a, st);
   else if (a.beams <= 16)
-    launch_reorder<16, uint4>(a, st);
+    launch_reorder<16, u32x4>(a, st);
   else if (a.beams <= 32)
     launch_reorder<32, uint32_t>(a, st);
   else

@@ -41,6 +41,7 @@ struct BeamReorderArgs {
   int64_t sequences, outer, mid, positions, run;
   int64_t ld_outer, ld_row, ld_mid, ld_position;
 };
+bool beam_reorder_fits(const BeamReorderArgs& a);  // a launch's pieces are counted in 32 bits
 hipError_t launch_beam_reorder(const BeamReorderArgs& a, hipStream_t st);
 
 }  // namespace fh

@@ -154,6 +154,7 @@ fh_status fh_beam_reorder(void* const* states, int64_t count, const fh_beam_layo
     for (int64_t i = 0; i < count; i += fh::kReorderStates) {
       a.count = (int)std::min<int64_t>(count - i, fh::kReorderStates);
       std::copy(states + i, states + i + a.count, a.state);
+      if (!fh::beam_reorder_fits(a)) return fail(FH_EINVAL, "the states are too large for one call");
       const hipError_t r = fh::launch_beam_reorder(a, static_cast<hipStream_t>(stream));
       if (r != hipSuccess) return hip_fail(r, "reordering launch");
     }

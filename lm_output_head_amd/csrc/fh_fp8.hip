@@ -208,11 +208,23 @@ __global__ __launch_bounds__(64 * KW * G) void k_fp8_few(FP8Args a) {
 // each takes a run of the blocks of k, with buffers of its own, and the first adds
 // up the sums.  HALF: in half precision, which the tokens are staged in and each
 // wave's rows of W are converted to as they are used.
+//
+// 64 rows of a wave (FN = 4) halve what it reads of LDS for a product; their sums
+// take half the registers, so two waves share a SIMD.  In fp8 (128 tokens) W then
+// has room for one block alone: a row's registers are loaded again right behind
+// their last product, and the other wave covers the wait.  4096 x 10240 x 2560 in us:
+// 132 with 32 rows of eight waves; 118 with 64 of four; 109 with tokens read in
+// whole lines (16 rows of 64 bytes a load before) and eight neighbouring row tiles
+// of a panel at once; 102 with those loads spread over the products and sums three
+// products behind (2.1 PFLOP/s; the library's fp8 product without scales per block
+// takes 122).  Without any load it would take 82, without the multiply-adds of
+// the scales too 67: the matrix cores are busy 63% of the cycles, at 1.75 GHz.
+// In half precision 300 x 100000 x 1024 takes 83 us, 0.74 PFLOP/s.
 template <int FT, int FN, int WN, int KW, bool HALF, bool PAST, bool BF16, bool HEAD>
-__global__ __launch_bounds__(64 * WN * KW) void k_fp8_tile(FP8Args a, int n_tiles, int q_tiles) {
+__global__ __launch_bounds__(64 * WN * KW) __attribute__((amdgpu_waves_per_eu(FN == 4 || WN * KW == 8 ? 2 : 1))) void k_fp8_tile(FP8Args a, int n_tiles, int q_tiles) {
   constexpr int kFrags = 2 * FT;                // 1 KB of codes each, of a token block
-  constexpr int kOwn = (kFrags + WN - 1) / WN;  // of them, this wave's to stage
   constexpr int kBlock = kFrags * 64 * (HALF ? 2 : 1);
+  constexpr int kDepth = FN == 4 && !HALF ? 1 : 2;  // blocks of W in registers
   static_assert(FT * 16 <= 64 * WN, "a thread of a group per token scale");
   static_assert(8 % FN == 0, "a wave's rows lie in one block of 128");
   typedef typename Out<BF16>::T T;
@@ -224,12 +236,15 @@ __global__ __launch_bounds__(64 * WN * KW) void k_fp8_tile(FP8Args a, int n_tile
   __shared__ float sScale[KW][2][16 * FT];
   __shared__ Part sP[HEAD ? WN : 1][HEAD ? 16 * FT : 1];
 
-  // workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles, token
-  // tiles fastest, so that its L2 keeps the rows of W that they share
+  // workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles, by panels of
+  // eight row tiles, so that its L2 keeps what neighbours share
   const int total = n_tiles * q_tiles, per = (total + 7) / 8;
   const int tile = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
   if ((int)(blockIdx.x >> 3) >= per || tile >= total) return;
-  const int nt = tile / q_tiles, qt = tile % q_tiles;
+  constexpr int kPanel = 8;
+  const int panel = tile / (kPanel * q_tiles), in = tile % (kPanel * q_tiles);
+  const int wide = min(kPanel, n_tiles - panel * kPanel);
+  const int nt = panel * kPanel + in % wide, qt = in / wide;
 
   const int tid = threadIdx.x, lane = tid & 63, all = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wave = all % WN, group = all / WN;
@@ -245,88 +260,120 @@ __global__ __launch_bounds__(64 * WN * KW) void k_fp8_tile(FP8Args a, int n_tile
 #pragma unroll
   for (int m = 0; m < FN; ++m) wp[m] = static_cast<const i32x4*>(a.W) + min(t0 + m, rows - 1) * steps * 128 + lane;
   const float* sp = a.ws + min(t0, rows - 1) / 8 * steps;
-  // this wave's fragments of a block: f = half * FT + token tile
+  // A block's chunks of 16 codes go to the group's threads in the order of the
+  // tokens' rows, so that eight lanes read 128 bytes of one; in LDS chunk g of half h
+  // of token `col` stands at 16 g + (col ^ (g + 4 h)) of its fragment, which spreads
+  // those eight over the banks.
+  const int mine = tid - group * 64 * WN;  // this thread in its group
+  constexpr int kOwn = (128 * FT + 64 * WN - 1) / (64 * WN);
+  constexpr bool kAllOwn = 128 * FT % (64 * WN) == 0;  // else some threads stage nothing
   const uint8_t* qp[kOwn];
-  int qh[kOwn];
+  int qs_at[kOwn];
+  const int qc = mine & 7;  // its chunk of the 128
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
-    const int f = min(wave + i * WN, kFrags - 1);
+    const int row = min(i * 8 * WN + (mine >> 3), 16 * FT - 1);
     // a token past the last stands in as the last, its results are dropped
-    qp[i] = a.q + (int64_t)min(q0 + 16 * (f % FT) + col, a.B - 1) * a.ld_q;
-    qh[i] = f / FT;
+    qp[i] = a.q + (int64_t)min(q0 + row, a.B - 1) * a.ld_q;
+    qs_at[i] = ((HALF ? 2 : 1) * (qc >> 2) * FT + row / 16) * 64 + 16 * (qc & 3) + ((row & 15) ^ qc);
   }
-  const int mine = tid - group * 64 * WN;  // this thread's token scale
+  int at_half[2];  // where this lane's chunk stands in a fragment of either half
+#pragma unroll
+  for (int h = 0; h < 2; ++h) at_half[h] = 16 * g + (col ^ (g + 4 * h));
   const float* qsp = a.qs + (int64_t)min(q0 + min(mine, 16 * FT - 1), a.B - 1) * a.ld_qs;
   i32x4 qr[kOwn];
   float sr;
+  auto load_own = [&](int blk, int i) {
+    // a 16-byte chunk past the row stands in as its first (see k_fp8_few)
+    const int c = 8 * (first + blk) + qc;
+    qr[i] = *reinterpret_cast<const i32x4*>(qp[i] + 16 * (c < chunks ? c : 0));
+    if (i == 0) sr = qsp[min(first + blk, steps - 1)];
+  };
   auto load_q = [&](int blk) {
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      // a 16-byte chunk past the row stands in as its first (see k_fp8_few)
-      const int c = 8 * (first + blk) + 4 * qh[i] + g;
-      qr[i] = *reinterpret_cast<const i32x4*>(qp[i] + 16 * (c < chunks ? c : 0));
-    }
-    sr = qsp[min(first + blk, steps - 1)];
+    for (int i = 0; i < kOwn; ++i) load_own(blk, i);
   };
   auto store_q = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-      const int f = wave + i * WN;
-      if (kFrags % WN != 0 && f >= kFrags) continue;
+      if (!kAllOwn && i * 8 * WN + (mine >> 3) >= 16 * FT) continue;
+      i32x4* at = sQ + buf * kBlock + qs_at[i];
       if constexpr (HALF) {
-        f16x8* at = reinterpret_cast<f16x8*>(sQ + buf * kBlock) + (2 * qh[i] * FT + f % FT) * 64 + lane;
-        at[0] = half_of(qr[i][0], qr[i][1]);
-        at[FT * 64] = half_of(qr[i][2], qr[i][3]);
+        *reinterpret_cast<f16x8*>(at) = half_of(qr[i][0], qr[i][1]);
+        *reinterpret_cast<f16x8*>(at + FT * 64) = half_of(qr[i][2], qr[i][3]);
       } else {
-        sQ[buf * kBlock + f * 64 + lane] = qr[i];
+        *at = qr[i];
       }
     }
     if (mine < 16 * FT) sScale[group][buf][mine] = sr;
   };
-  i32x4 wf[2][FN][2];
+  i32x4 wf[kDepth][FN][2];
   float wsc[2];
-  auto load_w = [&](int blk, i32x4 (&dst)[FN][2], float& s) {
+  auto load_frag = [&](int blk, int m, i32x4 (&dst)[2]) {
     const int at = min(first + blk, steps - 1);
 #pragma unroll
-    for (int m = 0; m < FN; ++m)
+    for (int h = 0; h < 2; ++h) {
+      const i32x4* p = wp[m] + (int64_t)at * 128 + 64 * h;
+      dst[h] = PAST ? __builtin_nontemporal_load(p) : *p;
+    }
+  };
+  auto load_w = [&](int blk, i32x4 (&dst)[FN][2], float& s) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const i32x4* p = wp[m] + (int64_t)at * 128 + 64 * h;
-        dst[m][h] = PAST ? __builtin_nontemporal_load(p) : *p;
-      }
-    s = sp[at];
+    for (int m = 0; m < FN; ++m) load_frag(blk, m, dst[m]);
+    s = sp[min(first + blk, steps - 1)];
   };
   f32x4 acc[FN][FT];
 #pragma unroll
   for (int m = 0; m < FN; ++m)
 #pragma unroll
     for (int t = 0; t < FT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](int blk, int buf, const i32x4 (&w)[FN][2], float ws) {
+  auto multiply = [&](int blk, int buf, i32x4 (&w)[FN][2], float ws) {
     if (KW > 1 && first + blk >= steps) return;
-    Halves wh[FN];
     if constexpr (HALF) {
+      Halves wh[FN];
 #pragma unroll
       for (int m = 0; m < FN; ++m) wh[m] = Halves(w[m][0], w[m][1]);
-    }
 #pragma unroll
-    for (int t = 0; t < FT; ++t) {
-      const float sc = sScale[group][buf][16 * t + col] * ws;
-      if constexpr (HALF) {
-        const f16x8* q = reinterpret_cast<const f16x8*>(sQ + buf * kBlock) + t * 64 + lane;
+      for (int t = 0; t < FT; ++t) {
+        const float sc = sScale[group][buf][16 * t + col] * ws;
+        const f16x8* q = reinterpret_cast<const f16x8*>(sQ + buf * kBlock) + t * 64;
         f32x4 part[FN];
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          const f16x8 qf = q[h * FT * 64];
+          const f16x8 qf = q[h * FT * 64 + at_half[h >> 1]];
 #pragma unroll
           for (int m = 0; m < FN; ++m)
             part[m] = mfma_half(wh[m].v[h], qf, h == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : part[m]);
         }
 #pragma unroll
         for (int m = 0; m < FN; ++m) add_scaled(acc[m][t], part[m], sc);
-      } else {
-        const i32x8 qf = both(sQ[buf * kBlock + t * 64 + lane], sQ[buf * kBlock + (FT + t) * 64 + lane]);
+      }
+    } else {
+      // the next tokens are read while these are multiplied, and a product is added
+      // up three products later; with one block of W, so are the loads for the next
+      static_assert(kDepth == 2 || (KW == 1 && 4 * kOwn <= FN * FT), "the loads fit between the products");
+      constexpr int kBehind = 3;
+      i32x8 qf[2];
+      float sc[4];  // of three tokens in use, while a fourth comes
+      f32x4 part[kBehind + 1];
+      auto load = [&](int t) {
+        qf[t & 1] = both(sQ[buf * kBlock + t * 64 + at_half[0]], sQ[buf * kBlock + (FT + t) * 64 + at_half[1]]);
+        sc[t % 4] = sScale[group][buf][16 * t + col];
+      };
+      load(0);
 #pragma unroll
-        for (int m = 0; m < FN; ++m) add_scaled(acc[m][t], mfma_fp8(both(w[m][0], w[m][1]), qf), sc);
+      for (int i = 0; i < FN * FT + kBehind; ++i) {
+        if (i % FN == 0 && i / FN + 1 < FT) load(i / FN + 1);
+        if (i < FN * FT) part[i % (kBehind + 1)] = mfma_fp8(both(w[i % FN][0], w[i % FN][1]), qf[i / FN & 1]);
+        if (kDepth == 1 && i % 4 == 2 && i / 4 < kOwn) load_own(blk + 1, i / 4);
+        if (kDepth == 1 && i >= FN * (FT - 1) && i < FN * FT) load_frag(blk + 1, i % FN, w[i % FN]);
+        if (i >= kBehind) {
+          const int b = i - kBehind;
+          if (b % FN == 0) sc[b / FN % 4] *= ws;
+          add_scaled(acc[b % FN][b / FN], part[b % (kBehind + 1)], sc[b / FN % 4]);
+          asm volatile("" : "+v"(acc[b % FN][b / FN]));  // here, not behind the next barrier
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
@@ -338,27 +385,41 @@ __global__ __launch_bounds__(64 * WN * KW) void k_fp8_tile(FP8Args a, int n_tile
   // since the barrier before.  Loads past the last block repeat it.
   load_q(0);
   load_w(0, wf[0], wsc[0]);
-  load_w(1, wf[1], wsc[1]);
-  store_q(0);
-  lds_barrier();
-  for (int blk = 0; blk < blocks; blk += 2) {
-    load_q(blk + 1);
-    stay();
-    multiply(blk, 0, wf[0], wsc[0]);
-    stay();
-    load_w(blk + 2, wf[0], wsc[0]);
-    stay();
-    store_q(1);
+  if constexpr (kDepth == 1) {
+    store_q(0);
     lds_barrier();
-    if (blk + 1 < blocks) {
-      load_q(blk + 2);
+    for (int blk = 0; blk < blocks; ++blk) {
+      wsc[1] = sp[min(first + blk + 1, steps - 1)];
       stay();
-      multiply(blk + 1, 1, wf[1], wsc[1]);
+      multiply(blk, blk & 1, wf[0], wsc[0]);
+      wsc[0] = wsc[1];
       stay();
-      load_w(blk + 3, wf[1], wsc[1]);
-      stay();
-      store_q(0);
+      store_q((blk + 1) & 1);
       lds_barrier();
+    }
+  } else {
+    load_w(1, wf[kDepth - 1], wsc[1]);
+    store_q(0);
+    lds_barrier();
+    for (int blk = 0; blk < blocks; blk += 2) {
+      load_q(blk + 1);
+      stay();
+      multiply(blk, 0, wf[0], wsc[0]);
+      stay();
+      load_w(blk + 2, wf[0], wsc[0]);
+      stay();
+      store_q(1);
+      lds_barrier();
+      if (blk + 1 < blocks) {
+        load_q(blk + 2);
+        stay();
+        multiply(blk + 1, 1, wf[kDepth - 1], wsc[1]);
+        stay();
+        load_w(blk + 3, wf[kDepth - 1], wsc[1]);
+        stay();
+        store_q(0);
+        lds_barrier();
+      }
     }
   }
 
@@ -494,8 +555,12 @@ __global__ __launch_bounds__(256) void k_fp8_pack(const void* W, const float* sc
 }
 
 // How a call is cut up: a tile of k_fp8_tile (named by its tokens), or a shape of
-// k_fp8_few.  x2, x4: groups that share a tile's k.
-enum Kind { kFew16Rows8, kFew16Rows4, kFew16Rows2, kTokens32Rows8, kTokens32Rows4, k16, k32, k32x2, k32x4, k64, k64x2, k128 };
+// k_fp8_few.  x2, x4: groups that share a tile's k.  Bf: bfloat16 results in the
+// matrix cores' own fp8.
+enum Kind {
+  kFew16Rows8, kFew16Rows4, kFew16Rows2, kTokens32Rows8, kTokens32Rows4,
+  k16, k32, k32x2, k32x4, k64, k64x2, kWide64, k64Bf, k64x2Bf, k128Bf
+};
 struct Plan {
   Kind kind;
   int rows, tokens;  // of a workgroup
@@ -503,16 +568,41 @@ struct Plan {
   int64_t token_tiles(int64_t B) const { return (B + tokens - 1) / tokens; }
   int64_t tiles(int64_t n, int64_t B) const { return row_tiles(n) * token_tiles(B); }
 };
-Plan plan_of(int64_t n, int64_t k, int64_t B) {
+// As for the int8 product the larger a tile, the seldomer W and the tokens are read
+// again, but a CU wants some eight waves with loads in flight, so a call takes the
+// largest shape whose workgroups still reach most CUs (180 of 256 count as most).
+//
+// us a call, back to back, weights of 500 MB together in turn (calls below some 8 us
+// are the host's time):
+// Up to 8 tokens: waves that share k, some 8 blocks of 64 each (1 token: 128256 x
+// 2048 37.5 with 4 waves, 40.8 and 42.5 with 2 and 8; 262144 x 1152 43.6 with 2, 44.2
+// and 56.0 with 4 and 8).  Up to 16 tokens staged in LDS where rows are many (16
+// tokens, 128256 x 2048: 47.7, with two waves on 16 rows 54.7; 8 tokens 46.3 and 42.1).
+// bfloat16 results: 256 rows x 128 tokens (4096 x 10240 x 2560 102, 2048 x 4096 x 2048
+// 21.9, with 256 x 64 23.1; 80 x 262144 x 1152 62.6 and 75.7; of two blocks of k alone,
+// 500 x 14260 x 256, 12.6 and 8.3); 256 x 64 (1000 x 4096 x 2048 14.2, with 128 x 64
+// in two groups 17.9); where those are few, groups that share the k of 128 x 64 (333 x
+// 5003 x 1152 8.8, with 256 x 64 10.1, with 128 x 32 11.9; 64 x 20000 x 4096 24.0, 33.0
+// and 30.1), down to some 100 of them (128 x 4096 x 8192 23.7, 17.4 with 64 x 32 in
+// four groups).
+// float32 results: 256 x 64, by four waves of 64 rows where many tokens fill the CUs
+// (300 x 100000 x 1024 83, by eight of 32 rows 85 and with 128 tokens 97; 1000 x 12000
+// x 2048 55.7 and 61.5; 500 x 8000 x 1024 16.8 and 13.8), by eight of 32 else (64 x
+// 151936 x 2560 87.5, by four 92.6).
+// Smaller calls as the int8 product's.
+Plan plan_of(int64_t n, int64_t k, int64_t B, bool bf16) {
   constexpr int kFull = 180;  // workgroups that about fill the 256 CUs
-  const int64_t tiles = (n + 15) / 16, steps = 2 * k_blocks(k);
+  const int64_t tiles = (n + 15) / 16, blocks = k_blocks(k), steps = 2 * blocks;
   if (B <= 16) {
-    if (tiles < 512 || (B <= 4 && steps >= 44)) return Plan{kFew16Rows8, 16, 16};
-    if (tiles < 2048 || (B <= 4 && steps >= 24)) return Plan{kFew16Rows4, 16, 16};
-    return B <= 4 ? Plan{kFew16Rows2, 32, 16} : Plan{k16, 128, 16};
+    if (tiles < 512 || (B <= 8 && steps >= 44)) return Plan{kFew16Rows8, 16, 16};
+    if (tiles < 2048 || (B <= 8 && steps >= 24)) return Plan{kFew16Rows4, 16, 16};
+    return B <= 8 ? Plan{kFew16Rows2, 32, 16} : Plan{k16, 128, 16};
   }
-  for (const Plan& p : {Plan{k128, 256, 128}, Plan{k64, 256, 64}})
-    if (2 * B > p.tokens && p.tiles(n, B) >= kFull) return p;
+  const Plan big{k128Bf, 256, 128}, mid{bf16 ? k64Bf : k64, 256, 64}, shared{k64x2Bf, 128, 64};
+  if (bf16 && B > 64 && blocks >= 4 && big.tiles(n, B) >= kFull) return big;
+  if (!bf16 && B > 64 && mid.tiles(n, B) >= 400) return Plan{kWide64, 256, 64};
+  if (B > 32 && mid.tiles(n, B) >= kFull) return mid;
+  if (bf16 && B > 32 && blocks >= 4 && shared.tiles(n, B) >= 100) return shared;
   const Plan p{k32, 128, 32};
   const int64_t t = p.tiles(n, B);
   if (t >= 2 * kFull) return steps >= 48 && B > 32 ? Plan{k64x2, 128, 64} : p;
@@ -523,6 +613,8 @@ Plan plan_of(int64_t n, int64_t k, int64_t B) {
   return narrow ? Plan{kTokens32Rows8, 16, 32} : Plan{kTokens32Rows4, 32, 32};
 }
 
+// Whether W passes the caches by: its rows are read by one workgroup alone, and
+// too many to be there still at the next call (the int8 product's measurements).
 bool past_caches(const Plan& p, int64_t n, int64_t k, int64_t B) {
   const int64_t from = (int64_t)(p.kind < k16 ? 64 : p.kind < k64 ? 128 : 256) << 20;
   return p.token_tiles(B) == 1 && w8a8_packed_bytes(n, k) > from;
@@ -555,15 +647,22 @@ void launch_kind(const FP8Args& a, Kind kind, hipStream_t st) {
     case k32: return launch_tile<2, 2, 4, 1, true, PAST, BF16, HEAD>(a, st);
     case k32x2: return launch_tile<2, 2, 4, 2, true, PAST, BF16, HEAD>(a, st);
     case k32x4: return launch_tile<2, 2, 2, 4, true, PAST, BF16, HEAD>(a, st);
-    case k64: return launch_tile<4, 2, 8, 1, !BF16, PAST, BF16, HEAD>(a, st);
-    case k64x2: return launch_tile<4, 2, 4, 2, !BF16, PAST, BF16, HEAD>(a, st);
-    case k128: return launch_tile<8, 2, 8, 1, !BF16, PAST, BF16, HEAD>(a, st);
+    case k64: return launch_tile<4, 2, 8, 1, true, PAST, BF16, HEAD>(a, st);
+    case k64x2: return launch_tile<4, 2, 4, 2, true, PAST, BF16, HEAD>(a, st);
+    case kWide64: return launch_tile<4, 4, 4, 1, true, PAST, BF16, HEAD>(a, st);
+    default: break;
+  }
+  if constexpr (BF16) switch (kind) {
+    case k64Bf: return launch_tile<4, 2, 8, 1, false, PAST, BF16, HEAD>(a, st);
+    case k64x2Bf: return launch_tile<4, 2, 4, 2, false, PAST, BF16, HEAD>(a, st);
+    case k128Bf: return launch_tile<8, 4, 4, 1, false, PAST, BF16, HEAD>(a, st);
+    default: break;
   }
 }
 
 template <bool BF16, bool HEAD>
 void launch_product(const FP8Args& a, hipStream_t st) {
-  const Plan p = plan_of(a.n, a.k, a.B);
+  const Plan p = plan_of(a.n, a.k, a.B, BF16);
   if (past_caches(p, a.n, a.k, a.B))
     launch_kind<true, BF16, HEAD>(a, p.kind, st);
   else
@@ -572,12 +671,15 @@ void launch_product(const FP8Args& a, hipStream_t st) {
 
 }  // namespace
 
-int64_t fp8_parts(int64_t n, int64_t k, int64_t B) { return plan_of(n, k, B).row_tiles(n); }
+int64_t fp8_parts(int64_t n, int64_t k, int64_t B) { return plan_of(n, k, B, false).row_tiles(n); }
 
 bool fp8_fits(int64_t n, int64_t k, int64_t B) {
   // tiles of 512 threads; the few-token kernels' grids have the tokens in y
-  const Plan p = plan_of(n, k, B);
-  return p.kind < k16 || p.tiles(n, B) < (int64_t(1) << 23);
+  for (bool bf16 : {false, true}) {
+    const Plan p = plan_of(n, k, B, bf16);
+    if (p.kind >= k16 && p.tiles(n, B) >= int64_t(1) << 23) return false;
+  }
+  return true;
 }
 
 hipError_t launch_fp8(const FP8Args& a, bool out_bf16, bool head, hipStream_t st) {
