@@ -15,19 +15,18 @@ def __getattr__(name):
                 "fh_dense_forward", "fh_get_int4", "fh_get_int8", "fh_spec_verify", "fh_profile_begin", "fh_profile_end",
                 "fh_set_path", "fh_sync_status", "fh_balanced_assign", "fh_cluster",
                 "fh_last_error", "fh_version"):
-        from . import flashhead
-        return getattr(flashhead, name)
-    if name in ("LogitRules", "W8A8Head", "rmsnorm", "logits_apply", "fh_rmsnorm", "fh_w8a8_create",
-                "fh_w8a8_create_codes", "fh_w8a8_destroy", "fh_w8a8_get", "fh_w8a8_workspace",
-                "fh_w8a8_matmul", "fh_w8a8_forward", "fh_logits_workspace", "fh_logits_apply"):
-        from . import serve
-        return getattr(serve, name)
-    if name in ("FP8Head", "rmsnorm_fp8", "fp8_quant", "fh_rmsnorm_fp8", "fh_fp8_quant", "fh_fp8_create",
-                "fh_fp8_create_codes", "fh_fp8_destroy", "fh_fp8_get", "fh_fp8_workspace", "fh_fp8_matmul",
-                "fh_fp8_forward"):
-        from . import fp8
-        return getattr(fp8, name)
-    if name in ("beam_select", "beam_reorder", "fh_beam_workspace", "fh_beam_select", "fh_beam_reorder"):
-        from . import beam
-        return getattr(beam, name)
-    raise AttributeError(name)
+        from . import flashhead as module
+    elif name in ("LogitRules", "W8A8Head", "rmsnorm", "logits_apply", "fh_rmsnorm", "fh_w8a8_create",
+                  "fh_w8a8_create_codes", "fh_w8a8_destroy", "fh_w8a8_get", "fh_w8a8_workspace",
+                  "fh_w8a8_matmul", "fh_w8a8_forward", "fh_logits_workspace", "fh_logits_apply"):
+        from . import serve as module
+    elif name in ("FP8Head", "rmsnorm_fp8", "fp8_quant", "fh_rmsnorm_fp8", "fh_fp8_quant", "fh_fp8_create",
+                  "fh_fp8_create_codes", "fh_fp8_destroy", "fh_fp8_get", "fh_fp8_workspace", "fh_fp8_matmul",
+                  "fh_fp8_forward"):
+        from . import fp8 as module
+    elif name in ("beam_select", "beam_reorder", "fh_beam_workspace", "fh_beam_select", "fh_beam_reorder"):
+        from . import beam as module
+    else:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(module, name)  # found at once from here on (0.6 us of a call)
+    return value

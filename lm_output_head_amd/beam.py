@@ -16,7 +16,7 @@ import torch
 
 from . import _abi
 from ._abi import check
-from .serve import _SHARED, _device, _on, _ptr, _rows, _size, _stream, _vector, _workspace_arg
+from .serve import _device, _on, _ptr, _rows, _size, _stream, _vector, _workspace_arg
 
 
 def _beams(t, dtype, shape, name):
@@ -84,39 +84,40 @@ def beam_select(logits, scores, *, keep=None, ids=None, v=None, lse=None, finish
         v = n
     if keep is None:
         keep = W
-    dev = _device(logits, ids, lse, scores, finished)
+    if keep < 1:
+        raise ValueError("keep must be at least 1")
+    dev = _device(logits, ids, scores, lse, finished)
     lib = _abi.load()
     with _on(dev, stream):
         size = _size(lib.fh_beam_workspace(S, W, n))
-        words, each = size // 4, S * max(keep, 0)
-        if size <= _SHARED:  # one allocation for all, where what outlives the call is small
-            ws, score, out = logits.new_empty(words + 4 * each).split_with_sizes((words, each, 3 * each))
-        else:
-            score, out = logits.new_empty(4 * each).split_with_sizes((each, 3 * each))
-            ws = logits.new_empty(words)
-        score = score.view(S, -1) if each else score
-        token, parent, done = out.view(torch.int32).view(3, S, -1).unbind(0) if each else (out, out, out)
+        out = logits.new_empty((3 if finished is None else 4, S, keep))
+        score, token, parent, *done = out.unbind(0)
+        token, parent = token.view(torch.int32), parent.view(torch.int32)
         got = {"score": score, "token": token, "parent": parent}
-        if finished is not None:
-            got["finished"] = done
+        if done:
+            got["finished"] = done = done[0].view(torch.int32)
+        ws = logits.new_empty(size // 4)
+        at = out.data_ptr()
+        step = 4 * S * keep
         check(lib.fh_beam_select(logits.data_ptr(), ld_z, _ptr(ids), ld_ids, S, W, n, v, _ptr(lse), scores.data_ptr(),
-                                 _ptr(finished), eos, keep, score.data_ptr(), token.data_ptr(), parent.data_ptr(),
-                                 done.data_ptr() if finished is not None else None, ws.data_ptr(), size, _stream(dev)))
+                                 _ptr(finished), eos, keep, at, at + step, at + 2 * step,
+                                 None if finished is None else at + 3 * step, ws.data_ptr(), size, _stream(dev)))
     return got
 
 
 def fh_beam_reorder(states, layout, parent, lengths=None, stream=None) -> None:
-    """Rows of states (tensors of one layout, a dict of fh_beam_layout's fields in
-    bytes) permuted in place by parent [S x W]."""
+    """Rows of states (tensors of one layout, fh_beam_layout's fields in bytes as a
+    sequence) permuted in place by parent [S x W]."""
     S, W = parent.shape
     _beams(parent, torch.int32, (S, W), "parent")
     if lengths is not None:
         _vector(lengths, torch.int32, S * W, "lengths")
     dev = _device(parent, lengths, *states)
-    pointers = (ctypes.c_void_p * len(states))(*[t.data_ptr() for t in states])
+    n = len(states)
     with _on(dev, stream):
-        check(_abi.load().fh_beam_reorder(pointers, len(states), ctypes.byref(_abi.FhBeamLayout(**layout)), S, W,
-                                          parent.data_ptr(), _ptr(lengths), _stream(dev)))
+        check(_abi.load().fh_beam_reorder((ctypes.c_void_p * n)(*[t.data_ptr() for t in states]), n,
+                                          _abi.FhBeamLayout(*layout), S, W, parent.data_ptr(), _ptr(lengths),
+                                          _stream(dev)))
 
 
 def _joined(shape, strides):
@@ -180,7 +181,7 @@ def beam_reorder(states, parent, *, dim=0, lengths=None, length_dim=None, stream
         layout = _layout(t, rows, dim, length_dim)
         if t.numel():
             groups.setdefault(layout, []).append(t)
-    _device(parent, lengths, *states)
-    names = [name for name, _ in _abi.FhBeamLayout._fields_]
+    if len(groups) != 1:  # a call checks its own
+        _device(parent, lengths, *states)
     for layout, same in groups.items():
-        fh_beam_reorder(same, dict(zip(names, layout)), parent, lengths, stream)
+        fh_beam_reorder(same, layout, parent, lengths, stream)

@@ -27,6 +27,8 @@ constexpr int kMaxBeams = 64, kMaxKeep = 64;
 typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef float f32x4a __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 
 // Four logits of a row from place i and their tokens, -inf where there is none.
 __device__ __forceinline__ void load_logits(const BeamArgs& a, const float* z, const int32_t* ids, int i, float (&v)[4],
@@ -111,11 +113,14 @@ __device__ __forceinline__ void exchange(Cand& c, int m, bool keep_better) {
 
 // A wave's 64 candidates, best first (bitonic); and two such lists' best 64.
 __device__ __forceinline__ void sort64(Cand& c, int lane) {
+#pragma unroll 1
   for (int size = 2; size <= 64; size <<= 1)
+#pragma unroll 1
     for (int m = size >> 1; m > 0; m >>= 1) exchange(c, m, ((lane & m) == 0) == ((lane & size) == 0 || size == 64));
 }
 __device__ __forceinline__ void merge64(Cand& c, const Cand& reversed, int lane) {
   if (beats(reversed, c)) c = reversed;
+#pragma unroll 1
   for (int m = 32; m > 0; m >>= 1) exchange(c, m, (lane & m) == 0);
 }
 __device__ __forceinline__ Cand reverse64(const Cand& c) { return lane_xor(c, 63); }
@@ -128,16 +133,18 @@ __device__ __forceinline__ int bin_of(double best, double t) {
   return min(max((int)(__float_as_uint(d) >> 20) - 967, 0), kBins - 1);
 }
 
-// A workgroup per sequence, a wave per row of it.  ROWS: rows of a wave, each of at
-// most 256 QUADS chunks, whose largest logits stay in registers; 0: they are read
-// again wherever they are looked at.
+// A workgroup per sequence.  SPLIT waves share a row and ROWS rows a wave; of rows of
+// at most 1024 chunks their largest logits stay in registers.  ROWS = 0: a wave per
+// row, which reads them again wherever it looks at them.
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kMaxChunks = 512, kMaxCands = 1024, kAllChunks = 64;
-constexpr int kQuads = 4;
-static_assert(kMaxCands == kWaves * 64, "every wave's list has a place");
+constexpr int kQuads = 4;  // four chunks each, of a lane of a wave that has a row to itself
+static_assert(kMaxCands == kWaves * 64 && kThreads == 1 << 10, "every wave's list has a place");
 
 struct BeamShared {
   double score[kMaxBeams], lse[kMaxBeams], best[kMaxBeams];
+  double part_sum[kWaves];
+  float part_top[kWaves];
   int32_t done[kMaxBeams];
   Cand cand[kMaxCands];
   int32_t token[kMaxCands];
@@ -172,11 +179,34 @@ __device__ __forceinline__ double wave_sum_d(double x) {
   return (readlane_d(x, 0) + readlane_d(x, 16)) + (readlane_d(x, 32) + readlane_d(x, 48));
 }
 
-template <int ROWS>
+// ln s of a sum s >= 0 (-inf of 0, NaN of NaN) to some 1e-14: s = f 2^e with f in
+// [0.7, 1.42), ln f = 2 artanh((f - 1) / (f + 1)) by its series.
+__device__ __forceinline__ double log_of(double s) {
+  if (!(s > 0.) || s == INFINITY) return s == 0. ? -INFINITY : s;
+  const int64_t b = __builtin_bit_cast(int64_t, s);
+  const int64_t up = (b >> 51) & 1;  // f >= 1.5 is halved
+  const double f = __builtin_bit_cast(double, (b & 0x000FFFFFFFFFFFFFll) | (1023 - up) << 52);
+  const double u = (f - 1.) / (f + 1.), v = u * u;
+  double p = 1. / 19.;
+#pragma unroll
+  for (int k = 17; k > 0; k -= 2) p = fma(p, v, 1. / k);
+  return fma((double)((b >> 52) - 1023 + up), 0.693147180559945309417, 2. * u * p);
+}
+
+// Places on a list for the lanes that are set in m, in one addition.
+__device__ __forceinline__ int take(int* length, uint64_t m, int lane) {
+  int first = 0;
+  if (lane == 0) first = atomicAdd(length, __popcll(m));
+  return __builtin_amdgcn_readfirstlane(first) + __popcll(m & ((1ull << lane) - 1));
+}
+
+template <int ROWS, int SPLIT>
 __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks) {
-  constexpr int kRows = ROWS > 0 ? ROWS : 1;
+  static_assert(ROWS <= 1 || SPLIT == 1, "waves share rows, or rows a wave");
+  constexpr int kRows = ROWS > 0 ? ROWS : 1, kOwn = kQuads / SPLIT, kTeams = kWaves / SPLIT;
   __shared__ BeamShared sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int team = wave / SPLIT, member = wave % SPLIT;
   const int64_t s = blockIdx.x, row0 = s * a.beams;
   const int W = a.beams, M = a.keep, all = W * chunks, quads = chunks / 4;
 
@@ -186,38 +216,36 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
   auto load_top = [&](int w, int i) {
     return *reinterpret_cast<const f32x4a*>(a.top + (row0 + w) * chunks + 4 * i);
   };
+  auto place_of = [&](int q) { return lane + 64 * (member + SPLIT * q); };
   const f32x4a none{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   // the beams' scores, and everything that the scan has left of them, on its way
   // together
   float score[kRows];
   int32_t fin[kRows];
-  f32x4a top[kRows][kQuads];
-  float sum[kRows][kQuads];
+  f32x4a top[kRows][kOwn];
+  float sum[kRows][kOwn];
   if constexpr (ROWS > 0) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int w = wave + r * kWaves;
+      const int w = team + r * kTeams;
       if (w >= W) break;
       score[r] = a.scores[row0 + w];
       fin[r] = a.finished ? a.finished[row0 + w] : 0;
 #pragma unroll
-      for (int q = 0; q < kQuads; ++q) {
-        const int i = lane + 64 * q;
+      for (int q = 0; q < kOwn; ++q) {
+        const int i = place_of(q);
         top[r][q] = i < quads ? load_top(w, i) : none;
         sum[r][q] = i < quads && !a.lse ? a.sum[(row0 + w) * quads + i] : 0.f;
       }
     }
   }
-  // the rows' log-sum-exps and best totals
-  auto begin_row = [&](int w, float sc, int32_t f, auto most, auto adds) {
+  // the rows' log-sum-exps and best totals, from their largest logit m and the sum
+  // of exp(z - m)
+  auto finish_row = [&](int w, float sc, int32_t f, float m, double acc) {
     const bool done = f || !(sc > -INFINITY);
     double lse = 0., best = sc;
     if (!done) {
-      const float m = wave_max(most());
-      if (a.lse)
-        lse = a.lse[row0 + w];
-      else
-        lse = m + log(wave_sum_d(adds(m)));
+      lse = a.lse ? (double)a.lse[row0 + w] : m + log_of(acc);
       best = sc + ((double)m - lse);
     }
     if (lane == 0) {
@@ -230,104 +258,66 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
   if constexpr (ROWS > 0) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int w = wave + r * kWaves;
-      if (w >= W) break;
-      begin_row(
-          w, score[r], fin[r],
-          [&]() {
-            float m = -INFINITY;
+      const int w = team + r * kTeams;
+      if (w >= W && SPLIT == 1) break;
+      float m = -INFINITY;
+      double acc = 0.;
+      if (w < W && !fin[r]) {
 #pragma unroll
-            for (int q = 0; q < kQuads; ++q) m = fmaxf(m, most4(top[r][q]));
-            return m;
-          },
-          [&](float m) {
-            double acc = 0.;
+        for (int q = 0; q < kOwn; ++q) m = fmaxf(m, most4(top[r][q]));
+        m = wave_max(m);
 #pragma unroll
-            for (int q = 0; q < kQuads; ++q) acc += (double)(sum[r][q] * exp_from(most4(top[r][q]), m));
-            return acc;
-          });
+        for (int q = 0; q < kOwn; ++q) acc += (double)(sum[r][q] * exp_from(most4(top[r][q]), m));
+        acc = wave_sum_d(acc);
+      }
+      if constexpr (SPLIT > 1) {
+        if (lane == 0) {
+          sh.part_top[wave] = m;
+          sh.part_sum[wave] = acc;
+        }
+        __syncthreads();
+        if (member == 0 && w < W) {
+          m = sh.part_top[wave];
+#pragma unroll
+          for (int i = 1; i < SPLIT; ++i) m = fmaxf(m, sh.part_top[wave + i]);
+          acc = 0.;
+#pragma unroll
+          for (int i = 0; i < SPLIT; ++i) acc += sh.part_sum[wave + i] * (double)exp_from(sh.part_top[wave + i], m);
+        }
+      }
+      if (member == 0 && w < W) finish_row(w, score[r], fin[r], m, acc);
     }
   } else {
-    for (int w = wave; w < W; w += kWaves)
-      begin_row(
-          w, a.scores[row0 + w], a.finished ? a.finished[row0 + w] : 0,
-          [&]() {
-            float m = -INFINITY;
-            for (int i = lane; i < quads; i += 64) m = fmaxf(m, most4(load_top(w, i)));
-            return m;
-          },
-          [&](float m) {
-            double acc = 0.;
-            for (int i = lane; i < quads; i += 64)
-              acc += (double)(a.sum[(row0 + w) * quads + i] * exp_from(most4(load_top(w, i)), m));
-            return acc;
-          });
+    for (int w = wave; w < W; w += kWaves) {
+      const int32_t f = a.finished ? a.finished[row0 + w] : 0;
+      float m = -INFINITY;
+      double acc = 0.;
+      if (!f) {
+        for (int i = lane; i < quads; i += 64) m = fmaxf(m, most4(load_top(w, i)));
+        m = wave_max(m);
+        if (!a.lse)
+          for (int i = lane; i < quads; i += 64)
+            acc += (double)(a.sum[(row0 + w) * quads + i] * exp_from(most4(load_top(w, i)), m));
+        acc = wave_sum_d(acc);
+      }
+      finish_row(w, a.scores[row0 + w], f, m, acc);
+    }
   }
   __syncthreads();
   double best = -INFINITY;
   for (int w = 0; w < W; ++w) best = sh.best[w] > best ? sh.best[w] : best;  // NaN is no total
 
   auto total = [&](int w, float z) { return sh.score[w] + ((double)z - sh.lse[w]); };
-  // every chunk: f(chunk, its largest total)
-  auto each_chunk = [&](auto f) {
-    auto four = [&](int w, double sc, double lse, int i, const f32x4a& x) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f(w * chunks + 4 * i + e, sc + ((double)x[e] - lse));
-    };
-    if constexpr (ROWS > 0) {
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        const int w = wave + r * kWaves;
-        if (w >= W) break;
-        if (sh.done[w]) continue;
-        const double sc = sh.score[w], lse = sh.lse[w];
-#pragma unroll
-        for (int q = 0; q < kQuads; ++q)
-          if (lane + 64 * q < quads) four(w, sc, lse, lane + 64 * q, top[r][q]);
-      }
-    } else {
-      for (int w = wave; w < W; w += kWaves) {
-        if (sh.done[w]) continue;
-        const double sc = sh.score[w], lse = sh.lse[w];
-        for (int i = lane; i < quads; i += 64) four(w, sc, lse, i, load_top(w, i));
-      }
-    }
+  auto count = [&](int bin) {
+    if (bin < kBins) atomicAdd(&sh.hist[bin], 1);
   };
-  // the listed chunks' places, a wave per chunk and two at a time, and the finished
-  // beams: f(total, beam << 32 | place, token)
-  auto each_place = [&](int listed, bool every, auto f) {
-    for (int i0 = wave; i0 < listed; i0 += 2 * kWaves) {
-      float z[2][4];
-      int32_t id[2][4];
-      int w[2], place[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int i = i0 + u * kWaves, at = i < listed ? every ? i : sh.list[i] : 0;
-        w[u] = at / chunks;
-        place[u] = at % chunks * kChunk + 4 * lane;
-        if (i < listed && !sh.done[w[u]]) {
-          load_logits(a, a.z + (row0 + w[u]) * a.ld_z, a.ids ? a.ids + (row0 + w[u]) * a.ld_ids : nullptr, place[u], z[u],
-                      id[u]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) z[u][e] = -INFINITY;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f(total(w[u], z[u][e]), (int64_t)w[u] << 32 | (place[u] + e), id[u][e]);
-    }
-    if (tid < W && sh.done[tid]) f(sh.score[tid], (int64_t)tid << 32, a.eos);
-  };
-  auto count = [&](double t) {
-    if (t > -INFINITY) atomicAdd(&sh.hist[bin_of(best, t)], 1);
-  };
+  auto bin_at = [&](double t) { return t > -INFINITY ? bin_of(best, t) : kBins; };
   // the first bin that, with those before it, holds `keep` totals
   auto find_border = [&]() {
     __syncthreads();
     if (wave == 0) {
       int border = kBins - 1, before = 0;
+#pragma unroll 1
       for (int b = 0; b < kBins; b += 64) {
         const int upto = before + wave_inclusive_scan(sh.hist[b + lane], lane);
         const uint64_t hit = __ballot(upto >= M);
@@ -342,34 +332,143 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
     __syncthreads();
     return sh.border;
   };
+  // the listed chunks' places, a wave per chunk and two at a time, and the finished
+  // beams: f(which lanes' eight and what they are), what they are being given by the
+  // bit's number
+  auto each_place = [&](int listed, bool every, auto f) {
+#pragma unroll 1
+    for (int i0 = wave; i0 < listed; i0 += 2 * kWaves) {
+      // as vectors: a choice between elements of an array would send it to memory
+      f32x8 z;
+      i32x8 id;
+      auto load = [&](int i, int* w, int* place, auto half) {
+        constexpr int H = decltype(half)::value;
+        const int at = i < listed ? every ? i : sh.list[i] : 0;
+        *w = at / chunks;
+        *place = at % chunks * kChunk + 4 * lane;
+        float v[4];
+        int32_t k[4];
+        if (i < listed && !sh.done[*w]) {
+          load_logits(a, a.z + (row0 + *w) * a.ld_z, a.ids ? a.ids + (row0 + *w) * a.ld_ids : nullptr, *place, v, k);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = -INFINITY, k[e] = 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[4 * H + e] = v[e], id[4 * H + e] = k[e];
+      };
+      int w0, w1, place0, place1;
+      load(i0, &w0, &place0, std::integral_constant<int, 0>());
+      load(i0 + kWaves, &w1, &place1, std::integral_constant<int, 1>());
+      int bin[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) bin[b] = bin_at(total(b < 4 ? w0 : w1, z[b]));
+      f(bin, [&](int b, double* t, int64_t* at, int32_t* token) {
+        float x = z[0];
+        int32_t k = id[0];
+#pragma unroll
+        for (int c = 1; c < 8; ++c) {
+          x = b == c ? z[c] : x;
+          k = b == c ? id[c] : k;
+        }
+        const int row = b < 4 ? w0 : w1;
+        *t = total(row, x);
+        *at = (int64_t)row << 32 | ((b < 4 ? place0 : place1) + (b & 3));
+        *token = k;
+      });
+    }
+    if (wave == 0) {
+      const bool mine = lane < W && sh.done[lane];
+      int bin[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) bin[b] = b == 0 && mine ? bin_at(sh.score[lane]) : kBins;
+      f(bin, [&](int, double* t, int64_t* at, int32_t* token) {
+        *t = sh.score[lane < W ? lane : 0];
+        *at = (int64_t)lane << 32;
+        *token = a.eos;
+      });
+    }
+  };
 
   const bool every = all <= kAllChunks;
   int border, listed = all;
   if (every) {
-    each_place(all, true, [&](double t, int64_t, int32_t) { count(t); });
+    each_place(all, true, [&](const int (&bin)[8], auto) {
+#pragma unroll
+      for (int b = 0; b < 8; ++b) count(bin[b]);
+    });
     border = find_border();
   } else {
-    each_chunk([&](int, double t) { count(t); });
-    if (tid < W && sh.done[tid]) count(sh.score[tid]);
-    border = find_border();
-    each_chunk([&](int at, double t) {
-      if (t > -INFINITY && bin_of(best, t) <= border) {
-        const int i = atomicAdd(&sh.chunks, 1);
-        if (i < kMaxChunks) sh.list[i] = at;
+    if (wave == 0 && lane < W && sh.done[lane]) count(bin_at(sh.score[lane]));
+    auto list = [&](uint32_t hits, auto chunk_of) {
+      for (uint64_t m; (m = __ballot(hits != 0)); hits &= hits - 1) {
+        const int i = take(&sh.chunks, m, lane);
+        if (hits && i < kMaxChunks) sh.list[i] = chunk_of(__ffs(hits) - 1);
       }
-    });
+    };
+    if constexpr (ROWS > 0) {
+      constexpr int kMine = kRows * kOwn * 4;
+      static_assert(kMine <= 32, "a bit per chunk of a lane");
+      int bin[kMine];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const int w = team + r * kTeams;
+        const bool use = w < W && !sh.done[w];
+        const double sc = use ? sh.score[w] : 0., lse = use ? sh.lse[w] : 0.;
+#pragma unroll
+        for (int q = 0; q < kOwn; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            int& b = bin[(r * kOwn + q) * 4 + e];
+            b = use && place_of(q) < quads ? bin_at(sc + ((double)top[r][q][e] - lse)) : kBins;
+            count(b);
+          }
+      }
+      border = find_border();
+      uint32_t hits = 0;
+#pragma unroll
+      for (int b = 0; b < kMine; ++b) hits |= (uint32_t)(bin[b] <= border) << b;
+      list(hits, [&](int b) {
+        return (team + b / (4 * kOwn) * kTeams) * chunks + 4 * place_of(b / 4 % kOwn) + (b & 3);
+      });
+    } else {
+      auto each_quad = [&](auto f) {
+        for (int w = wave; w < W; w += kWaves) {
+          if (sh.done[w]) continue;
+          for (int i0 = 0; i0 < quads; i0 += 64) {
+            const int i = i0 + lane;
+            const f32x4a x = i < quads ? load_top(w, i) : none;
+            int bin[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bin[e] = bin_at(total(w, x[e]));
+            f(w * chunks + 4 * i, bin);
+          }
+        }
+      };
+      each_quad([&](int, const int (&bin)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) count(bin[e]);
+      });
+      border = find_border();
+      each_quad([&](int at, const int (&bin)[4]) {
+        uint32_t hits = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) hits |= (uint32_t)(bin[e] <= border) << e;
+        list(hits, [&](int b) { return at + b; });
+      });
+    }
     __syncthreads();
     listed = sh.chunks;
   }
   int cands = kMaxCands + 1;
   if (every || listed <= kMaxChunks) {
-    each_place(listed, every, [&](double t, int64_t at, int32_t token) {
-      if (t > -INFINITY && bin_of(best, t) <= border) {
-        const int i = atomicAdd(&sh.cands, 1);
-        if (i < kMaxCands) {
-          sh.cand[i] = Cand{t, at};
-          sh.token[i] = token;
-        }
+    each_place(listed, every, [&](const int (&bin)[8], auto what) {
+      uint32_t hits = 0;
+#pragma unroll
+      for (int b = 0; b < 8; ++b) hits |= (uint32_t)(bin[b] <= border) << b;
+      for (uint64_t m; (m = __ballot(hits != 0)); hits &= hits - 1) {
+        const int i = take(&sh.cands, m, lane);
+        if (hits && i < kMaxCands) what(__ffs(hits) - 1, &sh.cand[i].t, &sh.cand[i].at, &sh.token[i]);
       }
     });
     __syncthreads();
@@ -385,15 +484,15 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
   };
   if (cands <= kMaxCands) {
     // each candidate's place among them, counted by a group of threads
-    int per = kThreads;  // threads of a candidate
-    while (per * cands > kThreads) per >>= 1;
-    const int i = tid / per;
+    int bits = 10;  // threads of a candidate, of all 2^10
+    while (cands << bits > kThreads) --bits;
+    const int i = tid >> bits;
     if (tid < cands) sh.rank[tid] = 0;
     __syncthreads();
     if (i < cands) {
       const Cand mine = sh.cand[i];
       int above = 0;
-      for (int j = tid % per; j < cands; j += per) above += beats(sh.cand[j], mine);
+      for (int j = tid & ((1 << bits) - 1); j < cands; j += 1 << bits) above += beats(sh.cand[j], mine);
       if (above) atomicAdd(&sh.rank[i], above);
     }
     __syncthreads();
@@ -591,9 +690,12 @@ hipError_t launch_beam_select(const BeamArgs& a, int64_t sequences, hipStream_t 
   const int chunks = (int)beam_chunks(a.n);
   hipLaunchKernelGGL(k_beam_scan, dim3((unsigned)((chunks + 15) / 16), (unsigned)(sequences * a.beams)), dim3(256), 0, st,
                      a, chunks);
-  void (*choose)(BeamArgs, int) = chunks > 256 * kQuads || a.beams > 2 * kWaves ? k_beam_choose<0>
-                                  : a.beams > kWaves                              ? k_beam_choose<2>
-                                                                                  : k_beam_choose<1>;
+  const int W = a.beams;
+  void (*choose)(BeamArgs, int) = chunks > 256 * kQuads || W > 32 ? k_beam_choose<0, 1>
+                                  : W > 16                       ? k_beam_choose<2, 1>
+                                  : W > 8                        ? k_beam_choose<1, 1>
+                                  : W > 4                        ? k_beam_choose<1, 2>
+                                                                 : k_beam_choose<1, 4>;
   hipLaunchKernelGGL(choose, dim3((unsigned)sequences), dim3(kThreads), 0, st, a, chunks);
   return hipGetLastError();
 }
