@@ -63,14 +63,16 @@ __device__ __forceinline__ void load_logits(const BeamArgs& a, const float* z, c
 __global__ __launch_bounds__(256) void k_beam_scan(BeamArgs a, int chunks) {
   const int lane = threadIdx.x & 63, part = (int)blockIdx.x * 4 + (int)(threadIdx.x >> 6);
   const int64_t row = blockIdx.y;
-  // a beam that is finished or has no total yet offers none of its logits
-  if (part * 4 >= chunks || (a.finished && a.finished[row]) || !(a.scores[row] > -INFINITY)) return;
+  // a finished beam offers none of its logits
+  if (part * 4 >= chunks || (a.finished && a.finished[row])) return;
   const float* z = a.z + row * a.ld_z;
   const int32_t* ids = a.ids ? a.ids + row * a.ld_ids : nullptr;
   float v[4][4], top[4];
   int32_t id[4][4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) load_logits(a, z, ids, part * kPart + c * kChunk + 4 * lane, v[c], id[c]);
+  // nor does one without a total yet, whose logits do not wait for that
+  if (!(a.scores[row] > -INFINITY)) return;
 #pragma unroll
   for (int c = 0; c < 4; ++c) top[c] = wave_max(fmaxf(fmaxf(v[c][0], v[c][1]), fmaxf(v[c][2], v[c][3])));
   float sum = 0.f;

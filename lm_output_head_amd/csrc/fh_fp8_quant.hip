@@ -61,8 +61,8 @@ __device__ __forceinline__ void store_fp8(const FP8QuantArgs& a, int64_t b, int6
 
 // W waves (or, W = 1, L of a wave's lanes) per row, C chunks per lane: the row
 // stays in registers between its one read and the writes.  A workgroup is
-// max(4, W) waves.
-template <typename T, int L, int W, int C>
+// max(4, W) waves.  PAST: out and out_residual pass the caches by.
+template <typename T, int L, int W, int C, bool PAST>
 __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void k_rmsnorm_fp8(FP8QuantArgs a, int64_t B) {
   static_assert(W == 1 || L == 64, "waves that share a row do so with all lanes");
   constexpr int N = Elems<T>::N, kRows = W == 1 ? 256 / L : 1, kLanes = L * W;
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void k_rmsnorm_fp8(FP8QuantA
   if (a.out_residual) {
     T* o = static_cast<T*>(a.out_residual) + b * a.ld_out_residual;
 #pragma unroll
-    for (int c = 0; c < C; ++c) store_chunk<T>(o, (int64_t)N * (lane + kLanes * c), d, y[c]);
+    for (int c = 0; c < C; ++c) store_chunk<T, PAST>(o, (int64_t)N * (lane + kLanes * c), d, y[c]);
   }
   float ss = 0.f;
 #pragma unroll
@@ -109,7 +109,7 @@ __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void k_rmsnorm_fp8(FP8QuantA
       y[c][i] *= inv;
       if (w) y[c][i] *= a.offset + v[i];
     }
-    if (a.out) store_chunk<T>(static_cast<T*>(a.out) + b * a.ld_out, at, d, y[c]);
+    if (a.out) store_chunk<T, PAST>(static_cast<T*>(a.out) + b * a.ld_out, at, d, y[c]);
     store_fp8<T, L>(a, b, at, y[c]);
   }
 }
@@ -174,10 +174,10 @@ __global__ __launch_bounds__(256) void k_fp8_quant(FP8QuantArgs a, int64_t group
 
 // Chunks per lane that rows of these lanes and waves come to.
 template <int L, int W>
-constexpr int kMost = L < 64 ? 1 : W == 1 ? 3 : W == 16 ? 6 : 2;
+constexpr int kMost = L < 64 ? 1 : W == 1 ? 6 : W == 16 ? 6 : 2;
 
 template <typename T, int L, int W>
-bool launch_w(const FP8QuantArgs& a, int64_t B, hipStream_t st) {
+bool launch_w(const FP8QuantArgs& a, int64_t B, bool past, hipStream_t st) {
   const int64_t chunks = (a.d + Elems<T>::N - 1) / Elems<T>::N, c = (chunks + L * W - 1) / (L * W);
   const int64_t rows = W == 1 ? 256 / L : 1, groups = (B + rows - 1) / rows;
   const dim3 grid((unsigned)groups), block(W <= 4 ? 256 : 64 * W);
@@ -186,7 +186,12 @@ bool launch_w(const FP8QuantArgs& a, int64_t B, hipStream_t st) {
 #define FH_CASE(CC)                                                                     \
   case CC:                                                                              \
     if constexpr (CC <= kMost<L, W>) {                                                  \
-      hipLaunchKernelGGL((k_rmsnorm_fp8<T, L, W, CC>), grid, block, 0, st, a, B);       \
+      if constexpr (sizeof(T) == 2 && L == 64)                                          \
+        if (past) {                                                                     \
+          hipLaunchKernelGGL((k_rmsnorm_fp8<T, L, W, CC, true>), grid, block, 0, st, a, B); \
+          return true;                                                                  \
+        }                                                                               \
+      hipLaunchKernelGGL((k_rmsnorm_fp8<T, L, W, CC, false>), grid, block, 0, st, a, B); \
       return true;                                                                      \
     }                                                                                   \
     return false;
@@ -196,17 +201,23 @@ bool launch_w(const FP8QuantArgs& a, int64_t B, hipStream_t st) {
   }
 }
 
-// Lanes and waves per row, by its chunks of 16 bytes: the int8 norm's rule.
+// Lanes and waves per row, by its chunks of 16 bytes: the int8 norm's rule, but
+// that many rows take a wave each up to six chunks a lane, as nothing waits for
+// other waves behind the sum (us a call: 16384 x 2560 bfloat16 with a residual 62.2,
+// in four waves 64.9; 4000 x 1152 float32 9.6 and 11.1; 8192 x 4096 in eight chunks
+// 74, in four waves 52).  bfloat16 outputs of more than 64 MB pass the caches by (62.2
+// -> 60.3; float32 ones lose, 3000 x 6000 50.0 -> 51.1).
 template <typename T>
 void launch_norm(const FP8QuantArgs& a, int64_t B, hipStream_t st) {
+  const bool past = B * a.d * (int64_t)sizeof(T) > int64_t(64) << 20;
   const int64_t chunks = (a.d + Elems<T>::N - 1) / Elems<T>::N;
-  const bool done = chunks <= 8                      ? launch_w<T, 8, 1>(a, B, st)
-                    : chunks <= 16                   ? launch_w<T, 16, 1>(a, B, st)
-                    : chunks <= 32                   ? launch_w<T, 32, 1>(a, B, st)
-                    : chunks <= (B < 2048 ? 64 : 192) ? launch_w<T, 64, 1>(a, B, st)
-                    : chunks <= (B < 1024 ? 256 : 384) ? launch_w<T, 64, 4>(a, B, st)
-                    : chunks <= (B < 512 ? 512 : 1024) ? launch_w<T, 64, 8>(a, B, st)
-                                                     : launch_w<T, 64, 16>(a, B, st);
+  const bool done = chunks <= 8                      ? launch_w<T, 8, 1>(a, B, past, st)
+                    : chunks <= 16                   ? launch_w<T, 16, 1>(a, B, past, st)
+                    : chunks <= 32                   ? launch_w<T, 32, 1>(a, B, past, st)
+                    : chunks <= (B < 2048 ? 64 : 384) ? launch_w<T, 64, 1>(a, B, past, st)
+                    : chunks <= (B < 1024 ? 256 : 384) ? launch_w<T, 64, 4>(a, B, past, st)
+                    : chunks <= (B < 512 ? 512 : 1024) ? launch_w<T, 64, 8>(a, B, past, st)
+                                                     : launch_w<T, 64, 16>(a, B, past, st);
   if (!done)
     hipLaunchKernelGGL((k_rmsnorm_fp8_long<T>), dim3((unsigned)std::min<int64_t>(B, 1 << 20)), dim3(1024), 0, st, a, B);
 }

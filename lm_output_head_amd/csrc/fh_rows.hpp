@@ -42,14 +42,18 @@ __device__ __forceinline__ void load_chunk(const T* p, int64_t at, int64_t d, fl
   }
 }
 
-template <typename T>
+// PAST: by the caches.
+template <typename T, bool PAST = false>
 __device__ __forceinline__ void store_chunk(T* p, int64_t at, int64_t d, const float (&v)[Elems<T>::N]) {
   constexpr int N = Elems<T>::N;
   if (at + N <= d) {
     typename Elems<T>::V x;
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = Elems<T>::put(v[i]);
-    *reinterpret_cast<typename Elems<T>::V*>(p + at) = x;
+    if constexpr (PAST)
+      __builtin_nontemporal_store(x, reinterpret_cast<typename Elems<T>::V*>(p + at));
+    else
+      *reinterpret_cast<typename Elems<T>::V*>(p + at) = x;
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)

@@ -144,8 +144,12 @@ def test_norm_sizes(dt, B, d):
     say("fp8 norm", dt, B, d)
     got = rmsnorm_fp8(x, w, residual=r, want_out=True)
     check_norm(x, r, w, 1e-6, 0.0, got)
+    # the int8 norm's sum of a row may go in another order: its out is within the same
+    # bound of y (check_norm's rel, each), s has no sum
     ref = rmsnorm(x, w, residual=r)
-    assert torch.equal(got["out"], ref["out"]) and torch.equal(got["residual"], ref["residual"])
+    assert torch.equal(got["residual"], ref["residual"])
+    rel, half = (d / 128 + 20) * U, 2.0 ** -8 if dt == torch.bfloat16 else 0.0
+    assert np.all(np.abs(f64(got["out"]) - f64(ref["out"])) <= 2.1 * (rel + half) * np.abs(f64(ref["out"])) + 1e-38)
     if dt == torch.float32:  # out is y itself
         again = fp8_quant(got["out"])
         assert np.array_equal(bits(again["q"]), bits(got["q"])) and torch.equal(again["q_scale"], got["q_scale"])
