@@ -742,7 +742,9 @@ typedef struct {
  *   lengths  device [sequences x beams] int32 or NULL (all): positions of each
  *            row that count, clamped to [0, positions].  A row takes its parent's;
  *            what lies behind them is left as it is.
- * parent and lengths must not lie in a state.  Any alignment.
+ * parent and lengths must not lie in a state, and no state is listed twice.  Any
+ * alignment.  Positions that do not follow each other directly, and their runs,
+ * are fewer than 2^31.
  */
 fh_status fh_beam_reorder(void* const* states, int64_t count, const fh_beam_layout* layout,
                           int64_t sequences, int64_t beams, const int32_t* parent,

@@ -182,7 +182,7 @@ __device__ __forceinline__ double wave_sum_d(double x) {
 }
 
 // ln s of a sum s >= 0 (-inf of 0, NaN of NaN) to some 1e-14: s = f 2^e with f in
-// [0.7, 1.42), ln f = 2 artanh((f - 1) / (f + 1)) by its series.
+// [0.75, 1.5), ln f = 2 artanh((f - 1) / (f + 1)) by its series.
 __device__ __forceinline__ double log_of(double s) {
   if (!(s > 0.) || s == INFINITY) return s == 0. ? -INFINITY : s;
   const int64_t b = __builtin_bit_cast(int64_t, s);
@@ -706,7 +706,7 @@ bool beam_reorder_fits(const BeamReorderArgs& a) {
   const int64_t most = (int64_t(1) << 31) - 1;
   const Cut c(a, column_bytes(a.beams));
   int64_t items = c.slabs;
-  if (items > most || (!c.dense && a.positions > most)) return false;
+  if (items > most || (!c.dense && (a.positions > most || a.run > most))) return false;
   for (int64_t n : {a.sequences, a.mid, a.outer, (int64_t)a.count}) {
     if (n > most / items) return false;
     items *= n;

@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <string>
 #include <utility>
+#include <vector>
 
 #include "fh_beam.hpp"
 #include "fh_serve_host.hpp"
@@ -138,6 +139,10 @@ fh_status fh_beam_reorder(void* const* states, int64_t count, const fh_beam_layo
       if (inside(parent, states[i]) || inside(lengths, states[i]))
         return fail(FH_EINVAL, "parent and lengths must not lie in a state");
     }
+    std::vector<void*> sorted(states, states + count);
+    std::sort(sorted.begin(), sorted.end());
+    if (std::adjacent_find(sorted.begin(), sorted.end()) != sorted.end())
+      return fail(FH_EINVAL, "a state is listed twice");
     fh::BeamReorderArgs a{};
     a.parent = parent;
     a.lengths = lengths;

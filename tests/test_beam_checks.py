@@ -139,6 +139,16 @@ def test_reorder_layout_refusals(lib, kw, needle):
     _refused(lib, lib.fh_beam_reorder((P * 1)(1 << 24), 1, ctypes.byref(l), 2, 3, A, None, None), needle)
 
 
+@pytest.mark.parametrize("kw", [
+    dict(run=1 << 32, positions=2, ld_position=1 << 33, mid=1, outer=1, ld_row=1 << 40),
+    dict(run=1, positions=1 << 32, ld_position=2, mid=1, outer=1, ld_row=1 << 40),
+    dict(run=1 << 50, positions=1, mid=1, outer=1, ld_row=1 << 51),
+    dict(run=4096, positions=1, mid=1 << 24, outer=1 << 10, ld_mid=4096, ld_row=1 << 36, ld_outer=1 << 40)])
+def test_states_too_large_for_one_call(lib, kw):
+    l = _abi.FhBeamLayout(**dict(LAYOUT, **kw))
+    _refused(lib, lib.fh_beam_reorder((P * 1)(1 << 24), 1, ctypes.byref(l), 2, 3, A, None, None), "too large for one call")
+
+
 def test_reorder_refusals(lib):
     l, st = _abi.FhBeamLayout(**LAYOUT), (P * 2)(1 << 24, 1 << 25)
     by = ctypes.byref(l)
@@ -148,7 +158,8 @@ def test_reorder_refusals(lib):
                          (((P * 2)(1 << 24, None), 2, by, 2, 3, A, None), "a state is NULL"),
                          ((st, 2, by, 2, 3, P((1 << 20) + 2), None), "aligned"),
                          ((st, 2, by, 2, 3, P((1 << 25) + 2876), None), "must not lie in a state"),
-                         ((st, 2, by, 2, 3, A, P(1 << 24)), "must not lie in a state")]:
+                         ((st, 2, by, 2, 3, A, P(1 << 24)), "must not lie in a state"),
+                         (((P * 3)(1 << 24, 1 << 25, 1 << 24), 3, by, 2, 3, A, None), "listed twice")]:
         _refused(lib, lib.fh_beam_reorder(*args, None), needle)
     # nothing to do: nothing is launched
     assert lib.fh_beam_reorder(None, 0, by, 2, 3, A, None, None) == 0

@@ -104,6 +104,23 @@ def test_equal_totals_come_in_order(S, W, n, keep):
     assert out["parent"].tolist() == [[min(r // n, W - 1) if r < W * n else -1 for r in range(keep)]] * S
 
 
+@pytest.mark.parametrize("S,W,n,keep", [(1, 8, 300000, 16), (1, 40, 9000, 64), (2, 3, 1100000, 64)])
+def test_rows_that_do_not_stay_in_registers(S, W, n, keep):
+    """More chunks than a lane holds, or more beams than waves hold: ordinary rows,
+    ascending ones, equal ones, masked ones."""
+    rng, z, scores = make(S, W, n, n)
+    say("long beams", S, W, n, keep)
+    check(z, scores, keep)
+    lse = np.full(S * W, 4.0, np.float32)
+    z[0].sort()
+    check(z, scores, keep, lse=lse)
+    z[1] = 0.5
+    check(z, scores, keep, lse=lse)
+    finished = (rng.random((S, W)) < 0.3).astype(np.int32)
+    z[2, rng.random(n) < 0.9999] = NEG
+    check(z, scores, keep, finished=finished, eos=7)
+
+
 def test_first_step_and_dead_beams():
     rng, z, scores = make(3, 5, 3000, 4)
     scores[:, 1:] = NEG
@@ -279,9 +296,25 @@ def test_reorder_views_and_layers():
         base.copy_(new)
 
 
+def test_reorder_of_interleaved_states():
+    """Keys and values as views of one cache, their bytes between each other's."""
+    from lm_output_head_amd import beam_reorder
+    S, W = 2, 4
+    p = parents(S, W, 3)
+    base = states_like((S * W, 30, 2, 3, 20), torch.bfloat16, 2)  # rows, positions, keys and values, heads, width
+    k, v = base[:, :, 0], base[:, :, 1]
+    old = raw(k), raw(v)
+    lengths = np.arange(4, 28, 3).astype(np.int32)
+    say("reorder interleaved")
+    beam_reorder([k, v], dev(p), lengths=dev(lengths), length_dim=1)
+    torch.cuda.synchronize()
+    assert np.array_equal(raw(k), beam_oracle.reorder(old[0], p, lengths, 0, 1))
+    assert np.array_equal(raw(v), beam_oracle.reorder(old[1], p, lengths, 0, 1))
+
+
 def test_reorder_of_many_states():
     """More states than one launch takes, of two layouts, in one call."""
-    from lm_output_head_amd import beam_reorder
+    from lm_output_head_amd import FlashHeadError, beam_reorder
     S, W = 3, 4
     p = parents(S, W, 1)
     xs = [states_like((S * W, 40, 6), torch.bfloat16, i) for i in range(130)] + [states_like((S * W, 40), torch.int32, 7)]
@@ -291,6 +324,8 @@ def test_reorder_of_many_states():
     beam_reorder(xs, dev(p), lengths=dev(lengths), length_dim=1)
     torch.cuda.synchronize()
     assert all(np.array_equal(raw(x), beam_oracle.reorder(o, p, lengths, 0, 1)) for x, o in zip(xs, old))
+    with pytest.raises(FlashHeadError, match="listed twice"):
+        beam_reorder([xs[0], xs[0]], dev(p))
     beam_reorder([], dev(p))
     beam_reorder([torch.empty(S * W, 0, device="cuda")], dev(p))
 
