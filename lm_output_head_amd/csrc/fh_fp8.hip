@@ -76,6 +76,9 @@ __device__ __forceinline__ void add_scaled(f32x4& acc, f32x4 part, float scale) 
 // KW waves, each a run of the blocks of k, that take their 16 FT tokens from the
 // caches and add up their sums in LDS, in one order.  A workgroup is G such
 // groups.  PAST: the rows pass the caches by.
+// One token is a read of W: 128256 x 2048 takes 37.5 us, 7.0 TB/s, so half precision
+// and its conversions cost nothing that shows; two blocks' loads go out
+// together (one at a time 1.5 us more).
 template <int FT, int FN, int KW, int G, bool PAST, bool BF16, bool HEAD>
 __global__ __launch_bounds__(64 * KW * G) void k_fp8_few(FP8Args a) {
   constexpr int kAhead = FN == 1 ? 2 : 1;  // blocks whose loads go out together
@@ -204,27 +207,37 @@ __global__ __launch_bounds__(64 * KW * G) void k_fp8_few(FP8Args a) {
 // More tokens: a workgroup of WN waves covers 16 FN WN rows by 16 FT tokens.  A
 // block of 128 of k of the tokens is staged in LDS in fragment order with its
 // scales, double buffered and loaded one block ahead; each wave's rows of W go
-// straight to registers, two blocks ahead.  KW groups of WN waves share the tile:
-// each takes a run of the blocks of k, with buffers of its own, and the first adds
-// up the sums.  HALF: in half precision, which the tokens are staged in and each
-// wave's rows of W are converted to as they are used.
+// straight to registers, one or two blocks ahead.  KW groups of WN waves share the
+// tile: each takes a run of the blocks of k, with buffers of its own, and the first
+// adds up the sums.  HALF: in half precision, which the tokens are staged in and
+// each wave's rows of W are converted to as they are used.
 //
 // 64 rows of a wave (FN = 4) halve what it reads of LDS for a product; their sums
-// take half the registers, so two waves share a SIMD.  In fp8 (128 tokens) W then
-// has room for one block alone: a row's registers are loaded again right behind
-// their last product, and the other wave covers the wait.  4096 x 10240 x 2560 in us:
-// 132 with 32 rows of eight waves; 118 with 64 of four; 109 with tokens read in
+// take half the registers, so two waves share a SIMD, and W has room for one block
+// alone: a row's registers are loaded again right behind their last use, and the
+// other wave covers the wait.
+// In fp8 (128 tokens) 4096 x 10240 x 2560 in us: 132 with 32 rows of eight waves; 118 with 64 of four; 109 with tokens read in
 // whole lines (16 rows of 64 bytes a load before) and eight neighbouring row tiles
 // of a panel at once; 102 with those loads spread over the products and sums three
 // products behind (2.1 PFLOP/s; the library's fp8 product without scales per block
 // takes 122).  Without any load it would take 82, without the multiply-adds of
 // the scales too 67: the matrix cores are busy 63% of the cycles, at 1.75 GHz.
-// In half precision 300 x 100000 x 1024 takes 83 us, 0.74 PFLOP/s.
+// In half precision (64 tokens) 300 x 100000 x 1024 takes 80 us, 0.77 PFLOP/s, and 82
+// with W's 64 rows converted at once and two blocks of them.  128 x 262144 x 1152 with
+// neither results nor draws takes 98: 86 with W from the caches, and some 5 less each
+// without the tokens' loads, the multiply-adds or the conversions; 66 with products
+// alone.  Work between each two products by hand gave nothing.
+// 32 rows of eight waves, whose next W is on its way before the products: 64 x 151936
+// x 2560 84 us, 88 with its loads behind them, the rate of a copy.
 template <int FT, int FN, int WN, int KW, bool HALF, bool PAST, bool BF16, bool HEAD>
 __global__ __launch_bounds__(64 * WN * KW) __attribute__((amdgpu_waves_per_eu(FN == 4 || WN * KW == 8 ? 2 : 1))) void k_fp8_tile(FP8Args a, int n_tiles, int q_tiles) {
   constexpr int kFrags = 2 * FT;                // 1 KB of codes each, of a token block
   constexpr int kBlock = kFrags * 64 * (HALF ? 2 : 1);
-  constexpr int kDepth = FN == 4 && !HALF ? 1 : 2;  // blocks of W in registers
+  constexpr int kDepth = FN == 4 ? 1 : 2;  // blocks of W in registers
+  // a row's next load goes out as soon as its registers are free, not behind the
+  // block's products
+  constexpr bool kEarly = FN * WN == 16;
+  static_assert(kEarly ? KW == 1 : kDepth == 2, "a block that is not multiplied loads nothing");
   static_assert(FT * 16 <= 64 * WN, "a thread of a group per token scale");
   static_assert(8 % FN == 0, "a wave's rows lie in one block of 128");
   typedef typename Out<BF16>::T T;
@@ -327,12 +340,47 @@ __global__ __launch_bounds__(64 * WN * KW) __attribute__((amdgpu_waves_per_eu(FN
   for (int m = 0; m < FN; ++m)
 #pragma unroll
     for (int t = 0; t < FT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](int blk, int buf, i32x4 (&w)[FN][2], float ws) {
+  // Block blk from buffer `buf`; where kEarly, its registers and scale are then
+  // block blk + kDepth's.
+  auto multiply = [&](int blk, int buf, i32x4 (&w)[FN][2], float& scale) {
     if (KW > 1 && first + blk >= steps) return;
-    if constexpr (HALF) {
+    const float ws = scale;
+    if constexpr (kEarly) scale = sp[min(first + blk + kDepth, steps - 1)];
+    if constexpr (HALF && FN == 4) {
+      // the tokens stay in registers, and W is converted 16 rows at a time
+      const f16x8* q = reinterpret_cast<const f16x8*>(sQ + buf * kBlock);
+      f16x8 qf[FT][4];
+      float sc[FT];
+#pragma unroll
+      for (int t = 0; t < FT; ++t) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) qf[t][h] = q[(h * FT + t) * 64 + at_half[h >> 1]];
+        sc[t] = sScale[group][buf][16 * t + col] * ws;
+      }
+#pragma unroll
+      for (int m = 0; m < FN; ++m) {
+        const Halves wh(w[m][0], w[m][1]);
+        load_frag(blk + kDepth, m, w[m]);
+        f32x4 part[FT];
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+          for (int t = 0; t < FT; ++t)
+            part[t] = mfma_half(wh.v[h], qf[t][h], h == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : part[t]);
+#pragma unroll
+        for (int t = 0; t < FT; ++t) add_scaled(acc[m][t], part[t], sc[t]);
+      }
+    } else if constexpr (HALF) {
       Halves wh[FN];
 #pragma unroll
-      for (int m = 0; m < FN; ++m) wh[m] = Halves(w[m][0], w[m][1]);
+      for (int m = 0; m < FN; ++m) {
+        wh[m] = Halves(w[m][0], w[m][1]);
+        if constexpr (kEarly) {
+          __builtin_amdgcn_sched_barrier(0);
+          load_frag(blk + kDepth, m, w[m]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
 #pragma unroll
       for (int t = 0; t < FT; ++t) {
         const float sc = sScale[group][buf][16 * t + col] * ws;
@@ -351,7 +399,7 @@ __global__ __launch_bounds__(64 * WN * KW) __attribute__((amdgpu_waves_per_eu(FN
     } else {
       // the next tokens are read while these are multiplied, and a product is added
       // up three products later; with one block of W, so are the loads for the next
-      static_assert(kDepth == 2 || (KW == 1 && 4 * kOwn <= FN * FT), "the loads fit between the products");
+      static_assert(kDepth == 2 || 4 * kOwn <= FN * FT, "the loads fit between the products");
       constexpr int kBehind = 3;
       i32x8 qf[2];
       float sc[4];  // of three tokens in use, while a fourth comes
@@ -366,7 +414,7 @@ __global__ __launch_bounds__(64 * WN * KW) __attribute__((amdgpu_waves_per_eu(FN
         if (i % FN == 0 && i / FN + 1 < FT) load(i / FN + 1);
         if (i < FN * FT) part[i % (kBehind + 1)] = mfma_fp8(both(w[i % FN][0], w[i % FN][1]), qf[i / FN & 1]);
         if (kDepth == 1 && i % 4 == 2 && i / 4 < kOwn) load_own(blk + 1, i / 4);
-        if (kDepth == 1 && i >= FN * (FT - 1) && i < FN * FT) load_frag(blk + 1, i % FN, w[i % FN]);
+        if (kEarly && i >= FN * (FT - 1) && i < FN * FT) load_frag(blk + kDepth, i % FN, w[i % FN]);
         if (i >= kBehind) {
           const int b = i - kBehind;
           if (b % FN == 0) sc[b / FN % 4] *= ws;
@@ -389,10 +437,9 @@ __global__ __launch_bounds__(64 * WN * KW) __attribute__((amdgpu_waves_per_eu(FN
     store_q(0);
     lds_barrier();
     for (int blk = 0; blk < blocks; ++blk) {
-      wsc[1] = sp[min(first + blk + 1, steps - 1)];
+      if constexpr (HALF) load_q(blk + 1);
       stay();
       multiply(blk, blk & 1, wf[0], wsc[0]);
-      wsc[0] = wsc[1];
       stay();
       store_q((blk + 1) & 1);
       lds_barrier();
@@ -406,7 +453,7 @@ __global__ __launch_bounds__(64 * WN * KW) __attribute__((amdgpu_waves_per_eu(FN
       stay();
       multiply(blk, 0, wf[0], wsc[0]);
       stay();
-      load_w(blk + 2, wf[0], wsc[0]);
+      if constexpr (!kEarly) load_w(blk + 2, wf[0], wsc[0]);
       stay();
       store_q(1);
       lds_barrier();
@@ -415,7 +462,7 @@ __global__ __launch_bounds__(64 * WN * KW) __attribute__((amdgpu_waves_per_eu(FN
         stay();
         multiply(blk + 1, 1, wf[kDepth - 1], wsc[1]);
         stay();
-        load_w(blk + 3, wf[kDepth - 1], wsc[1]);
+        if constexpr (!kEarly) load_w(blk + 3, wf[kDepth - 1], wsc[1]);
         stay();
         store_q(0);
         lds_barrier();
@@ -586,9 +633,9 @@ struct Plan {
 // and 30.1), down to some 100 of them (128 x 4096 x 8192 23.7, 17.4 with 64 x 32 in
 // four groups).
 // float32 results: 256 x 64, by four waves of 64 rows where many tokens fill the CUs
-// (300 x 100000 x 1024 83, by eight of 32 rows 85 and with 128 tokens 97; 1000 x 12000
-// x 2048 55.7 and 61.5; 500 x 8000 x 1024 16.8 and 13.8), by eight of 32 else (64 x
-// 151936 x 2560 87.5, by four 92.6).
+// (300 x 100000 x 1024 80, by eight of 32 rows 93 and with 128 tokens 97; 1000 x 12000
+// x 2048 52.9 and 59.7; 500 x 8000 x 1024 15.4 and 12.9), by eight of 32 else (64 x
+// 151936 x 2560 84, by four 89).
 // Smaller calls as the int8 product's.
 Plan plan_of(int64_t n, int64_t k, int64_t B, bool bf16) {
   constexpr int kFull = 180;  // workgroups that about fill the 256 CUs
