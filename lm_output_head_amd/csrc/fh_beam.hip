@@ -59,6 +59,32 @@ __device__ __forceinline__ void load_logits(const BeamArgs& a, const float* z, c
   }
 }
 
+// A wave's 1024 logits of a row; their chunks' largest, and the sum of exponentials
+// from the largest of all.
+__device__ __forceinline__ void load_part(const BeamArgs& a, int64_t row, int part, int lane, float (&v)[4][4]) {
+  const float* z = a.z + row * a.ld_z;
+  const int32_t* ids = a.ids ? a.ids + row * a.ld_ids : nullptr;
+  int32_t id[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) load_logits(a, z, ids, part * kPart + c * kChunk + 4 * lane, v[c], id);
+}
+__device__ __forceinline__ f32x4a reduce_part(const float (&v)[4][4], bool want_sum, float* sum) {
+  f32x4a top;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) top[c] = wave_max(fmaxf(fmaxf(v[c][0], v[c][1]), fmaxf(v[c][2], v[c][3])));
+  *sum = 0.f;
+  if (want_sum) {
+    const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    const float shift = m == -INFINITY ? 0.f : m;  // +inf leaves NaN, as a NaN does
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) *sum += __expf(v[c][e] - shift);
+    *sum = wave_sum(*sum);
+  }
+  return top;
+}
+
 // A wave per 1024 logits, all on their way before the first is used; the largest
 // come out of exchanges between lanes, the exponentials' sum in float32 (1024
 // terms of at most 1, in one order).  16 x 8 beams x 151936, of which 62 MB count,
@@ -69,28 +95,13 @@ __global__ __launch_bounds__(256) void k_beam_scan(BeamArgs a, int chunks) {
   const int64_t row = blockIdx.y;
   // a finished beam offers none of its logits
   if (part * 4 >= chunks || (a.finished && a.finished[row])) return;
-  const float* z = a.z + row * a.ld_z;
-  const int32_t* ids = a.ids ? a.ids + row * a.ld_ids : nullptr;
-  float v[4][4], top[4];
-  int32_t id[4][4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) load_logits(a, z, ids, part * kPart + c * kChunk + 4 * lane, v[c], id[c]);
+  float v[4][4], sum;
+  load_part(a, row, part, lane, v);
   // nor does one without a total yet, whose logits do not wait for that
   if (!(a.scores[row] > -INFINITY)) return;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) top[c] = wave_max(fmaxf(fmaxf(v[c][0], v[c][1]), fmaxf(v[c][2], v[c][3])));
-  float sum = 0.f;
-  if (!a.lse) {
-    const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-    const float shift = m == -INFINITY ? 0.f : m;  // +inf leaves NaN, as a NaN does
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum += __expf(v[c][e] - shift);
-    sum = wave_sum(sum);
-  }
+  const f32x4a top = reduce_part(v, !a.lse, &sum);
   if (lane == 0) {
-    *reinterpret_cast<f32x4a*>(a.top + row * chunks + part * 4) = f32x4a{top[0], top[1], top[2], top[3]};
+    *reinterpret_cast<f32x4a*>(a.top + row * chunks + part * 4) = top;
     if (!a.lse) a.sum[row * (chunks / 4) + part] = sum;
   }
 }
@@ -148,10 +159,12 @@ __device__ __forceinline__ int bin_of(double best, double t) {
 //
 // SPLIT waves share a row and ROWS rows a wave; of rows of
 // at most 1024 chunks their largest logits stay in registers.  ROWS = 0: a wave per
-// row, which reads them again wherever it looks at them.
+// row, which reads them again wherever it looks at them.  ALONE: nothing has been
+// scanned yet: its waves do that first, up to kParts parts of a row each.
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kMaxChunks = 512, kMaxCands = 1024, kAllChunks = 64;
+constexpr int kMaxChunks = 512, kMaxCands = 1024;
 constexpr int kQuads = 4;  // four chunks each, of a lane of a wave that has a row to itself
+constexpr int kParts = 2;  // of a wave that scans them itself
 static_assert(kMaxCands == kWaves * 64 && kThreads == 1 << 10, "every wave's list has a place");
 
 struct BeamShared {
@@ -192,6 +205,14 @@ __device__ __forceinline__ double wave_sum_d(double x) {
   return (readlane_d(x, 0) + readlane_d(x, 16)) + (readlane_d(x, 32) + readlane_d(x, 48));
 }
 
+__device__ __forceinline__ double wave_max_d(double x) {
+  x = fmax(x, dpp_d<0xB1>(x));
+  x = fmax(x, dpp_d<0x4E>(x));
+  x = fmax(x, dpp_d<0x141>(x));
+  x = fmax(x, dpp_d<0x140>(x));
+  return fmax(fmax(readlane_d(x, 0), readlane_d(x, 16)), fmax(readlane_d(x, 32), readlane_d(x, 48)));
+}
+
 // ln s of a sum s >= 0 (-inf of 0, NaN of NaN) to some 1e-14: s = f 2^e with f in
 // [0.75, 1.5), ln f = 2 artanh((f - 1) / (f + 1)) by its series.
 __device__ __forceinline__ double log_of(double s) {
@@ -213,10 +234,11 @@ __device__ __forceinline__ int take(int* length, uint64_t m, int lane) {
   return __builtin_amdgcn_readfirstlane(first) + __popcll(m & ((1ull << lane) - 1));
 }
 
-template <int ROWS, int SPLIT>
+template <int ROWS, int SPLIT, bool ALONE>
 __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks) {
   static_assert(ROWS <= 1 || SPLIT == 1, "waves share rows, or rows a wave");
-  constexpr int kRows = ROWS > 0 ? ROWS : 1, kOwn = kQuads / SPLIT, kTeams = kWaves / SPLIT;
+  static_assert(!ALONE || ROWS == 1, "a wave's parts are of one row");
+  constexpr int kRows = ROWS > 0 ? ROWS : 1, kOwn = ALONE ? 1 : kQuads / SPLIT, kTeams = kWaves / SPLIT;
   __shared__ BeamShared sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int team = wave / SPLIT, member = wave % SPLIT;
@@ -229,7 +251,7 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
   auto load_top = [&](int w, int i) {
     return *reinterpret_cast<const f32x4a*>(a.top + (row0 + w) * chunks + 4 * i);
   };
-  auto place_of = [&](int q) { return lane + 64 * (member + SPLIT * q); };
+  auto place_of = [&](int q) { return ALONE ? lane * SPLIT + member : lane + 64 * (member + SPLIT * q); };
   const f32x4a none{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   // the beams' scores, and everything that the scan has left of them, on its way
   // together
@@ -245,10 +267,33 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
       score[r] = a.scores[row0 + w];
       fin[r] = a.finished ? a.finished[row0 + w] : 0;
 #pragma unroll
-      for (int q = 0; q < kOwn; ++q) {
+      for (int q = 0; q < kOwn && !ALONE; ++q) {
         const int i = place_of(q);
         top[r][q] = i < quads ? load_top(w, i) : none;
         sum[r][q] = i < quads && !a.lse ? a.sum[(row0 + w) * quads + i] : 0.f;
+      }
+    }
+  }
+  if constexpr (ALONE) {
+    top[0][0] = none;
+    sum[0][0] = 0.f;
+    const bool live = team < W && !fin[0];
+    float v[kParts][4][4];
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+      if (live && member + i * SPLIT < quads) load_part(a, row0 + team, member + i * SPLIT, lane, v[i]);
+    if (live && score[0] > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) {
+        const int p = member + i * SPLIT;
+        if (p >= quads) break;
+        float total;
+        const f32x4a most = reduce_part(v[i], !a.lse, &total);
+        if (lane == i) {
+          top[0][0] = most;
+          sum[0][0] = total;
+          *reinterpret_cast<f32x4a*>(a.top + (row0 + team) * chunks + 4 * p) = most;
+        }
       }
     }
   }
@@ -317,8 +362,7 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
     }
   }
   __syncthreads();
-  double best = -INFINITY;
-  for (int w = 0; w < W; ++w) best = sh.best[w] > best ? sh.best[w] : best;  // NaN is no total
+  const double best = wave_max_d(lane < W ? sh.best[lane] : -INFINITY);  // NaN is no total
 
   auto total = [&](int w, float z) { return sh.score[w] + ((double)z - sh.lse[w]); };
   auto count = [&](int bin) {
@@ -403,7 +447,10 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
     }
   };
 
-  const bool every = all <= kAllChunks;
+  // No more chunks than `keep` would all be listed, so their places are counted at
+  // once; of more, the chunks' largest say enough (8 x 2048 candidates, keep 8, 9.9 us;
+  // counting all of the places 15.5).
+  const bool every = all <= M;
   int border, listed = all;
   if (every) {
     each_place(all, true, [&](const int (&bin)[8], auto) {
@@ -709,15 +756,24 @@ void launch_reorder(const BeamReorderArgs& a, hipStream_t st) {
 int64_t beam_chunks(int64_t n) { return (n + kPart - 1) / kPart * (kPart / kChunk); }
 
 hipError_t launch_beam_select(const BeamArgs& a, int64_t sequences, hipStream_t st) {
-  const int chunks = (int)beam_chunks(a.n);
-  hipLaunchKernelGGL(k_beam_scan, dim3((unsigned)((chunks + 15) / 16), (unsigned)(sequences * a.beams)), dim3(256), 0, st,
-                     a, chunks);
-  const int W = a.beams;
-  void (*choose)(BeamArgs, int) = chunks > 256 * kQuads || W > 32 ? k_beam_choose<0, 1>
-                                  : W > 16                       ? k_beam_choose<2, 1>
-                                  : W > 8                        ? k_beam_choose<1, 1>
-                                  : W > 4                        ? k_beam_choose<1, 2>
-                                                                 : k_beam_choose<1, 4>;
+  const int chunks = (int)beam_chunks(a.n), W = a.beams;
+  void (*choose)(BeamArgs, int);
+  // Short rows are scanned by the sequence's one workgroup.  us a call from the host
+  // and in a graph, against two launches: 4 x 4096 10.8 and 8.2, 13.5 and 9.0; 8 x 4096
+  // candidates 11.6 and 10.1, 14.2 and 9.8; with four parts a wave, 2 x 16384, 10.8 and
+  // 9.6, 13.7 and 7.9, with eight 11.9 and 11.7, 13.7 and 7.6.
+  const int split = W > 8 ? 1 : W > 4 ? 2 : 4;
+  if (W <= 16 && chunks / 4 <= kParts * split) {
+    choose = W > 8 ? k_beam_choose<1, 1, true> : W > 4 ? k_beam_choose<1, 2, true> : k_beam_choose<1, 4, true>;
+  } else {
+    hipLaunchKernelGGL(k_beam_scan, dim3((unsigned)((chunks + 15) / 16), (unsigned)(sequences * W)), dim3(256), 0, st, a,
+                       chunks);
+    choose = chunks > 256 * kQuads || W > 32 ? k_beam_choose<0, 1, false>
+             : W > 16                       ? k_beam_choose<2, 1, false>
+             : W > 8                        ? k_beam_choose<1, 1, false>
+             : W > 4                        ? k_beam_choose<1, 2, false>
+                                            : k_beam_choose<1, 4, false>;
+  }
   hipLaunchKernelGGL(choose, dim3((unsigned)sequences), dim3(kThreads), 0, st, a, chunks);
   return hipGetLastError();
 }
