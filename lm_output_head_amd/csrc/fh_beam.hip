@@ -154,7 +154,7 @@ __device__ __forceinline__ int bin_of(double best, double t) {
 // a histogram of totals leaves in question (some `keep` of them), then their places
 // in the same bins, and ranks those.  Nothing is sorted unless more than 1024 places
 // are left.  It is bound by the chain of its dependent steps and by instructions that
-// no cache holds yet, not by data: 6.2 us for one sequence of four beams of 128256, 8.7
+// no cache holds yet, not by data: 6.1 us for one sequence of four beams of 128256, 8.6
 // for sixteen of eight of 151936; 256 or 512 threads a workgroup change neither.
 //
 // SPLIT waves share a row and ROWS rows a wave; of rows of
@@ -169,8 +169,8 @@ static_assert(kMaxCands == kWaves * 64 && kThreads == 1 << 10, "every wave's lis
 
 struct BeamShared {
   double score[kMaxBeams], lse[kMaxBeams], best[kMaxBeams];
-  double part_sum[kWaves];
-  float part_top[kWaves];
+  double part_sum[kMaxBeams];  // of a row's waves, one after another
+  float part_top[kMaxBeams];
   int32_t done[kMaxBeams];
   Cand cand[kMaxCands];
   int32_t token[kMaxCands];
@@ -255,19 +255,22 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
   const f32x4a none{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   // the beams' scores, and everything that the scan has left of them, on its way
   // together
-  float score[kRows];
-  int32_t fin[kRows];
+  float beam_score = 0.f, beam_lse = 0.f;
+  int32_t beam_fin = 0;
+  if (tid < W) {
+    beam_score = a.scores[row0 + tid];
+    beam_fin = a.finished ? a.finished[row0 + tid] : 0;
+    beam_lse = a.lse ? a.lse[row0 + tid] : 0.f;
+  }
   f32x4a top[kRows][kOwn];
   float sum[kRows][kOwn];
-  if constexpr (ROWS > 0) {
+  if constexpr (ROWS > 0 && !ALONE) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int w = team + r * kTeams;
       if (w >= W) break;
-      score[r] = a.scores[row0 + w];
-      fin[r] = a.finished ? a.finished[row0 + w] : 0;
 #pragma unroll
-      for (int q = 0; q < kOwn && !ALONE; ++q) {
+      for (int q = 0; q < kOwn; ++q) {
         const int i = place_of(q);
         top[r][q] = i < quads ? load_top(w, i) : none;
         sum[r][q] = i < quads && !a.lse ? a.sum[(row0 + w) * quads + i] : 0.f;
@@ -277,12 +280,13 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
   if constexpr (ALONE) {
     top[0][0] = none;
     sum[0][0] = 0.f;
-    const bool live = team < W && !fin[0];
+    const bool live = team < W && !(a.finished && a.finished[row0 + team]);
+    const float score = team < W ? a.scores[row0 + team] : 0.f;
     float v[kParts][4][4];
 #pragma unroll
     for (int i = 0; i < kParts; ++i)
       if (live && member + i * SPLIT < quads) load_part(a, row0 + team, member + i * SPLIT, lane, v[i]);
-    if (live && score[0] > -INFINITY) {
+    if (live && score > -INFINITY) {
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
         const int p = member + i * SPLIT;
@@ -297,69 +301,62 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
       }
     }
   }
-  // the rows' log-sum-exps and best totals, from their largest logit m and the sum
-  // of exp(z - m)
-  auto finish_row = [&](int w, float sc, int32_t f, float m, double acc) {
-    const bool done = f || !(sc > -INFINITY);
-    double lse = 0., best = sc;
-    if (!done) {
-      lse = a.lse ? (double)a.lse[row0 + w] : m + log_of(acc);
-      best = sc + ((double)m - lse);
-    }
+  // the rows' largest logits m and sums of exp(z - m); what a finished row holds
+  // here is not looked at
+  auto leave = [&](int at, float m, double acc) {
     if (lane == 0) {
-      sh.score[w] = sc;
-      sh.lse[w] = lse;
-      sh.best[w] = best;
-      sh.done[w] = done;
+      sh.part_top[at] = m;
+      sh.part_sum[at] = acc;
     }
   };
   if constexpr (ROWS > 0) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int w = team + r * kTeams;
-      if (w >= W && SPLIT == 1) break;
+      if (w >= W) break;
       float m = -INFINITY;
       double acc = 0.;
-      if (w < W && !fin[r]) {
 #pragma unroll
-        for (int q = 0; q < kOwn; ++q) m = fmaxf(m, most4(top[r][q]));
-        m = wave_max(m);
+      for (int q = 0; q < kOwn; ++q) m = fmaxf(m, most4(top[r][q]));
+      m = wave_max(m);
 #pragma unroll
-        for (int q = 0; q < kOwn; ++q) acc += (double)(sum[r][q] * exp_from(most4(top[r][q]), m));
-        acc = wave_sum_d(acc);
-      }
-      if constexpr (SPLIT > 1) {
-        if (lane == 0) {
-          sh.part_top[wave] = m;
-          sh.part_sum[wave] = acc;
-        }
-        __syncthreads();
-        if (member == 0 && w < W) {
-          m = sh.part_top[wave];
-#pragma unroll
-          for (int i = 1; i < SPLIT; ++i) m = fmaxf(m, sh.part_top[wave + i]);
-          acc = 0.;
-#pragma unroll
-          for (int i = 0; i < SPLIT; ++i) acc += sh.part_sum[wave + i] * (double)exp_from(sh.part_top[wave + i], m);
-        }
-      }
-      if (member == 0 && w < W) finish_row(w, score[r], fin[r], m, acc);
+      for (int q = 0; q < kOwn; ++q) acc += (double)(sum[r][q] * exp_from(most4(top[r][q]), m));
+      leave(w * SPLIT + member, m, wave_sum_d(acc));
     }
   } else {
     for (int w = wave; w < W; w += kWaves) {
-      const int32_t f = a.finished ? a.finished[row0 + w] : 0;
       float m = -INFINITY;
       double acc = 0.;
-      if (!f) {
-        for (int i = lane; i < quads; i += 64) m = fmaxf(m, most4(load_top(w, i)));
-        m = wave_max(m);
-        if (!a.lse)
-          for (int i = lane; i < quads; i += 64)
-            acc += (double)(a.sum[(row0 + w) * quads + i] * exp_from(most4(load_top(w, i)), m));
-        acc = wave_sum_d(acc);
-      }
-      finish_row(w, a.scores[row0 + w], f, m, acc);
+      for (int i = lane; i < quads; i += 64) m = fmaxf(m, most4(load_top(w, i)));
+      m = wave_max(m);
+      if (!a.lse)
+        for (int i = lane; i < quads; i += 64)
+          acc += (double)(a.sum[(row0 + w) * quads + i] * exp_from(most4(load_top(w, i)), m));
+      leave(w, m, wave_sum_d(acc));
     }
+  }
+  __syncthreads();
+  // the log-sum-exps and best totals, a lane per row
+  if (tid < W) {
+    const bool done = beam_fin || !(beam_score > -INFINITY);
+    double lse = 0., best = beam_score;
+    if (!done) {
+      float m = sh.part_top[tid * SPLIT];
+#pragma unroll
+      for (int i = 1; i < SPLIT; ++i) m = fmaxf(m, sh.part_top[tid * SPLIT + i]);
+      double acc = sh.part_sum[tid * SPLIT];
+      if constexpr (SPLIT > 1) {
+        acc = 0.;
+#pragma unroll
+        for (int i = 0; i < SPLIT; ++i) acc += sh.part_sum[tid * SPLIT + i] * (double)exp_from(sh.part_top[tid * SPLIT + i], m);
+      }
+      lse = a.lse ? (double)beam_lse : m + log_of(acc);
+      best = beam_score + ((double)m - lse);
+    }
+    sh.score[tid] = beam_score;
+    sh.lse[tid] = lse;
+    sh.best[tid] = best;
+    sh.done[tid] = done;
   }
   __syncthreads();
   const double best = wave_max_d(lane < W ? sh.best[lane] : -INFINITY);  // NaN is no total
