@@ -157,10 +157,10 @@ __device__ __forceinline__ int bin_of(double best, double t) {
 // no cache holds yet, not by data: 6.1 us for one sequence of four beams of 128256, 8.6
 // for sixteen of eight of 151936; 256 or 512 threads a workgroup change neither.
 //
-// SPLIT waves share a row and ROWS rows a wave; of rows of
-// at most 1024 chunks their largest logits stay in registers.  ROWS = 0: a wave per
-// row, which reads them again wherever it looks at them.  ALONE: nothing has been
-// scanned yet: its waves do that first, up to kParts parts of a row each.
+// SPLIT waves share a row and ROWS rows a wave; of rows of at most 1024 chunks their
+// largest logits stay in registers.  ROWS = 0: a wave per row, which reads them again
+// wherever it looks at them.  ALONE: nothing has been scanned yet: its waves do that
+// first, up to kParts parts of a row each.
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kMaxChunks = 512, kMaxCands = 1024;
 constexpr int kQuads = 4;  // four chunks each, of a lane of a wave that has a row to itself
@@ -448,14 +448,8 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
   // once; of more, the chunks' largest say enough (8 x 2048 candidates, keep 8, 9.9 us;
   // counting all of the places 15.5).
   const bool every = all <= M;
-  int border, listed = all;
-  if (every) {
-    each_place(all, true, [&](const int (&bin)[8], auto) {
-#pragma unroll
-      for (int b = 0; b < 8; ++b) count(bin[b]);
-    });
-    border = find_border();
-  } else {
+  int border = 0, listed = all;
+  if (!every) {
     if (wave == 0 && lane < W && sh.done[lane]) count(bin_at(sh.score[lane]));
     auto list = [&](uint32_t hits, auto chunk_of) {
       for (uint64_t m; (m = __ballot(hits != 0)); hits &= hits - 1) {
@@ -518,18 +512,35 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
     listed = sh.chunks;
   }
   int cands = kMaxCands + 1;
-  if (every || listed <= kMaxChunks) {
-    each_place(listed, every, [&](const int (&bin)[8], auto what) {
-      uint32_t hits = 0;
+  if (listed <= kMaxChunks) {
+    // too many places where most of the chunks are listed (a few beams not finished,
+    // say): then by a border among the places themselves (4 x 32 beams of 1000, keep 64,
+    // 20 of each 32 finished: 26 us a call; by the sort below 105)
+    for (bool counted = every;; counted = true) {
+      if (counted) {
+        each_place(listed, every, [&](const int (&bin)[8], auto) {
 #pragma unroll
-      for (int b = 0; b < 8; ++b) hits |= (uint32_t)(bin[b] <= border) << b;
-      for (uint64_t m; (m = __ballot(hits != 0)); hits &= hits - 1) {
-        const int i = take(&sh.cands, m, lane);
-        if (hits && i < kMaxCands) what(__ffs(hits) - 1, &sh.cand[i].t, &sh.cand[i].at, &sh.token[i]);
+          for (int b = 0; b < 8; ++b) count(bin[b]);
+        });
+        border = find_border();
       }
-    });
-    __syncthreads();
-    cands = sh.cands;
+      each_place(listed, every, [&](const int (&bin)[8], auto what) {
+        uint32_t hits = 0;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) hits |= (uint32_t)(bin[b] <= border) << b;
+        for (uint64_t m; (m = __ballot(hits != 0)); hits &= hits - 1) {
+          const int i = take(&sh.cands, m, lane);
+          if (hits && i < kMaxCands) what(__ffs(hits) - 1, &sh.cand[i].t, &sh.cand[i].at, &sh.token[i]);
+        }
+      });
+      __syncthreads();
+      cands = sh.cands;
+      if (cands <= kMaxCands || counted) break;
+      __syncthreads();
+      if (tid < kBins) sh.hist[tid] = 0;
+      if (tid == 0) sh.cands = 0;
+      __syncthreads();
+    }
   }
 
   auto write = [&](int r, const Cand& c, int32_t token) {

@@ -150,6 +150,37 @@ def test_finished_beams(n, ids):
     assert out["finished"].sum() >= 6
 
 
+@pytest.mark.parametrize("S,W,n,keep,live", [(3, 32, 1000, 64, 12), (2, 16, 700, 32, 3), (1, 64, 2000, 64, 30),
+                                             (2, 4, 2000, 64, 1), (1, 10, 30000, 64, 1), (2, 32, 400, 64, 20)])
+def test_few_beams_left(S, W, n, keep, live):
+    """Not many more places of 256 than continuations: a border among the largest
+    of each leaves thousands, and one among all of them is needed."""
+    rng, z, scores = make(S, W, n, W + n)
+    finished = np.ones((S, W), np.int32)
+    for s in range(S):
+        finished[s, rng.permutation(W)[:live]] = 0
+    say("few beams left", S, W, n, keep, live)
+    check(z, scores, keep, finished=finished, eos=7)
+    check(z, scores, keep, finished=finished, eos=7, lse=rng.uniform(8, 12, S * W).astype(np.float32))
+
+
+@pytest.mark.parametrize("S,W,n", [(3, 4, 8192), (2, 4, 8193), (3, 8, 4096), (2, 8, 4097), (3, 16, 2048), (2, 16, 2049),
+                                   (3, 1, 8192), (2, 2, 1025), (1, 3, 6000), (1, 12, 1500), (1, 5, 3000)])
+@pytest.mark.parametrize("listed", [False, True])
+def test_rows_that_one_workgroup_scans(S, W, n, listed):
+    """Up to two parts of 1024 a wave, and just beyond; with dead and finished beams."""
+    rng, z, scores = make(S, W, n, W + n, 0.6)
+    z[S * W // 2] = NEG
+    finished = (rng.random((S, W)) < 0.3).astype(np.int32)
+    scores[0, W // 3] = NEG
+    kw = dict(finished=finished, eos=2)
+    if listed:
+        kw.update(ids=np.stack([rng.permutation(n + 50)[:n] for _ in range(S * W)]).astype(np.int32), v=n + 20)
+    for keep in (1, W, 2 * W):
+        say("short rows", S, W, n, listed, keep)
+        check(z, scores, keep, **kw)
+
+
 def test_candidates():
     """Listed tokens in no order, some of them no tokens, with the rows' sums over
     more than the list; a token listed twice is two continuations."""

@@ -270,7 +270,9 @@ SHAPES = [(1, 1, 1), (1, 16, 64), (3, 17, 65), (5, 130, 16), (16, 128, 128), (17
           (257, 33001, 448), (200, 4000, 320), (129, 70001, 130), (2, 33001, 320), (3, 33000, 1600),
           (1, 9001, 2900), (9, 32770, 130), (100, 6000, 1600), (128, 3200, 4200), (200, 7000, 3100), (30, 6001, 100),
           (1000, 4000, 1152), (700, 10000, 320), (1030, 5200, 640), (90, 60001, 513), (333, 5003, 1152), (500, 20000, 512),
-          (65, 26000, 520), (8, 9000, 1600), (6, 40000, 130), (33, 13000, 1030)]
+          (65, 26000, 520), (8, 9000, 1600), (6, 40000, 130), (33, 13000, 1030),
+          # one block of k
+          (129, 50001, 100), (100, 60001, 128), (64, 50000, 60)]
 
 
 @pytest.mark.parametrize("B,n,k", SHAPES)
