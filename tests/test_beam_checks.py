@@ -48,7 +48,7 @@ def test_select_by_hand():
     assert beam_oracle.select(z, [[0.0, -1.0]], 1, lse=np.zeros(2))[1].tolist() == [[1]]
 
 
-def test_the_checker_finds_mistakes():
+def test_the_oracle_finds_mistakes():
     rng = np.random.default_rng(2)
     z, scores = rng.normal(size=(6, 50)), np.sort(rng.normal(size=(2, 3)))[:, ::-1]
     s, t, p = beam_oracle.select(z, scores, 4)
