@@ -22,7 +22,7 @@ def __getattr__(name):
         from . import serve as module
     elif name in ("FP8Head", "rmsnorm_fp8", "fp8_quant", "fh_rmsnorm_fp8", "fh_fp8_quant", "fh_fp8_create",
                   "fh_fp8_create_codes", "fh_fp8_destroy", "fh_fp8_get", "fh_fp8_workspace", "fh_fp8_matmul",
-                  "fh_fp8_forward"):
+                  "fh_fp8_matmul_native", "fh_fp8_forward"):
         from . import fp8 as module
     elif name in ("beam_select", "beam_reorder", "fh_beam_workspace", "fh_beam_select", "fh_beam_reorder"):
         from . import beam as module

@@ -28,7 +28,8 @@ EXPORTS = (
     "fh_balanced_assign", "fh_cluster", "fh_rmsnorm", "fh_w8a8_create", "fh_w8a8_create_codes",
     "fh_w8a8_destroy", "fh_w8a8_get", "fh_w8a8_workspace", "fh_w8a8_matmul", "fh_w8a8_forward",
     "fh_logits_workspace", "fh_logits_apply", "fh_rmsnorm_fp8", "fh_fp8_quant", "fh_fp8_create",
-    "fh_fp8_create_codes", "fh_fp8_destroy", "fh_fp8_get", "fh_fp8_workspace", "fh_fp8_matmul", "fh_fp8_forward",
+    "fh_fp8_create_codes", "fh_fp8_destroy", "fh_fp8_get", "fh_fp8_workspace", "fh_fp8_matmul",
+    "fh_fp8_matmul_native", "fh_fp8_forward",
     "fh_beam_workspace", "fh_beam_select", "fh_beam_reorder", "fh_last_error", "fh_version",
 )
 
@@ -119,6 +120,7 @@ _SIGS = {
     "fh_fp8_get": ([_p, _p, _p, _p], _int),
     "fh_fp8_workspace": ([_p, _p, _i64, _i64, _int], _i64),
     "fh_fp8_matmul": ([_p, _p, _i64, _p, _i64, _i64, _p, _i64, _int, _p, _i64, _p], _int),
+    "fh_fp8_matmul_native": ([_p, _p, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _p], _int),
     "fh_fp8_forward": ([_p, _p, _i64, _p, _i64, _i64, _int, _f, _u64, _p, _p, _p, _p, _i64, _p,
                         _i64, _p], _int),
     "fh_beam_workspace": ([_i64, _i64, _i64], _i64),

@@ -3,16 +3,18 @@
 //   out[b, j] = sum_g (sum_{i in g} q[b, i] w[j, i]) (qs[b, g] ws[j / 128, g]),
 // and the dense head on it.
 //
-// Two instructions can do it.  The matrix cores' own fp8 product
-// (v_mfma_f32_16x16x128_f8f6f4) adds up eight neighbouring products before
-// anything is float32, and keeps of them what lies within 13 binades of the
-// largest: 1.5e-5 of normally distributed results is lost (2-norm), which bfloat16
-// results (2^-9 each) do not show and float32 ones do.  So it serves bfloat16
-// results where the matrix cores are the bound.  All else is multiplied in
-// half precision (v_mfma_f32_16x16x32_f16, at half the rate), which every code
-// converts to exactly: exact products, summed in float32 (1e-8 by the same
-// measure).  Either way the sum over one g is scaled and added to the running sum
-// in float32, a fused multiply-add per result.
+// Two instructions can do it.  Products are formed in half precision
+// (v_mfma_f32_16x16x32_f16), which every code converts to exactly: exact products,
+// summed in float32 (1e-8 of normally distributed results, 2-norm).  The matrix
+// cores' own fp8 product (v_mfma_f32_16x16x128_f8f6f4, at twice the rate; the one
+// over 32 elements rounds alike) adds up eight neighbouring products before
+// anything is float32 and drops what lies 13 binades below the largest: 1.5e-5 of
+// normally distributed results, 5e-5 of codes of all sizes, and all of a result
+// whose large products cancel.  One bfloat16 result in ninety comes out another
+// value for it.  So only a call that asks for it (fh_fp8_matmul_native, bfloat16
+// results) takes it, where the matrix cores are the bound.  Either way the sum
+// over one g is scaled and added to the running sum in float32, a fused
+// multiply-add per result.
 //
 // W lies in the int8 product's order: of 16 rows and 64 elements of k one contiguous
 // 1 KB, lane l's 16 bytes row l % 16 and elements 16 (l / 16) .. + 15 (any order
@@ -602,11 +604,11 @@ __global__ __launch_bounds__(256) void k_fp8_pack(const void* W, const float* sc
 }
 
 // How a call is cut up: a tile of k_fp8_tile (named by its tokens), or a shape of
-// k_fp8_few.  x2, x4: groups that share a tile's k.  Bf: bfloat16 results in the
-// matrix cores' own fp8.
+// k_fp8_few.  x2, x4: groups that share a tile's k.  Native: in the matrix cores'
+// own fp8.
 enum Kind {
   kFew16Rows8, kFew16Rows4, kFew16Rows2, kTokens32Rows8, kTokens32Rows4,
-  k16, k32, k32x2, k32x4, k64, k64x2, kWide64, k64Bf, k64x2Bf, k128Bf
+  k16, k32, k32x2, k32x4, k64, k64x2, kWide64, k64Native, k64x2Native, k128Native
 };
 struct Plan {
   Kind kind;
@@ -625,19 +627,20 @@ struct Plan {
 // 2048 37.5 with 4 waves, 40.8 and 42.5 with 2 and 8; 262144 x 1152 43.6 with 2, 44.2
 // and 56.0 with 4 and 8).  Up to 16 tokens staged in LDS where rows are many (16
 // tokens, 128256 x 2048: 47.7, with two waves on 16 rows 54.7; 8 tokens 46.3 and 42.1).
-// bfloat16 results: 256 rows x 128 tokens (4096 x 10240 x 2560 102, 2048 x 4096 x 2048
+// More: 256 x 64, by four waves of 64 rows where many tokens fill the CUs (float32
+// results: 300 x 100000 x 1024 80, by eight of 32 rows 93 and with 128 tokens 97; 1000 x
+// 12000 x 2048 52.9 and 59.7; 500 x 8000 x 1024 15.4 and 12.9; bfloat16 ones: 4096 x
+// 10240 x 2560 190 and 222, 2048 x 4096 x 2048 32.7 and 37.9, 1000 x 4096 x 2048 22.2
+// and 19.5), by eight of 32 else (64 x 151936 x 2560 84, by four 89).
+// Smaller calls as the int8 product's.
+// Native: 256 rows x 128 tokens (4096 x 10240 x 2560 102, 2048 x 4096 x 2048
 // 21.9, with 256 x 64 23.1; 80 x 262144 x 1152 62.6 and 75.7; of two blocks of k alone,
 // 500 x 14260 x 256, 12.6 and 8.3); 256 x 64 (1000 x 4096 x 2048 14.2, with 128 x 64
 // in two groups 17.9); where those are few, groups that share the k of 128 x 64 (333 x
 // 5003 x 1152 8.8, with 256 x 64 10.1, with 128 x 32 11.9; 64 x 20000 x 4096 24.0, 33.0
 // and 30.1), down to some 100 of them (128 x 4096 x 8192 23.7, 17.4 with 64 x 32 in
-// four groups).
-// float32 results: 256 x 64, by four waves of 64 rows where many tokens fill the CUs
-// (300 x 100000 x 1024 80, by eight of 32 rows 93 and with 128 tokens 97; 1000 x 12000
-// x 2048 52.9 and 59.7; 500 x 8000 x 1024 15.4 and 12.9), by eight of 32 else (64 x
-// 151936 x 2560 84, by four 89).
-// Smaller calls as the int8 product's.
-Plan plan_of(int64_t n, int64_t k, int64_t B, bool bf16) {
+// four groups); else as the others.
+Plan plan_of(int64_t n, int64_t k, int64_t B, bool native) {
   constexpr int kFull = 180;  // workgroups that about fill the 256 CUs
   const int64_t tiles = (n + 15) / 16, blocks = k_blocks(k), steps = 2 * blocks;
   if (B <= 16) {
@@ -645,11 +648,11 @@ Plan plan_of(int64_t n, int64_t k, int64_t B, bool bf16) {
     if (tiles < 2048 || (B <= 8 && steps >= 24)) return Plan{kFew16Rows4, 16, 16};
     return B <= 8 ? Plan{kFew16Rows2, 32, 16} : Plan{k16, 128, 16};
   }
-  const Plan big{k128Bf, 256, 128}, mid{bf16 ? k64Bf : k64, 256, 64}, shared{k64x2Bf, 128, 64};
-  if (bf16 && B > 64 && blocks >= 4 && big.tiles(n, B) >= kFull) return big;
-  if (!bf16 && B > 64 && mid.tiles(n, B) >= 400) return Plan{kWide64, 256, 64};
+  const Plan big{k128Native, 256, 128}, mid{native ? k64Native : k64, 256, 64}, shared{k64x2Native, 128, 64};
+  if (native && B > 64 && blocks >= 4 && big.tiles(n, B) >= kFull) return big;
+  if (!native && B > 64 && mid.tiles(n, B) >= 400) return Plan{kWide64, 256, 64};
   if (B > 32 && mid.tiles(n, B) >= kFull) return mid;
-  if (bf16 && B > 32 && blocks >= 4 && shared.tiles(n, B) >= 100) return shared;
+  if (native && B > 32 && blocks >= 4 && shared.tiles(n, B) >= 100) return shared;
   const Plan p{k32, 128, 32};
   const int64_t t = p.tiles(n, B);
   if (t >= 2 * kFull) return steps >= 48 && B > 32 ? Plan{k64x2, 128, 64} : p;
@@ -700,16 +703,16 @@ void launch_kind(const FP8Args& a, Kind kind, hipStream_t st) {
     default: break;
   }
   if constexpr (BF16) switch (kind) {
-    case k64Bf: return launch_tile<4, 2, 8, 1, false, PAST, BF16, HEAD>(a, st);
-    case k64x2Bf: return launch_tile<4, 2, 4, 2, false, PAST, BF16, HEAD>(a, st);
-    case k128Bf: return launch_tile<8, 4, 4, 1, false, PAST, BF16, HEAD>(a, st);
+    case k64Native: return launch_tile<4, 2, 8, 1, false, PAST, BF16, HEAD>(a, st);
+    case k64x2Native: return launch_tile<4, 2, 4, 2, false, PAST, BF16, HEAD>(a, st);
+    case k128Native: return launch_tile<8, 4, 4, 1, false, PAST, BF16, HEAD>(a, st);
     default: break;
   }
 }
 
 template <bool BF16, bool HEAD>
-void launch_product(const FP8Args& a, hipStream_t st) {
-  const Plan p = plan_of(a.n, a.k, a.B, BF16);
+void launch_product(const FP8Args& a, bool native, hipStream_t st) {
+  const Plan p = plan_of(a.n, a.k, a.B, native);
   if (past_caches(p, a.n, a.k, a.B))
     launch_kind<true, BF16, HEAD>(a, p.kind, st);
   else
@@ -722,20 +725,20 @@ int64_t fp8_parts(int64_t n, int64_t k, int64_t B) { return plan_of(n, k, B, fal
 
 bool fp8_fits(int64_t n, int64_t k, int64_t B) {
   // tiles of 512 threads; the few-token kernels' grids have the tokens in y
-  for (bool bf16 : {false, true}) {
-    const Plan p = plan_of(n, k, B, bf16);
+  for (bool native : {false, true}) {
+    const Plan p = plan_of(n, k, B, native);
     if (p.kind >= k16 && p.tiles(n, B) >= int64_t(1) << 23) return false;
   }
   return true;
 }
 
-hipError_t launch_fp8(const FP8Args& a, bool out_bf16, bool head, hipStream_t st) {
-  if (head)
-    launch_product<false, true>(a, st);
-  else if (out_bf16)
-    launch_product<true, false>(a, st);
+hipError_t launch_fp8(const FP8Args& a, FP8Out out, hipStream_t st) {
+  if (out == FP8Out::kHead)
+    launch_product<false, true>(a, false, st);
+  else if (out == FP8Out::kF32)
+    launch_product<false, false>(a, false, st);
   else
-    launch_product<false, false>(a, st);
+    launch_product<true, false>(a, out == FP8Out::kBf16Native, st);
   return hipGetLastError();
 }
 

@@ -96,6 +96,9 @@ hipError_t launch_fp8_pack(const void* W, bool bf16, const float* scales, int64_
                            hipStream_t st);
 int64_t fp8_parts(int64_t n, int64_t k, int64_t B);  // partials per row of the head
 bool fp8_fits(int64_t n, int64_t k, int64_t B);  // a launch holds fewer than 2^32 threads
-hipError_t launch_fp8(const FP8Args& a, bool out_bf16, bool head, hipStream_t st);
+// What a launch gives: results, in the matrix cores' own fp8 where that is asked
+// for, or a head's float32 logits (or none) and partials.
+enum class FP8Out { kF32, kBf16, kBf16Native, kHead };
+hipError_t launch_fp8(const FP8Args& a, FP8Out out, hipStream_t st);
 
 }  // namespace fh

@@ -168,6 +168,26 @@ hipError_t take_rows(const fh_fp8* w, const uint8_t* q, int64_t ld_q, const floa
                                a->ld_q, st);
 }
 
+fh_status matmul(const fh_fp8* w, const uint8_t* q, int64_t ld_q, const float* q_scale, int64_t ld_scale, int64_t B,
+                 void* out, int64_t ld_out, fh::FP8Out kind, void* workspace, int64_t workspace_bytes,
+                 hipStream_t st) {
+  fh_status s = check_product(w, q, ld_q, q_scale, ld_scale, B);
+  if (s != FH_OK) return s;
+  if (!out) return fail(FH_EINVAL, "out is NULL");
+  if (!aligned_to(out, kind == fh::FP8Out::kF32 ? 4 : 2)) return fail(FH_EINVAL, "out must be aligned to its elements");
+  s = check_ld("ld_out", ld_out, w->n, B);
+  if (s == FH_OK) s = check_workspace(workspace, workspace_bytes, need_bytes(w, q, ld_q, B, false));
+  if (s != FH_OK) return s;
+  DeviceGuard g(w->device);
+  if (!g.ok) return fail(FH_EHIP, "cannot select the weight's device");
+  fh::FP8Args a{};
+  hipError_t r = take_rows(w, q, ld_q, q_scale, ld_scale, B, workspace, st, &a);
+  a.out = out;
+  a.ld_out = ld_out;
+  if (r == hipSuccess) r = fh::launch_fp8(a, kind, st);
+  return r == hipSuccess ? FH_OK : hip_fail(r, "fp8 product launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -277,23 +297,19 @@ fh_status fh_fp8_matmul(const fh_fp8* w, const uint8_t* q, int64_t ld_q, const f
                         int64_t B, void* out, int64_t ld_out, fh_dtype out_dtype, void* workspace,
                         int64_t workspace_bytes, void* stream) {
   return guarded(FH_ENOMEM, [&]() -> fh_status {
-    fh_status s = check_product(w, q, ld_q, q_scale, ld_scale, B);
-    if (s != FH_OK) return s;
-    if (!out) return fail(FH_EINVAL, "out is NULL");
     if (out_dtype != FH_F32 && out_dtype != FH_BF16) return fail(FH_EINVAL, "unknown out_dtype");
-    if (!aligned_to(out, out_dtype == FH_BF16 ? 2 : 4)) return fail(FH_EINVAL, "out must be aligned to its elements");
-    s = check_ld("ld_out", ld_out, w->n, B);
-    if (s == FH_OK) s = check_workspace(workspace, workspace_bytes, need_bytes(w, q, ld_q, B, false));
-    if (s != FH_OK) return s;
-    DeviceGuard g(w->device);
-    if (!g.ok) return fail(FH_EHIP, "cannot select the weight's device");
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    fh::FP8Args a{};
-    hipError_t r = take_rows(w, q, ld_q, q_scale, ld_scale, B, workspace, st, &a);
-    a.out = out;
-    a.ld_out = ld_out;
-    if (r == hipSuccess) r = fh::launch_fp8(a, out_dtype == FH_BF16, false, st);
-    return r == hipSuccess ? FH_OK : hip_fail(r, "fp8 product launch");
+    return matmul(w, q, ld_q, q_scale, ld_scale, B, out, ld_out,
+                  out_dtype == FH_BF16 ? fh::FP8Out::kBf16 : fh::FP8Out::kF32, workspace, workspace_bytes,
+                  static_cast<hipStream_t>(stream));
+  });
+}
+
+fh_status fh_fp8_matmul_native(const fh_fp8* w, const uint8_t* q, int64_t ld_q, const float* q_scale,
+                               int64_t ld_scale, int64_t B, void* out, int64_t ld_out, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+  return guarded(FH_ENOMEM, [&]() -> fh_status {
+    return matmul(w, q, ld_q, q_scale, ld_scale, B, out, ld_out, fh::FP8Out::kBf16Native, workspace, workspace_bytes,
+                  static_cast<hipStream_t>(stream));
   });
 }
 
@@ -323,7 +339,7 @@ fh_status fh_fp8_forward(const fh_fp8* w, const uint8_t* q, int64_t ld_q, const 
     a.inverse_t = a.token_sample ? inverse_of(temperature) : 1.f;
     a.seed = seed;
     a.parts = reinterpret_cast<fh::Part*>(static_cast<char*>(workspace) + copy_bytes(w, q, ld_q, B));
-    if (r == hipSuccess) r = fh::launch_fp8(a, false, true, st);
+    if (r == hipSuccess) r = fh::launch_fp8(a, fh::FP8Out::kHead, st);
     if (r == hipSuccess)
       r = fh::launch_choice(a.parts, B, fh::fp8_parts(w->n, w->k, B), out_token, out_token_logit, out_lse, st);
     return r == hipSuccess ? FH_OK : hip_fail(r, "fp8 head launch");

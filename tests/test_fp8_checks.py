@@ -209,3 +209,16 @@ def test_binding_product_refusals(weight):
         fp8.FP8Head(codes=q, scales=torch.zeros(2, 2))
     with pytest.raises(ValueError, match="scales: must be contiguous"):
         fp8.FP8Head(codes=f8(200, 200), scales=torch.zeros(2, 2).t())
+
+
+def test_native_product_refusals(lib, weight):
+    _refused(lib, lib.fh_fp8_matmul_native(None, A, 64, A, 1, 1, A, 8, None, 0, None), "w is NULL")
+    q, s = f8(2, 200), torch.zeros(2, 2)
+    for out, needle in [(torch.zeros(2, 12), "out: expected"), (bf(2, 11), "out: expected"), (bf(2, 12), "one GPU")]:
+        with pytest.raises(ValueError, match=needle):
+            fp8.fh_fp8_matmul_native(weight, q, s, out)
+    head = fp8.FP8Head.__new__(fp8.FP8Head)
+    head.w, head.n, head.k, head.device = None, 12, 200, torch.device("cpu")
+    head._inputs = lambda *a: (200, 2, 0)
+    with pytest.raises(ValueError, match="native products are bfloat16"):
+        head.matmul(q, s, native=True)
