@@ -765,6 +765,13 @@ fh_status fh_beam_reorder(void* const* states, int64_t count, const fh_beam_layo
                           int64_t sequences, int64_t beams, const int32_t* parent,
                           const int32_t* lengths, void* stream);
 
+/* fh_beam_reorder_check — what fh_beam_reorder would refuse of these arguments, with
+ * nothing moved: for states of several layouts, all of which are checked before the
+ * first is reordered. */
+fh_status fh_beam_reorder_check(void* const* states, int64_t count, const fh_beam_layout* layout,
+                                int64_t sequences, int64_t beams, const int32_t* parent,
+                                const int32_t* lengths);
+
 /* Thread-local description of the last error on this thread ("" if none). */
 const char* fh_last_error(void);
 

@@ -24,7 +24,8 @@ def __getattr__(name):
                   "fh_fp8_create_codes", "fh_fp8_destroy", "fh_fp8_get", "fh_fp8_workspace", "fh_fp8_matmul",
                   "fh_fp8_matmul_native", "fh_fp8_forward"):
         from . import fp8 as module
-    elif name in ("beam_select", "beam_reorder", "fh_beam_workspace", "fh_beam_select", "fh_beam_reorder"):
+    elif name in ("beam_select", "beam_reorder", "fh_beam_workspace", "fh_beam_select", "fh_beam_reorder",
+                  "fh_beam_reorder_check"):
         from . import beam as module
     else:
         raise AttributeError(name)

@@ -30,7 +30,7 @@ EXPORTS = (
     "fh_logits_workspace", "fh_logits_apply", "fh_rmsnorm_fp8", "fh_fp8_quant", "fh_fp8_create",
     "fh_fp8_create_codes", "fh_fp8_destroy", "fh_fp8_get", "fh_fp8_workspace", "fh_fp8_matmul",
     "fh_fp8_matmul_native", "fh_fp8_forward",
-    "fh_beam_workspace", "fh_beam_select", "fh_beam_reorder", "fh_last_error", "fh_version",
+    "fh_beam_workspace", "fh_beam_select", "fh_beam_reorder", "fh_beam_reorder_check", "fh_last_error", "fh_version",
 )
 
 
@@ -127,6 +127,7 @@ _SIGS = {
     "fh_beam_select": ([_p, _i64, _p, _i64, _i64, _i64, _i64, _i64, _p, _p, _p, _i32, _i64, _p, _p,
                         _p, _p, _p, _i64, _p], _int),
     "fh_beam_reorder": ([_p, _i64, ctypes.POINTER(FhBeamLayout), _i64, _i64, _p, _p, _p], _int),
+    "fh_beam_reorder_check": ([_p, _i64, ctypes.POINTER(FhBeamLayout), _i64, _i64, _p, _p], _int),
     "fh_last_error": ([], ctypes.c_char_p),
     "fh_version": ([], ctypes.c_char_p),
 }

@@ -105,19 +105,29 @@ def beam_select(logits, scores, *, keep=None, ids=None, v=None, lse=None, finish
     return got
 
 
-def fh_beam_reorder(states, layout, parent, lengths=None, stream=None) -> None:
-    """Rows of states (tensors of one layout, fh_beam_layout's fields in bytes as a
-    sequence) permuted in place by parent [S x W]."""
+def _reorder_args(states, layout, parent, lengths):
+    """The GPU of a call, and its arguments but for the stream."""
     S, W = parent.shape
     _beams(parent, torch.int32, (S, W), "parent")
     if lengths is not None:
         _vector(lengths, torch.int32, S * W, "lengths")
     dev = _device(parent, lengths, *states)
     n = len(states)
+    return dev, ((ctypes.c_void_p * n)(*[t.data_ptr() for t in states]), n, _abi.FhBeamLayout(*layout), S, W,
+                 parent.data_ptr(), _ptr(lengths))
+
+
+def fh_beam_reorder(states, layout, parent, lengths=None, stream=None) -> None:
+    """Rows of states (tensors of one layout, fh_beam_layout's fields in bytes as a
+    sequence) permuted in place by parent [S x W]."""
+    dev, args = _reorder_args(states, layout, parent, lengths)
     with _on(dev, stream):
-        check(_abi.load().fh_beam_reorder((ctypes.c_void_p * n)(*[t.data_ptr() for t in states]), n,
-                                          _abi.FhBeamLayout(*layout), S, W, parent.data_ptr(), _ptr(lengths),
-                                          _stream(dev)))
+        check(_abi.load().fh_beam_reorder(*args, _stream(dev)))
+
+
+def fh_beam_reorder_check(states, layout, parent, lengths=None) -> None:
+    """Raises what fh_beam_reorder would, and moves nothing."""
+    check(_abi.load().fh_beam_reorder_check(*_reorder_args(states, layout, parent, lengths)[1]))
 
 
 def _joined(shape, strides):
@@ -168,7 +178,8 @@ def beam_reorder(states, parent, *, dim=0, lengths=None, length_dim=None, stream
     rows are in dimension `dim`, dimensions before it are layers.  lengths [S W]
     int32 with length_dim (behind dim): only that many first positions of each row
     count; what lies behind them stays.  parent and lengths must not be part of a
-    state.  States of one layout go together in one launch."""
+    state.  States of one layout go together in one launch; a call that is refused
+    has moved none."""
     if isinstance(states, torch.Tensor):
         states = [states]
     if parent.dim() != 2:
@@ -181,7 +192,9 @@ def beam_reorder(states, parent, *, dim=0, lengths=None, length_dim=None, stream
         layout = _layout(t, rows, dim, length_dim)
         if t.numel():
             groups.setdefault(layout, []).append(t)
-    if len(groups) != 1:  # a call checks its own
+    if len(groups) != 1:  # a call checks its own; none moves before all are checked
         _device(parent, lengths, *states)
+        for layout, same in groups.items():
+            fh_beam_reorder_check(same, layout, parent, lengths)
     for layout, same in groups.items():
         fh_beam_reorder(same, layout, parent, lengths, stream)

@@ -39,6 +39,66 @@ int64_t need_bytes(int64_t rows, int64_t n) {
   return (int64_t)sizeof(float) * rows * (fh::beam_chunks(n) + fh::beam_chunks(n) / 4);
 }
 
+// A call's arguments checked, and as the launcher takes them (but for the states);
+// `any` is false where there is nothing to move.
+fh_status check_reorder(void* const* states, int64_t count, const fh_beam_layout* layout, int64_t sequences,
+                        int64_t beams, const int32_t* parent, const int32_t* lengths, fh::BeamReorderArgs* a,
+                        bool* any) {
+  *any = false;
+  if (count < 0 || count > (int64_t(1) << 20)) return fail(FH_EINVAL, "count outside [0, 2^20]");
+  if (!layout || !parent || (count > 0 && !states))
+    return fail(FH_EINVAL, "states, layout and parent must not be NULL");
+  const fh_status s = check_beams(sequences, beams);
+  if (s != FH_OK) return s;
+  if (!aligned_to(parent, 4) || !aligned_to(lengths, 4))
+    return fail(FH_EINVAL, "parent and lengths must be aligned to 4 bytes");
+  const fh_beam_layout& l = *layout;
+  if (l.outer < 0 || l.mid < 0 || l.positions < 0 || l.run < 0) return fail(FH_EINVAL, "a size is negative");
+  if (l.outer == 0 || l.mid == 0 || l.positions == 0 || l.run == 0) return FH_OK;
+  if (l.positions > kMaxBytes / l.run) return fail(FH_EINVAL, "the state is too large");
+  // from the smallest stride up, each steps over what the ones before it span:
+  // no byte belongs to two places
+  std::pair<int64_t, int64_t> dims[] = {
+      {l.ld_outer, l.outer}, {l.ld_row, sequences * beams}, {l.ld_mid, l.mid}, {l.ld_position, l.positions}};
+  std::sort(dims, dims + 4);
+  int64_t span = l.run;
+  for (const auto& d : dims) {
+    if (d.second == 1) continue;
+    if (d.first < span) return fail(FH_EINVAL, "the layout's strides overlap");
+    if (d.first > (kMaxBytes - span) / d.second) return fail(FH_EINVAL, "the state is too large");
+    span += (d.second - 1) * d.first;
+  }
+  const auto inside = [&](const void* p, const void* state) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(state);
+    return p && a >= b && a < b + (uintptr_t)span;
+  };
+  for (int64_t i = 0; i < count; ++i) {
+    if (!states[i]) return fail(FH_EINVAL, "a state is NULL");
+    if (inside(parent, states[i]) || inside(lengths, states[i]))
+      return fail(FH_EINVAL, "parent and lengths must not lie in a state");
+  }
+  std::vector<void*> sorted(states, states + count);
+  std::sort(sorted.begin(), sorted.end());
+  if (std::adjacent_find(sorted.begin(), sorted.end()) != sorted.end())
+    return fail(FH_EINVAL, "a state is listed twice");
+  a->parent = parent;
+  a->lengths = lengths;
+  a->beams = (int)beams;
+  a->sequences = sequences;
+  a->outer = l.outer;
+  a->mid = l.mid;
+  a->positions = l.positions;
+  a->run = l.run;
+  a->ld_outer = l.ld_outer;
+  a->ld_row = l.ld_row;
+  a->ld_mid = l.ld_mid;
+  a->ld_position = l.ld_position;
+  a->count = (int)std::min<int64_t>(count, fh::kReorderStates);  // of the largest launch
+  if (count > 0 && !fh::beam_reorder_fits(*a)) return fail(FH_EINVAL, "the states are too large for one call");
+  *any = count > 0;
+  return FH_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -107,63 +167,26 @@ fh_status fh_beam_select(const float* logits, int64_t ld_logits, const int32_t* 
 fh_status fh_beam_reorder(void* const* states, int64_t count, const fh_beam_layout* layout, int64_t sequences,
                           int64_t beams, const int32_t* parent, const int32_t* lengths, void* stream) {
   return guarded(FH_ENOMEM, [&]() -> fh_status {
-    if (count < 0 || count > (int64_t(1) << 20)) return fail(FH_EINVAL, "count outside [0, 2^20]");
-    if (!layout || !parent || (count > 0 && !states))
-      return fail(FH_EINVAL, "states, layout and parent must not be NULL");
-    const fh_status s = check_beams(sequences, beams);
-    if (s != FH_OK) return s;
-    if (!aligned_to(parent, 4) || !aligned_to(lengths, 4))
-      return fail(FH_EINVAL, "parent and lengths must be aligned to 4 bytes");
-    const fh_beam_layout& l = *layout;
-    if (l.outer < 0 || l.mid < 0 || l.positions < 0 || l.run < 0) return fail(FH_EINVAL, "a size is negative");
-    if (l.outer == 0 || l.mid == 0 || l.positions == 0 || l.run == 0) return FH_OK;
-    if (l.positions > kMaxBytes / l.run) return fail(FH_EINVAL, "the state is too large");
-    // from the smallest stride up, each steps over what the ones before it span:
-    // no byte belongs to two places
-    std::pair<int64_t, int64_t> dims[] = {
-        {l.ld_outer, l.outer}, {l.ld_row, sequences * beams}, {l.ld_mid, l.mid}, {l.ld_position, l.positions}};
-    std::sort(dims, dims + 4);
-    int64_t span = l.run;
-    for (const auto& d : dims) {
-      if (d.second == 1) continue;
-      if (d.first < span) return fail(FH_EINVAL, "the layout's strides overlap");
-      if (d.first > (kMaxBytes - span) / d.second) return fail(FH_EINVAL, "the state is too large");
-      span += (d.second - 1) * d.first;
-    }
-    const auto inside = [&](const void* p, const void* state) {
-      const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(state);
-      return p && a >= b && a < b + (uintptr_t)span;
-    };
-    for (int64_t i = 0; i < count; ++i) {
-      if (!states[i]) return fail(FH_EINVAL, "a state is NULL");
-      if (inside(parent, states[i]) || inside(lengths, states[i]))
-        return fail(FH_EINVAL, "parent and lengths must not lie in a state");
-    }
-    std::vector<void*> sorted(states, states + count);
-    std::sort(sorted.begin(), sorted.end());
-    if (std::adjacent_find(sorted.begin(), sorted.end()) != sorted.end())
-      return fail(FH_EINVAL, "a state is listed twice");
     fh::BeamReorderArgs a{};
-    a.parent = parent;
-    a.lengths = lengths;
-    a.beams = (int)beams;
-    a.sequences = sequences;
-    a.outer = l.outer;
-    a.mid = l.mid;
-    a.positions = l.positions;
-    a.run = l.run;
-    a.ld_outer = l.ld_outer;
-    a.ld_row = l.ld_row;
-    a.ld_mid = l.ld_mid;
-    a.ld_position = l.ld_position;
+    bool any;
+    const fh_status s = check_reorder(states, count, layout, sequences, beams, parent, lengths, &a, &any);
+    if (s != FH_OK || !any) return s;
     for (int64_t i = 0; i < count; i += fh::kReorderStates) {
       a.count = (int)std::min<int64_t>(count - i, fh::kReorderStates);
       std::copy(states + i, states + i + a.count, a.state);
-      if (!fh::beam_reorder_fits(a)) return fail(FH_EINVAL, "the states are too large for one call");
       const hipError_t r = fh::launch_beam_reorder(a, static_cast<hipStream_t>(stream));
       if (r != hipSuccess) return hip_fail(r, "reordering launch");
     }
     return FH_OK;
+  });
+}
+
+fh_status fh_beam_reorder_check(void* const* states, int64_t count, const fh_beam_layout* layout, int64_t sequences,
+                                int64_t beams, const int32_t* parent, const int32_t* lengths) {
+  return guarded(FH_ENOMEM, [&]() -> fh_status {
+    fh::BeamReorderArgs a{};
+    bool any;
+    return check_reorder(states, count, layout, sequences, beams, parent, lengths, &a, &any);
   });
 }
 

@@ -225,3 +225,17 @@ def test_binding_reorder_refusals():
                        ({"parent": p.long()}, "one GPU|parent")]:
         with pytest.raises(ValueError, match=needle):
             beam.beam_reorder(**dict({"states": x, "parent": p}, **kw))
+
+
+def test_reorder_check_refuses_as_the_call_and_launches_nothing(lib):
+    by, st = ctypes.byref(_abi.FhBeamLayout(**LAYOUT)), (P * 2)(1 << 24, 1 << 25)
+    for args, needle in [((st, 2, None, 2, 3, A, None), "must not be NULL"), ((st, 2, by, 2, 65, A, None), "beams outside"),
+                         ((st, 2, by, 2, 3, P((1 << 25) + 2876), None), "must not lie in a state"),
+                         ((st, 2, ctypes.byref(_abi.FhBeamLayout(**dict(LAYOUT, ld_row=239))), 2, 3, A, None), "overlap"),
+                         ((st, 2, ctypes.byref(_abi.FhBeamLayout(**dict(LAYOUT, run=1 << 50, positions=1, mid=1, outer=1,
+                                                                        ld_row=1 << 51))), 2, 3, A, None),
+                          "too large for one call"),
+                         (((P * 2)(1 << 24, 1 << 24), 2, by, 2, 3, A, None), "listed twice")]:
+        _refused(lib, lib.fh_beam_reorder_check(*args), needle)
+    assert lib.fh_beam_reorder_check(st, 2, by, 2, 3, A, None) == 0
+    assert lib.fh_beam_reorder_check(None, 0, by, 2, 3, A, None) == 0
