@@ -178,8 +178,8 @@ def beam_reorder(states, parent, *, dim=0, lengths=None, length_dim=None, stream
     rows are in dimension `dim`, dimensions before it are layers.  lengths [S W]
     int32 with length_dim (behind dim): only that many first positions of each row
     count; what lies behind them stays.  parent and lengths must not be part of a
-    state.  States of one layout go together in one launch; a call that is refused
-    has moved none."""
+    state, and states must not overlap (one listed twice is refused).  States of
+    one layout go together in one launch; a call that is refused has moved none."""
     if isinstance(states, torch.Tensor):
         states = [states]
     if parent.dim() != 2:
@@ -193,6 +193,9 @@ def beam_reorder(states, parent, *, dim=0, lengths=None, length_dim=None, stream
         if t.numel():
             groups.setdefault(layout, []).append(t)
     if len(groups) != 1:  # a call checks its own; none moves before all are checked
+        at = [t.data_ptr() for same in groups.values() for t in same]
+        if len(set(at)) != len(at):
+            raise ValueError("a state is listed twice, in two layouts")
         _device(parent, lengths, *states)
         for layout, same in groups.items():
             fh_beam_reorder_check(same, layout, parent, lengths)

@@ -239,3 +239,14 @@ def test_reorder_check_refuses_as_the_call_and_launches_nothing(lib):
         _refused(lib, lib.fh_beam_reorder_check(*args), needle)
     assert lib.fh_beam_reorder_check(st, 2, by, 2, 3, A, None) == 0
     assert lib.fh_beam_reorder_check(None, 0, by, 2, 3, A, None) == 0
+
+
+def test_one_storage_in_two_layouts_is_refused():
+    x, p = torch.zeros(6, 10), torch.zeros(2, 3, dtype=torch.int32)
+    for states, kw in [([x, x[:, :4]], {}), ([x, torch.zeros(6, 3), x.view(6, 5, 2).transpose(1, 2)], {}),
+                       ([x, x[:, :4]], {"lengths": torch.zeros(6, dtype=torch.int32), "length_dim": 1})]:
+        with pytest.raises(ValueError, match="listed twice"):
+            beam.beam_reorder(states, p, **kw)
+    # nothing lies in an empty one
+    with pytest.raises(ValueError, match="one GPU"):
+        beam.beam_reorder([x, torch.zeros(6, 3), x[:, :0]], p)

@@ -59,3 +59,23 @@ def test_states_of_several_layouts():
     say("reorder layouts")
     beam_reorder(states, parents(2, 3))
     assert all(torch.equal(a, b) for a, b in zip(states, want))
+
+
+def test_one_storage_in_two_layouts_is_not_moved():
+    from lm_output_head_amd import beam_reorder
+    x = state(6, 10)
+    before = x.clone()
+    say("reorder of one storage twice")
+    with pytest.raises(ValueError, match="listed twice"):
+        beam_reorder([x, x[:, :4]], parents(2, 3))
+    assert torch.equal(x, before)
+
+
+def test_keys_and_values_that_interleave():
+    """States of two layouts whose bytes lie between each other's."""
+    from lm_output_head_amd import beam_reorder
+    both = state(6, 4, 12)
+    want = both.view(2, 3, 4, 12).roll(-1, 1).reshape(6, 4, 12)
+    say("reorder interleaved")
+    beam_reorder([both[:, :, :5], both[:, :, 5:9], both[:, :, 9:]], parents(2, 3))
+    assert torch.equal(both, want)
