@@ -757,7 +757,8 @@ typedef struct {
  *   lengths  device [sequences x beams] int32 or NULL (all): positions of each
  *            row that count, clamped to [0, positions].  A row takes its parent's;
  *            what lies behind them is left as it is.
- * parent and lengths must not lie in a state, and no state is listed twice.  Any
+ * parent and lengths must not lie among a state's bytes, from its first to its last,
+ * not in part either, and no state is listed twice.  Any
  * alignment.  Positions that do not follow each other directly, and their runs,
  * are fewer than 2^31.
  */

@@ -68,13 +68,14 @@ fh_status check_reorder(void* const* states, int64_t count, const fh_beam_layout
     if (d.first > (kMaxBytes - span) / d.second) return fail(FH_EINVAL, "the state is too large");
     span += (d.second - 1) * d.first;
   }
-  const auto inside = [&](const void* p, const void* state) {
+  const uintptr_t list = sizeof(int32_t) * (uintptr_t)(sequences * beams);  // bytes of parent, of lengths
+  const auto meets = [&](const void* p, const void* state) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(state);
-    return p && a >= b && a < b + (uintptr_t)span;
+    return p && a < b + (uintptr_t)span && b < a + list;
   };
   for (int64_t i = 0; i < count; ++i) {
     if (!states[i]) return fail(FH_EINVAL, "a state is NULL");
-    if (inside(parent, states[i]) || inside(lengths, states[i]))
+    if (meets(parent, states[i]) || meets(lengths, states[i]))
       return fail(FH_EINVAL, "parent and lengths must not lie in a state");
   }
   std::vector<void*> sorted(states, states + count);

@@ -250,3 +250,16 @@ def test_one_storage_in_two_layouts_is_refused():
     # nothing lies in an empty one
     with pytest.raises(ValueError, match="one GPU"):
         beam.beam_reorder([x, torch.zeros(6, 3), x[:, :0]], p)
+
+
+def test_lists_that_reach_into_a_state_are_refused(lib):
+    """parent and lengths of 6 beams are 24 bytes: in a state that begins within them
+    too, and not in one that begins right behind them or ends right before."""
+    l = _abi.FhBeamLayout(**LAYOUT)
+    by, first, behind = ctypes.byref(l), 1 << 24, (1 << 24) + 2 * 6 * 240
+    for at in (first - 20, first - 4, first, behind - 4):
+        _refused(lib, lib.fh_beam_reorder_check((P * 1)(first), 1, by, 2, 3, P(at), None), "must not lie in a state")
+        _refused(lib, lib.fh_beam_reorder_check((P * 1)(first), 1, by, 2, 3, A, P(at)), "must not lie in a state")
+        _refused(lib, lib.fh_beam_reorder((P * 1)(first), 1, by, 2, 3, A, P(at), None), "must not lie in a state")
+    for at in (first - 24, behind):
+        assert lib.fh_beam_reorder_check((P * 1)(first), 1, by, 2, 3, P(at), P(at)) == 0
