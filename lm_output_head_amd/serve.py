@@ -67,10 +67,6 @@ def _device(*tensors):
 
 _SAME = contextlib.nullcontext()
 
-# torch.cuda.current_device without its check for a first use, which a tensor on
-# a GPU has had (0.1 us of a call), where torch has it.
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-
 
 def _on(dev, stream):
     """Make `dev` current for a call, and `stream`, so that outputs allocated
@@ -79,7 +75,7 @@ def _on(dev, stream):
         if stream.device != dev:
             raise ValueError("stream is on another device than the tensors")
         return torch.cuda.stream(stream)
-    return _SAME if dev.index == _current_device() else torch.cuda.device(dev)
+    return _SAME if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _stream(dev):

@@ -316,3 +316,12 @@ def test_oracle_norm_and_product_by_hand():
     y, s = serve_oracle.rmsnorm([[3.0, 4.0]], [[1.0, -1.0]], [1.0, 2.0], 0.0, 1.0)
     assert s.tolist() == [[4.0, 3.0]] and np.allclose(y, np.array([[8.0, 9.0]]) / np.sqrt(12.5))
     assert serve_oracle.product([[1, -2]], [0.5], [[3, 4], [-128, 127]], [1.0, 2.0]).tolist() == [[-2.5, -382.0]]
+
+
+def test_the_current_device_is_torchs(monkeypatch):
+    """A call on the current GPU changes no device, one on another does: by
+    torch.cuda.current_device and torch.cuda.device, as a program may replace them."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "device", lambda dev: ("device", dev))
+    assert serve._on(torch.device("cuda", 3), None) is serve._SAME
+    assert serve._on(torch.device("cuda", 1), None) == ("device", torch.device("cuda", 1))
