@@ -73,7 +73,8 @@ def beam_select(logits, scores, *, keep=None, ids=None, v=None, lse=None, finish
     ids, scores [S x W] float32 the beams' totals so far.  "score", "token" and
     "parent" [S x keep], best first; -inf, -1 and -1 where there are fewer.  lse
     [S W]: the rows' log-sum-exps where they are known, as of a retrieval head's
-    candidates.  finished [S x W] int32: beams that offer `eos` alone, at their own
+    candidates; else the call's own, in float32 sums (1e-7 or so, which order beams
+    whose totals are that near to each other).  finished [S x W] int32: beams that offer `eos` alone, at their own
     score; then "finished" says which of the continuations are.  v: the number of
     tokens, which ids need."""
     S, W, ld_z, ld_ids = _select_inputs(logits, ids, scores, lse, finished)

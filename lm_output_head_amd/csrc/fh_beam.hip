@@ -1,11 +1,16 @@
 // Decoding by beams: the best continuations of each sequence over its beams and
 // all tokens, and the reordering of states by the beams that they continue.
 //
-// The total of a continuation is t = score + (z - lse), in float64 (logits and
-// scores are float32; neighbours of different beams are told apart by the exact
-// difference of their logits).  In a row t grows with z, so what one pass over the
-// logits leaves is enough: the largest z of each 256 places (a chunk) and sums of
-// exponentials of each 1024 for the row's lse.
+// The total of a continuation is t = score + (z - lse), in float64 from there on
+// (logits, scores and an lse that is given are float32).  In a row t grows with z, so
+// what one pass over the logits leaves is enough: the largest z of each 256 places (a
+// chunk) and sums of exponentials of each 1024 for the row's lse.  Those
+// exponentials and sums are float32, the hardware's exponential with its argument
+// rounded: what an lse is off by, at most (42 + 8 ln n) 2^-24, is common to its beam
+// and decides the order only between beams, and only there where their totals are
+// nearer than that.  Totals of 64 to 300000 logits were off by 5e-7 at most, their
+// rounding to float32 included.  In float64 the 16 million exponentials of 16 x 8 x
+// 151936 are, by count, some 8 us of instructions beside a scan of 13.
 // The `keep` best of a sequence lie in the `keep` best chunks, by their largest t
 // and, of equal ones, by their order: a chunk outside of them is beaten by one
 // element of each.  So a second pass looks at those few chunks alone.
