@@ -93,8 +93,9 @@ __device__ __forceinline__ f32x4a reduce_part(const float (&v)[4][4], bool want_
 // A wave per 1024 logits, all on their way before the first is used; the largest
 // come out of exchanges between lanes, the exponentials' sum in float32 (1024
 // terms of at most 1, in one order).  16 x 8 beams x 151936, of which 62 MB count,
-// take 13.6 us (a copy's rate would be 12.7); two or four of these parts a wave 14.5
-// and 17, a workgroup of 1024 threads 14.9.  Four beams of 128256 take 3.6.
+// take 13.0 us (a copy's rate would be 12.7; a read's, 9); two or four of these parts a
+// wave 0.9 and 3.4 us more, a workgroup of 1024 threads 1.3.  Four beams of 128256 take
+// 3.5.
 __global__ __launch_bounds__(256) void k_beam_scan(BeamArgs a, int chunks) {
   const int lane = threadIdx.x & 63, part = (int)blockIdx.x * 4 + (int)(threadIdx.x >> 6);
   const int64_t row = blockIdx.y;
@@ -574,8 +575,11 @@ __global__ __launch_bounds__(kThreads) void k_beam_choose(BeamArgs a, int chunks
     return;
   }
 
-  // Many totals on one step (rows of equal logits, say): every wave keeps the best
-  // 64 of its chunks in order, and the waves' lists are merged.
+  // Many totals on one step: every wave keeps the best 64 of its chunks in order, and
+  // the waves' lists are merged.  Rows of equal logits come here (16 x 9 beams of
+  // 151936, keep 16, 223 us; one sequence of four 305), and totals far below the best
+  // one, whose steps are wide there (a finished beam 40 above the eight live ones of
+  // each of those 16 sequences 368 us; among them 24).
   Cand mine = worst();
   auto offer = [&](const Cand& c) {
     const Cand last{readlane_d(mine.t, M - 1), readlane_l(mine.at, M - 1)};
@@ -658,9 +662,12 @@ __device__ __forceinline__ void store_bytes(char* p, uint32_t v, int n) {
 // In place, so what moves is read once and written once, and nothing else is
 // touched: no second cache, and beams that continue themselves cost nothing.  Bound by
 // memory: 16 states of 8 x 8 beams x 8 heads x 2000 x 64 bfloat16, 2.33 GB read and
-// written, take 448 us, 5.2 TB/s, a little above a copy's rate.  Steps there: 1228 us with the parents looked up by every
-// thread, 564 by a lane each, 480 with one slab of 4 KB a workgroup, 470 with stores
-// past the caches, 448 with the loads past them as well (PAST).
+// written, take 435 us, 5.3 TB/s, a little above a copy's rate.  Steps there: 1228 us
+// with the parents looked up by every thread, 564 by a lane each, 480 with one slab of
+// 4 KB a workgroup, 470 with stores past the caches, 448 with the loads past them as
+// well (PAST).  Three gigabytes by more beams: 4 x 16 4.7 TB/s, 2 x 32 5.2, 1 x 64 4.8;
+// with positions that are not one run (64 of 128 bfloat16 each) 8 x 8 5.0, 4 x 16 4.7,
+// 2 x 32 and 1 x 64, whose columns are four bytes, 4.2.
 constexpr int kSlab = 256;
 
 template <int WMAX, typename V, bool DENSE, bool PAST>

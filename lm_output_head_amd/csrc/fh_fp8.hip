@@ -218,13 +218,14 @@ __global__ __launch_bounds__(64 * KW * G) void k_fp8_few(FP8Args a) {
 // take half the registers, so two waves share a SIMD, and W has room for one block
 // alone: a row's registers are loaded again right behind their last use, and the
 // other wave covers the wait.
-// In fp8 (128 tokens) 4096 x 10240 x 2560 in us: 132 with 32 rows of eight waves; 118 with 64 of four; 109 with tokens read in
+// Native (128 tokens) 4096 x 10240 x 2560 in us: 132 with 32 rows of eight waves; 118 with 64 of four; 109 with tokens read in
 // whole lines (16 rows of 64 bytes a load before) and eight neighbouring row tiles
 // of a panel at once; 102 with those loads spread over the products and sums three
 // products behind (2.1 PFLOP/s; the library's fp8 product without scales per block
 // takes 122).  Without any load it would take 82, without the multiply-adds of
 // the scales too 67: the matrix cores are busy 63% of the cycles, at 1.75 GHz.
-// In half precision (64 tokens) 300 x 100000 x 1024 takes 80 us, 0.77 PFLOP/s, and 82
+// In half precision (64 tokens) 4096 x 10240 x 2560 takes 190 us, 1.13 PFLOP/s: the
+// matrix cores are busy 51% of the cycles.  300 x 100000 x 1024 takes 80 us, 0.77 PFLOP/s, and 82
 // with W's 64 rows converted at once and two blocks of them.  128 x 262144 x 1152 with
 // neither results nor draws takes 98: 86 with W from the caches, and some 5 less each
 // without the tokens' loads, the multiply-adds or the conversions; 66 with products
@@ -542,7 +543,8 @@ __global__ __launch_bounds__(64 * WN * KW) __attribute__((amdgpu_waves_per_eu(FN
 }
 
 // scale of each block of 128 x 128: max |W| / 448; *bad is set where a block is
-// not finite.
+// not finite.  128256 x 2048 bfloat16, 525 MB, takes 118 us, 4.4 TB/s; its codes (below),
+// 788 MB, 134 us, 5.9 TB/s.  A weight is made once.
 template <typename T>
 __global__ __launch_bounds__(256) void k_fp8_scales(const void* W, int64_t n, int64_t k, float* scales, int* bad) {
   __shared__ uint32_t sh[4];
@@ -632,7 +634,16 @@ struct Plan {
 // 12000 x 2048 52.9 and 59.7; 500 x 8000 x 1024 15.4 and 12.9; bfloat16 ones: 4096 x
 // 10240 x 2560 190 and 222, 2048 x 4096 x 2048 32.7 and 37.9, 1000 x 4096 x 2048 22.2
 // and 19.5), by eight of 32 else (64 x 151936 x 2560 84, by four 89).
-// Smaller calls as the int8 product's.
+// Smaller calls as the int8 product's, whose borders hold here within some 10%, us in a
+// graph by the shape that is taken and by the nearest other: 1 x 10000 x 2048 6.4 (R4) and
+// 7.0 (R8); 16 x 6000 x 2048 7.0 (R8) and 6.1 (R4); 40000 x 2048 by 1 token 14.0 (R2) and
+// 13.6 (R4); 4 x 60000 x 2944 29.2 (R8) and 26.9 (R4); 12 x 128256 x 2048 45.4 (16 tokens)
+// and 47.6 (R2); 64 x 10000 x 2048 11.4 (32x2) and 13.6 (32); 64 x 12000 x 1024 9.0 (32)
+// and 8.3 (32x2); 64 x 25000 x 4096 27.3 (64x2) and 32.1 (32); 64 x 7000 x 4096 13.4
+// (32x4) and 17.9 (32x2); 30 x 5000 x 2048 7.6 (32 rows, T4) and 8.1 (T8).  Another shape
+// would be faster by more where k is just too short for the groups that share it: 48 x
+// 24000 x 2944 24.8 (32) and 20.4 (64x2), 60 x 2000 x 2048 6.3 (T4) and 5.2 (T8), 64 x 7000
+// x 2048 10.6 (T4) and 9.4 (32x4).
 // Native: 256 rows x 128 tokens (4096 x 10240 x 2560 102, 2048 x 4096 x 2048
 // 21.9, with 256 x 64 23.1; 80 x 262144 x 1152 62.6 and 75.7; of two blocks of k alone,
 // 500 x 14260 x 256, 12.6 and 8.3); 256 x 64 (1000 x 4096 x 2048 14.2, with 128 x 64
@@ -664,7 +675,11 @@ Plan plan_of(int64_t n, int64_t k, int64_t B, bool native) {
 }
 
 // Whether W passes the caches by: its rows are read by one workgroup alone, and
-// too many to be there still at the next call (the int8 product's measurements).
+// too many to be there still at the next call (the int8 product's borders, between
+// calls on other data).  One weight again and again, with nothing between, us past the
+// caches and by them: one token 64 MB 9.8 and 10.9, 256 MB 35.4 and 35.7, 400 MB 55 and
+// 64; 8 tokens 100 MB 17.2 and 16.3, 256 MB 41.6 and 37.2, 400 MB 71 and 77; 64 tokens 256
+// MB 52.4 and 48.3, 400 MB 82.1 and 83.7.
 bool past_caches(const Plan& p, int64_t n, int64_t k, int64_t B) {
   const int64_t from = (int64_t)(p.kind < k16 ? 64 : p.kind < k64 ? 128 : 256) << 20;
   return p.token_tiles(B) == 1 && w8a8_packed_bytes(n, k) > from;

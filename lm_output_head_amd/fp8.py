@@ -277,7 +277,7 @@ class FP8Head(_Steps):
         """[B x n] = q code^T under both scales, in float32 or bfloat16; q and
         q_scale as rmsnorm_fp8 and fp8_quant give them.  Products are exact, sums in
         float32.  native (bfloat16): large calls take the matrix cores' own fp8
-        product, about twice as fast, whose sums of eight products keep 13 binades
+        product (4096 x 10240 x 2560: 103 us for 190), whose sums of eight products keep 13 binades
         below the largest: results may be off by 2^-10 of the sum of their products'
         magnitudes (1.5e-5 of normally distributed codes' results, all of one whose
         products cancel), and by as much with the batch that a token is in."""
