@@ -675,11 +675,12 @@ fh_status fh_fp8_matmul(const fh_fp8* w, const uint8_t* q, int64_t ld_q, const f
  * own fp8 product where n, k and B make it pay (4096 x 10240 x 2560: 103 us for 190;
  * small calls are fh_fp8_matmul's).  It adds up each eight neighbouring products (k
  * 8 i .. 8 i + 7) in fewer bits than float32: of the others it drops what lies below
- * 2^-13 of the largest one's power of two.  So a result may be off by 2^-10 of the
- * sum of its products' magnitudes besides its rounding: 1.5e-5 of the results of
- * normally distributed codes (2-norm), 5e-5 of codes of all sizes, but all of a result
- * whose products cancel.  A token's results may differ by as much with the batch that
- * it is in.
+ * 2^-13 of the largest one's power of two, where a code below 2^-6 but 0 counts as
+ * 2^-6.  So a result may be off by 2^-10 of the sum of its products' magnitudes, such
+ * codes counted so, besides its rounding: 1.5e-5 of the results of normally
+ * distributed codes (2-norm), 5e-5 of codes of all sizes, but all of a result whose
+ * products cancel.  A token's results may differ by as much with the batch that it
+ * is in.
  */
 fh_status fh_fp8_matmul_native(const fh_fp8* w, const uint8_t* q, int64_t ld_q, const float* q_scale,
                                int64_t ld_scale, int64_t B, void* out, int64_t ld_out,

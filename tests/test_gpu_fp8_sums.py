@@ -2,8 +2,9 @@
 
 By default they are the float32 results rounded once: the same sums, so the same
 bits.  What `native` may lose is held to its bound: of eight neighbouring products
-each of the seven others is off by less than 2^-13 of the largest one's power of two,
-the eight by less than 2^-10 of their sum of magnitudes, beside the float32 sums'
+each of the seven others is off by less than 2^-13 of the largest one's power of two, a
+subnormal code's counted as 2^-6's, so the eight by less than 2^-10 of their sum of
+magnitudes (counted so), beside the float32 sums'
 (256 + 2 + k / 128 + 8) 2^-24 (test_gpu_fp8 counts it) and half a step of bfloat16,
 2^-8.  Of normally distributed codes it loses 1.5e-5 of the results (2-norm), 1.2e-5
 s on average for results of deviation s.  A step of bfloat16 is at least 2^-8 |z|,
@@ -153,6 +154,27 @@ def test_native_is_within_its_bound(B, n, k, outliers):
         assert float(other.float().mean()) <= 0.007, float(other.float().mean())
 
 
+def test_native_bound_counts_subnormal_codes_as_the_smallest_normal():
+    """Eights of one product that cancels with the next eight's and seven small ones, from 6
+    binades below it to 17, the tokens' codes from 1 down to the smallest."""
+    from lm_output_head_amd import FP8Head
+    B, n, k = 700, 10000, 592
+    ones = lambda r: torch.ones(r, (k + 127) // 128, device="cuda")  # noqa: E731
+    d = torch.arange(12) + 6  # of channel j: j % 12
+    w = (256 * 2.0 ** -d[torch.arange(n) % 12].float())[:, None].repeat(1, k)
+    w[:, ::16], w[:, 8::16] = 448, -448
+    tokens = torch.tensor([1.0, 2.0 ** -6, 7 * 2.0 ** -9, 2.0 ** -7, 2.0 ** -8, 2.0 ** -9])
+    q = tokens[torch.arange(B) % 6][:, None].repeat(1, k)
+    head = FP8Head(codes=w.to(F8).cuda(), scales=ones((n + 127) // 128))
+    say("fp8 native, subnormal")
+    got = head.matmul(q.to(F8).cuda(), ones(B), dtype=BF, native=True).double().cpu()
+    want = q.double() @ w.double().t().contiguous()
+    size = q.double().clamp_min(2.0 ** -6) @ w.double().abs().t().contiguous()
+    tol = ((256 + 2 + k / 128 + 8) * U + 2.0 ** -10) * size
+    assert torch.all((got - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol))
+    assert torch.equal(head.matmul(q.to(F8).cuda(), ones(B), dtype=BF).double().cpu(), want.to(BF).double())
+
+
 def test_native_of_a_small_call_is_the_default():
     from lm_output_head_amd import FP8Head
     for B, n, k in [(1, 3000, 640), (20, 3000, 640), (32, 46100, 592)]:
@@ -180,3 +202,34 @@ def test_native_rows_strides_workspace_and_what_lies_between():
     assert torch.equal(out[:B, 3:3 + n], want.to(BF))
     out[:B, 3:3 + n] = 7
     assert torch.all(out == 7)
+
+
+@pytest.mark.parametrize("native", [False, True])
+@pytest.mark.parametrize("k", [592, 600])
+def test_captured_bfloat16_products_replay_as_eager_ones(k, native):
+    """On a stream of its own, captured, replayed over new codes with eager work between;
+    at k = 600 the call copies its rows into the workspace first."""
+    from lm_output_head_amd import FP8Head
+    B, n = 333, 5003
+    q, qs, w, ws = operands(B, n, k, 5)
+    head = FP8Head(codes=w, scales=ws)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    say("fp8 bf16 captured", k, native)
+    aside = head.matmul(q, qs, dtype=BF, native=native, stream=s)
+    s.synchronize()
+    assert torch.equal(aside, head.matmul(q, qs, dtype=BF, native=native))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = head.matmul(q, qs, dtype=BF, native=native)
+    for rep in range(4):
+        q2, qs2, _, _ = operands(B, n, k, 6 + rep)
+        q.copy_(q2)
+        qs.copy_(qs2)
+        say("fp8 bf16 replay", rep)
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        want = head.matmul(q, qs, dtype=BF, native=native)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), rep
